@@ -12,6 +12,15 @@ Entry points (same names as the C ABI):
   chunk_fwd(q, k, v, beta, G, chunk, ...)         -> (o, S_out)  (kda_chunk_fwd)
   chunk_fwd_z(q, k, v, beta, z, A, g_min, chunk)  -> (o, S_out)  (kda_chunk_fwd_z)
   decode_step(q, k, v, z, beta, A, S, g_min)      -> o           (kda_decode_step; S updated in place)
+
+Beside the delta rule, on the same layouts:
+  linear_chunk_fwd(q, k, v, g)                    -> (o, S_out)  linear attention with a decay per head
+  linear_chunk_bwd(q, k, v, g, d_o)               -> gradients
+  linear_decode_step(q, k, v, g, S)               -> (o, S)      (S updated in place unless S_out is given)
+  attn_prompt_fwd(q, k, v, cu_seqlens)            -> (o, lse)    causal attention over packed prompts
+  attn_prompt_bwd(q, k, v, cu_seqlens, o, lse, d_o) -> gradients
+  kv_cache_append(k, v, cu_seqlens, ...)          -> None        paged cache in 8 bits, written in place
+  attn_decode_step(q, k_cache, v_cache, ...)      -> (o, lse)    attention of one token over it
 """
 from __future__ import annotations
 
@@ -23,7 +32,10 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["gate", "chunk_fwd", "chunk_fwd_z", "chunk_fwd_workspace_bytes", "decode_step", "chunk_uses_mfma", "lib",
-           "KDAError", "LIB_PATH", "G_MIN"]
+           "linear_chunk_fwd", "linear_chunk_fwd_workspace_bytes", "linear_chunk_bwd",
+           "linear_chunk_bwd_workspace_bytes", "linear_decode_step", "attn_prompt_fwd", "attn_prompt_bwd",
+           "attn_prompt_bwd_workspace_bytes", "kv_cache_append", "attn_decode_step",
+           "attn_decode_step_workspace_bytes", "KDAError", "LIB_PATH", "G_MIN"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 G_MIN = -5.0
@@ -80,6 +92,28 @@ def lib() -> ctypes.CDLL:
     L.kda_chunk_fwd_z_segmented.argtypes = [P, P, P, P, P, I, P, F, P, P, I, P, I, I, I, I, I, I, F, I, P,
                                             ctypes.c_size_t, P]
     L.kda_chunk_fwd_z_segmented.restype = I
+    L.kda_linear_chunk_fwd_workspace_bytes.argtypes = [I] * 6
+    L.kda_linear_chunk_fwd_workspace_bytes.restype = Z
+    L.kda_linear_chunk_fwd.argtypes = [P, P, P, I, P, I, P, P, I, P, I, I, I, I, I, F, P, Z, P]
+    L.kda_linear_chunk_fwd.restype = I
+    L.kda_linear_chunk_bwd_workspace_bytes.argtypes = [I] * 7
+    L.kda_linear_chunk_bwd_workspace_bytes.restype = Z
+    L.kda_linear_chunk_bwd.argtypes = [P, P, P, I, P, I, P, P, P, P, P, P, I, P, P, I, I, I, I, I, F, P, Z, P]
+    L.kda_linear_chunk_bwd.restype = I
+    L.kda_linear_decode_step.argtypes = [P, P, P, I, P, I, P, P, P, I, I, I, I, I, F, P]
+    L.kda_linear_decode_step.restype = I
+    L.kda_attn_prompt_fwd.argtypes = [P, P, P, I, P, P, I, P, I, I, I, I, I, F, P]
+    L.kda_attn_prompt_fwd.restype = I
+    L.kda_attn_prompt_bwd_workspace_bytes.argtypes = [I, I]
+    L.kda_attn_prompt_bwd_workspace_bytes.restype = Z
+    L.kda_attn_prompt_bwd.argtypes = [P, P, P, I, P, P, I, P, P, P, P, P, I, I, I, I, I, I, F, P, Z, P]
+    L.kda_attn_prompt_bwd.restype = I
+    L.kda_kv_cache_append.argtypes = [P, P, I, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
+    L.kda_kv_cache_append.restype = I
+    L.kda_attn_decode_step_workspace_bytes.argtypes = [I] * 6
+    L.kda_attn_decode_step_workspace_bytes.restype = Z
+    L.kda_attn_decode_step.argtypes = [P, I, P, P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, F, P, Z, P]
+    L.kda_attn_decode_step.restype = I
     _lib = L
     return L
 
@@ -415,3 +449,280 @@ def decode_replay(q, k, v, z, beta, A, S_snapshot, accepted, g_min: float = G_MI
                                    H, dk, dv, float(scale), _stream(stream)),
            "kda_decode_replay")
     return o, S_commit
+
+
+# --------------------------------------------------------------------------
+# Linear attention with a decay per head, attention over packed prompts and over
+# a paged cache in 8 bits.
+
+def _run_on_stream(fn):
+    """As ``_on_tensor_device``, and with a ``stream`` argument made current for the call, so that
+    outputs and workspaces allocated here belong to the stream that uses them (the allocator
+    would otherwise hand their memory on while the call still runs there)."""
+    @functools.wraps(fn)
+    def wrapper(*args, stream=None, **kwargs):
+        t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)), None)
+        if t is None:
+            raise KDAError(f"{fn.__name__}: no tensor given")
+        if not t.is_cuda:
+            raise KDAError("libkda runs on the GPU only: tensor is on the CPU")
+        if stream is not None and stream.device != t.device:
+            raise KDAError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.device(t.device):
+            if stream is None:
+                return fn(*args, **kwargs)
+            with torch.cuda.stream(stream):
+                return fn(*args, **kwargs)
+    return wrapper
+
+
+def _dims(what: str, *specs):
+    """specs are (name, tensor, number of dimensions): checked before any shape is unpacked."""
+    for name, t, n in specs:
+        if not isinstance(t, torch.Tensor) or t.dim() != n:
+            raise KDAError(f"{what}: {name} must be a tensor of {n} dimensions")
+
+
+def _need(workspace, need: int, device):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of ``need`` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _dev(workspace)
+    if workspace.device != device:
+        raise KDAError(f"the workspace is on {workspace.device}, the tensors on {device}")
+    return _p(workspace), workspace.numel() * workspace.element_size(), workspace
+
+
+def _out_dtype(dtype, what: str, name: str) -> torch.dtype:
+    dtype = dtype or torch.float32
+    if dtype not in _IO:
+        raise KDAError(f"{what}: {name} is {dtype}, expected {' or '.join(map(str, _IO))}")
+    return dtype
+
+
+def _io_of(t) -> tuple:
+    return (t.dtype,) if t.dtype in _IO else _IO
+
+
+def _linear_shapes(what, q, k, v, g, **more):
+    """(B, T, H, dk, dv, g is per head) after every tensor's check; ``more`` maps a name to
+    (tensor or None, "o" / "k" / "S" layout, dtypes)."""
+    _dims(what, ("q", q, 4), ("v", v, 4))
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    per_head = isinstance(g, torch.Tensor) and g.dim() == 1
+    layouts = {"o": (B, T, H, dv), "k": (B, T, H, dk), "S": (B, H, dk, dv)}
+    io = _io_of(q)
+    _shapes(what, ("q", q, (B, T, H, dk), _IO), ("k", k, (B, T, H, dk), io), ("v", v, (B, T, H, dv), io),
+            ("g", g, (H,) if per_head else (B, T, H), _F32), *[(n, t, layouts[at], dt) for n, (t, at, dt) in more.items()])
+    _dev(q, k, v, g, *[t for t, _, _ in more.values()])
+    return B, T, H, dk, dv, per_head
+
+
+def linear_chunk_fwd_workspace_bytes(B: int, T: int, H: int, dk: int, dv: int, dtype: torch.dtype) -> int:
+    """Device bytes ``linear_chunk_fwd`` needs as workspace (0: none) for inputs of ``dtype``."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_linear_chunk_fwd_workspace_bytes(int(B), int(T), int(H), int(dk), int(dv), code))
+
+
+@_run_on_stream
+def linear_chunk_fwd(q, k, v, g, S_in=None, o=None, S_out=None, o_dtype=None, scale: float = 1.0,
+                     want_state: bool = True, workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay per head: S_t = e^g S_{t-1} + k v^T, o_t = scale S_t^T q.
+    q, k [B,T,H,dk], v [B,T,H,dv]; g fp32 log-decays (at most 0), [B,T,H] or [H].
+    Returns (o [B,T,H,dv], S_out [B,H,dk,dv] or None).  ``stream``: as everywhere."""
+    what = "kda_linear_chunk_fwd"
+    _dims(what, ("q", q, 4), ("v", v, 4))
+    o, S_out = _outs(q, v, o, S_out, _out_dtype(o_dtype, what, "o_dtype"), want_state)
+    B, T, H, dk, dv, ph = _linear_shapes(what, q, k, v, g, S_in=(S_in, "S", _F32), o=(o, "o", _IO),
+                                         S_out=(S_out, "S", _F32))
+    wp, wb, _keep = _need(workspace, linear_chunk_fwd_workspace_bytes(B, T, H, dk, dv, q.dtype), q.device)
+    _check(lib().kda_linear_chunk_fwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(g), int(ph), _p(S_in), _p(o),
+                                      _dtype_code(o), _p(S_out), B, T, H, dk, dv, float(scale), wp, wb,
+                                      _stream(None)), what)
+    return o, S_out
+
+
+def linear_chunk_bwd_workspace_bytes(B: int, T: int, H: int, dk: int, dv: int, dtype: torch.dtype,
+                                     g_per_head: bool = False) -> int:
+    """Device bytes ``linear_chunk_bwd`` needs as workspace for inputs of ``dtype``."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_linear_chunk_bwd_workspace_bytes(int(B), int(T), int(H), int(dk), int(dv), code,
+                                                          int(bool(g_per_head))))
+
+
+@_run_on_stream
+def linear_chunk_bwd(q, k, v, g, d_o, dS_out=None, S_in=None, scale: float = 1.0, want_dS_in: bool = True,
+                     grad_dtype=None, workspace=None) -> dict:
+    """Backward of ``linear_chunk_fwd``, given dL/do (``d_o``, the inputs' dtype) and optionally
+    dL/dS_out.  Returns a dict with dq, dk, dv (``grad_dtype``, default fp32), dg (fp32, g's shape)
+    and dS_in (fp32, None unless ``want_dS_in``)."""
+    what = "kda_linear_chunk_bwd"
+    grad_dtype = _out_dtype(grad_dtype, what, "grad_dtype")
+    B, T, H, dk, dv, ph = _linear_shapes(what, q, k, v, g, d_o=(d_o, "o", _io_of(q)), dS_out=(dS_out, "S", _F32),
+                                         S_in=(S_in, "S", _F32))
+    new = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=q.device)  # noqa: E731
+    out = {"dq": new(grad_dtype, B, T, H, dk), "dk": new(grad_dtype, B, T, H, dk), "dv": new(grad_dtype, B, T, H, dv),
+           "dg": torch.empty_like(g), "dS_in": new(torch.float32, B, H, dk, dv) if want_dS_in else None}
+    wp, wb, _keep = _need(workspace, linear_chunk_bwd_workspace_bytes(B, T, H, dk, dv, q.dtype, ph), q.device)
+    _check(lib().kda_linear_chunk_bwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(g), int(ph), _p(S_in), _p(d_o),
+                                      _p(dS_out), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _dtype_code(out["dq"]),
+                                      _p(out["dg"]), _p(out["dS_in"]), B, T, H, dk, dv, float(scale), wp, wb,
+                                      _stream(None)), what)
+    return out
+
+
+@_run_on_stream
+def linear_decode_step(q, k, v, g, S, o=None, o_dtype=None, scale: float = 1.0,
+                       S_out=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token per sequence of linear attention with a decay per head: q, k [N,H,dk], v [N,H,dv],
+    g [N,H] or [H] fp32.  S [N,H,dk,dv] fp32 is updated in place, or kept when another
+    ``S_out`` is given.  Returns (o [N,H,dv], the new state)."""
+    what = "kda_linear_decode_step"
+    _dims(what, ("q", q, 3), ("v", v, 3), ("S", S, 4))
+    N, H, dk = q.shape
+    dv = v.shape[-1]
+    if o is None:
+        o = torch.empty((N, H, dv), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
+    if S_out is None:
+        S_out = S
+    ph = isinstance(g, torch.Tensor) and g.dim() == 1
+    io = _io_of(q)
+    _shapes(what, ("q", q, (N, H, dk), _IO), ("k", k, (N, H, dk), io), ("v", v, (N, H, dv), io),
+            ("g", g, (H,) if ph else (N, H), _F32), ("S", S, (N, H, dk, dv), _F32), ("S_out", S_out, (N, H, dk, dv), _F32),
+            ("o", o, (N, H, dv), _IO))
+    _dev(q, k, v, g, S, S_out, o)
+    _check(lib().kda_linear_decode_step(_p(q), _p(k), _p(v), _dtype_code(q), _p(g), int(ph), _p(S), _p(S_out), _p(o),
+                                        _dtype_code(o), N, H, dk, dv, float(scale), _stream(None)), what)
+    return o, S_out
+
+
+_I32 = (torch.int32,)
+
+
+def _prompt_shapes(what, q, k, v, cu_seqlens, *more):
+    _dims(what, ("q", q, 3), ("k", k, 3), ("cu_seqlens", cu_seqlens, 1))
+    n, Hq, d = q.shape
+    Hkv = k.shape[1]
+    if cu_seqlens.shape[0] < 1:
+        raise KDAError(f"{what}: cu_seqlens has no entry (n_seqs + 1 are needed)")
+    io = _io_of(q)
+    at = {"q": (n, Hq, d), "k": (n, Hkv, d), "l": (n, Hq)}
+    _shapes(what, ("q", q, (n, Hq, d), _IO), ("k", k, (n, Hkv, d), io), ("v", v, (n, Hkv, d), io),
+            ("cu_seqlens", cu_seqlens, tuple(cu_seqlens.shape), _I32), *[(m, t, at[s], dt) for m, t, s, dt in more])
+    _dev(q, k, v, cu_seqlens, *[t for _, t, _, _ in more])
+    return n, cu_seqlens.shape[0] - 1, Hq, Hkv, d
+
+
+def _softmax_scale(scale, d: int) -> float:
+    return float(d) ** -0.5 if scale is None else float(scale)
+
+
+@_run_on_stream
+def attn_prompt_fwd(q, k, v, cu_seqlens, scale: Optional[float] = None, o=None, lse=None, o_dtype=None,
+                    want_lse: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal attention over packed prompts: q [n,Hq,d], k, v [n,Hkv,d], sequence s in rows
+    cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32, on the device).  ``scale`` defaults to 1 / sqrt(d).
+    Returns (o [n,Hq,d], lse [n,Hq] fp32 or None).  Rows behind the last sequence are not written:
+    given ``o`` and ``lse`` keep what they hold there, new ones are zero there."""
+    what = "kda_attn_prompt_fwd"
+    _dims(what, ("q", q, 3))
+    n, Hq, d = q.shape
+    if o is None:
+        o = torch.zeros((n, Hq, d), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
+    if lse is None and want_lse:
+        lse = torch.zeros((n, Hq), dtype=torch.float32, device=q.device)
+    n, ns, Hq, Hkv, d = _prompt_shapes(what, q, k, v, cu_seqlens, ("o", o, "q", _IO), ("lse", lse, "l", _F32))
+    _check(lib().kda_attn_prompt_fwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(cu_seqlens), _p(o), _dtype_code(o), _p(lse),
+                                     n, ns, Hq, Hkv, d, _softmax_scale(scale, d), _stream(None)), what)
+    return o, lse
+
+
+def attn_prompt_bwd_workspace_bytes(n: int, Hq: int) -> int:
+    """Device bytes ``attn_prompt_bwd`` needs as workspace for n rows of Hq query heads."""
+    return int(lib().kda_attn_prompt_bwd_workspace_bytes(int(n), int(Hq)))
+
+
+@_run_on_stream
+def attn_prompt_bwd(q, k, v, cu_seqlens, o, lse, d_o, scale: Optional[float] = None, grad_dtype=None,
+                    workspace=None) -> dict:
+    """Backward of ``attn_prompt_fwd``, from its o and lse and dL/do (``d_o``, the inputs' dtype).
+    Returns a dict with dq [n,Hq,d], dk and dv [n,Hkv,d] (``grad_dtype``, default fp32), zero
+    in rows behind the last sequence."""
+    what = "kda_attn_prompt_bwd"
+    grad_dtype = _out_dtype(grad_dtype, what, "grad_dtype")
+    n, ns, Hq, Hkv, d = _prompt_shapes(what, q, k, v, cu_seqlens, ("o", o, "q", _IO), ("lse", lse, "l", _F32),
+                                       ("d_o", d_o, "q", _io_of(q)))
+    out = {"dq": torch.zeros((n, Hq, d), dtype=grad_dtype, device=q.device),
+           "dk": torch.zeros((n, Hkv, d), dtype=grad_dtype, device=q.device),
+           "dv": torch.zeros((n, Hkv, d), dtype=grad_dtype, device=q.device)}
+    wp, wb, _keep = _need(workspace, attn_prompt_bwd_workspace_bytes(n, Hq), q.device)
+    _check(lib().kda_attn_prompt_bwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(cu_seqlens), _p(o), _dtype_code(o), _p(lse),
+                                     _p(d_o), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _dtype_code(out["dq"]), n, ns,
+                                     Hq, Hkv, d, _softmax_scale(scale, d), wp, wb, _stream(None)), what)
+    return out
+
+
+_F8 = (torch.float8_e4m3fn,)
+
+
+def _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len, *more):
+    _dims(what, ("k_cache", k_cache, 4), ("block_table", block_table, 2))
+    pages, _, page, _ = k_cache.shape
+    N, max_pages = block_table.shape
+    _shapes(what, *more, ("k_cache", k_cache, (pages, Hkv, page, d), _F8), ("v_cache", v_cache, (pages, Hkv, d, page), _F8),
+            ("k_scale", k_scale, (pages, Hkv), _F32), ("v_scale", v_scale, (pages, Hkv), _F32),
+            ("block_table", block_table, (N, max_pages), _I32), ("context_len", context_len, (N,), _I32))
+    _dev(k_cache, v_cache, k_scale, v_scale, block_table, context_len, *[m[1] for m in more])
+    return N, page, pages, max_pages
+
+
+@_run_on_stream
+def kv_cache_append(k, v, cu_seqlens, context_len, block_table, k_cache, v_cache, k_scale, v_scale) -> None:
+    """Quantise new tokens into a paged cache, in place: k, v [n,Hkv,d], rows
+    cu_seqlens[i] .. cu_seqlens[i+1] - 1 behind the context_len[i] tokens that sequence i holds.
+    k_cache [pages,Hkv,page,d] and v_cache [pages,Hkv,d,page] float8_e4m3fn, k_scale and v_scale
+    [pages,Hkv] fp32, block_table [N,max_pages] int32.  context_len is not changed."""
+    what = "kda_kv_cache_append"
+    _dims(what, ("k", k, 3), ("cu_seqlens", cu_seqlens, 1), ("context_len", context_len, 1))
+    n, Hkv, d = k.shape
+    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
+                                       ("k", k, (n, Hkv, d), _IO), ("v", v, (n, Hkv, d), _io_of(k)),
+                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32))
+    _check(lib().kda_kv_cache_append(_p(k), _p(v), _dtype_code(k), _p(cu_seqlens), _p(context_len), _p(block_table),
+                                     _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), n, N, Hkv, d, page, pages, mp,
+                                     _stream(None)), what)
+
+
+def attn_decode_step_workspace_bytes(N: int, Hq: int, Hkv: int, d: int, page: int, max_pages: int) -> int:
+    """Device bytes ``attn_decode_step`` needs as workspace (0: none)."""
+    return int(lib().kda_attn_decode_step_workspace_bytes(int(N), int(Hq), int(Hkv), int(d), int(page), int(max_pages)))
+
+
+@_run_on_stream
+def attn_decode_step(q, k_cache, v_cache, k_scale, v_scale, block_table, context_len, scale: Optional[float] = None,
+                     o=None, lse=None, o_dtype=None, want_lse: bool = False,
+                     workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of one token per sequence over a paged cache in 8 bits (``kv_cache_append``):
+    q [N,Hq,d].  ``scale`` defaults to 1 / sqrt(d).  Returns (o [N,Hq,d], lse [N,Hq] fp32 or
+    None); a sequence with no tokens gets o = 0, lse = -inf."""
+    what = "kda_attn_decode_step"
+    _dims(what, ("q", q, 3), ("k_cache", k_cache, 4))
+    N, Hq, d = q.shape
+    Hkv = k_cache.shape[1]
+    if o is None:
+        o = torch.empty((N, Hq, d), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+    Nt, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
+                                        ("q", q, (N, Hq, d), _IO), ("o", o, (N, Hq, d), _IO),
+                                        ("lse", lse, (N, Hq), _F32))
+    if Nt != N:
+        raise KDAError(f"{what}: block_table has {Nt} rows, q {N}")
+    wp, wb, _keep = _need(workspace, attn_decode_step_workspace_bytes(N, Hq, Hkv, d, page, mp), q.device)
+    _check(lib().kda_attn_decode_step(_p(q), _dtype_code(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                      _p(block_table), _p(context_len), _p(o), _dtype_code(o), _p(lse), N, Hq, Hkv, d,
+                                      page, pages, mp, _softmax_scale(scale, d), wp, wb, _stream(None)), what)
+    return o, lse

@@ -1,0 +1,216 @@
+// kda_mma.hpp -- matrix-core operands shared by the linear-attention, prompt-attention
+// and cache-attention kernels, for bf16 and fp32 elements alike.
+//
+// A fragment is the eight k-elements one lane feeds a product with: lane l holds row
+// (A) or column (B) l % 32 and k = 8 (l / 32) .. + 7 of a 32x32x16 product, or l % 16
+// and k = 8 (l / 16) .. + 7 of a 16x16x32 product.  With bf16 that is one
+// v_mfma_f32_32x32x16_bf16 (16x16x32); with fp32 the same fragment feeds eight
+// v_mfma_f32_32x32x2_f32 (16x16x4), product j taking element j of every lane, so both
+// element types share one data layout.  A product's k order does not matter as long as A
+// and B agree on it.  Results (fp32): lane l holds column l % 32, rows
+// 8 (i / 4) + 4 (l / 32) + i % 4 in register i (32x32), or column l % 16, rows
+// 4 (l / 16) + i (16x16).  Hence a result's registers 8 s .. 8 s + 7 are again a fragment:
+// k-step s of a product over its rows, element j standing for row
+// 16 s + 4 (l / 32) + j (j < 4) or 16 s + 8 + 4 (l / 32) + j - 4 (`perm` below).
+#pragma once
+
+#include "kda_common.hpp"
+
+namespace kda {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+
+// Row of a 32x32 result held by register i in lane half h.
+__device__ __forceinline__ constexpr int crow(int i, int h) { return 8 * (i / 4) + 4 * h + i % 4; }
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+template <typename T> struct Op;
+
+template <> struct Op<bf16_t> {
+  typedef bf16x8 frag;
+  __device__ __forceinline__ static frag zero() { return __builtin_bit_cast(frag, u32x4{0, 0, 0, 0}); }
+  __device__ __forceinline__ static frag load(const bf16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
+  __device__ __forceinline__ static frag join(bf16x4 a, bf16x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  // round to nearest even (v_cvt_pk_bf16_f32)
+  __device__ __forceinline__ static frag pack(const f32x8 f) { return __builtin_convertvector(f, bf16x8); }
+  __device__ __forceinline__ static f32x8 unpack(const frag a) { return __builtin_convertvector(a, f32x8); }
+  __device__ __forceinline__ static frag neg(const frag a) { return -a; }
+  __device__ __forceinline__ static f32x16 mma32(frag a, frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  __device__ __forceinline__ static f32x4 mma16(frag a, frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+
+template <> struct Op<float> {
+  typedef f32x8 frag;
+  __device__ __forceinline__ static frag zero() { return frag{0, 0, 0, 0, 0, 0, 0, 0}; }
+  __device__ __forceinline__ static frag load(const float* p) {
+    return join(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+  }
+  __device__ __forceinline__ static frag join(f32x4 a, f32x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  __device__ __forceinline__ static frag pack(const f32x8 f) { return f; }
+  __device__ __forceinline__ static f32x8 unpack(const frag a) { return a; }
+  __device__ __forceinline__ static frag neg(const frag a) { return -a; }
+  __device__ __forceinline__ static f32x16 mma32(frag a, frag b, f32x16 c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+  }
+  __device__ __forceinline__ static f32x4 mma16(frag a, frag b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+  }
+};
+
+// Registers 8 s .. 8 s + 7 of a result as a fragment.
+template <typename T>
+__device__ __forceinline__ typename Op<T>::frag frag_of(const f32x16& c, int s) {
+  f32x8 f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = c[8 * s + j];
+  return Op<T>::pack(f);
+}
+
+// A tile of rows of COLS elements in LDS.  Each row's 16-byte chunks are permuted by the
+// row's number, so that reads of one chunk from 8 or 16 consecutive rows, and transposing
+// reads of 4 rows by 16 columns, spread over the banks.
+template <typename T, int COLS>
+struct Tile {
+  static constexpr int EPC = 16 / int(sizeof(T));  // elements of a chunk
+  static constexpr int CH = COLS / EPC;            // chunks of a row
+  static_assert(COLS % EPC == 0 && (CH & (CH - 1)) == 0 && CH >= 4, "rows of a power of two of chunks");
+  __device__ __forceinline__ static int swz(int row) {
+    if constexpr (CH >= 16) return ((row << 1) & 14) | ((row >> 3) & 1);
+    else return row & (CH - 1);
+  }
+  // element offset of (row, col); `col` a multiple of 4 keeps 4 elements together
+  __device__ __forceinline__ static int off(int row, int col) {
+    return row * COLS + (((col / EPC) ^ swz(row)) * EPC) + col % EPC;
+  }
+  // columns col .. col + 7 of a row (col a multiple of 8)
+  __device__ __forceinline__ static typename Op<T>::frag row8(const T* t, int row, int col) {
+    if constexpr (sizeof(T) == 2) {
+      return Op<T>::load(t + off(row, col));
+    } else {
+      return Op<T>::join(*reinterpret_cast<const f32x4*>(t + off(row, col)),
+                         *reinterpret_cast<const f32x4*>(t + off(row, col + 4)));
+    }
+  }
+  // columns a .. a + 3 and b .. b + 3 of a row
+  __device__ __forceinline__ static typename Op<T>::frag row44(const T* t, int row, int a, int b) {
+    if constexpr (sizeof(T) == 2) {
+      return Op<T>::join(*reinterpret_cast<const bf16x4*>(t + off(row, a)),
+                         *reinterpret_cast<const bf16x4*>(t + off(row, b)));
+    } else {
+      return Op<T>::join(*reinterpret_cast<const f32x4*>(t + off(row, a)),
+                         *reinterpret_cast<const f32x4*>(t + off(row, b)));
+    }
+  }
+  // rows a .. a + 3 and b .. b + 3 of column c0 + lane % 32 (c0 a multiple of 32).  a and b may
+  // differ between the two halves of the wavefront.  With bf16 by two transposing reads
+  // (ds_read_b64_tr_b16): 16 lanes fetch 4 rows of 16 columns, 4 columns each, and lane i of them
+  // receives column i.
+  __device__ __forceinline__ static typename Op<T>::frag col44(const T* t, int a, int b, int c0, int lane) {
+    if constexpr (sizeof(T) == 2) {
+      typedef s16x4 __attribute__((address_space(3)))* lds_ptr;
+      const int r = (lane & 15) >> 2, c = c0 + (lane & 16) + 4 * (lane & 3);
+      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + off(a + r, c)));
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + off(b + r, c)));
+      return Op<T>::join(__builtin_bit_cast(bf16x4, x), __builtin_bit_cast(bf16x4, y));
+    } else {
+      f32x8 f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = t[off(j < 4 ? a + j : b + j - 4, c0 + (lane & 31))];
+      return f;
+    }
+  }
+  // four consecutive columns of a row as fp32
+  __device__ __forceinline__ static f32x4 get4(const T* t, int row, int col) {
+    if constexpr (sizeof(T) == 2)
+      return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(t + off(row, col)), f32x4);
+    else
+      return *reinterpret_cast<const f32x4*>(t + off(row, col));
+  }
+  __device__ __forceinline__ static void put4(T* t, int row, int col, f32x4 x) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<bf16x4*>(t + off(row, col)) = __builtin_convertvector(x, bf16x4);
+    else
+      *reinterpret_cast<f32x4*>(t + off(row, col)) = x;
+  }
+};
+
+// Four consecutive elements to global memory, rounded to the output type.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f32x4 x) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(x, bf16x4);
+  else
+    *reinterpret_cast<f32x4*>(p) = x;
+}
+
+// The sum and maximum of a value and the other half-wavefront's (lane ^ 32).
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Rows of a global matrix staged through registers: `NT` threads hold a tile of ROWS rows of
+// PCOLS elements, of which the first COLS come from memory (the rest, and rows at or past
+// `valid`, are zero).  load() issues the reads, store() puts them into a Tile.
+template <typename T, int ROWS, int COLS, int PCOLS, int NT>
+struct Stage {
+  typedef Tile<T, PCOLS> L;
+  static constexpr int N = (ROWS * L::CH + NT - 1) / NT;
+  u32x4 r[N];
+  __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t valid, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = tid + i * NT, row = e / L::CH, ch = e % L::CH;
+      r[i] = u32x4{0, 0, 0, 0};
+      if (row < valid && row < ROWS && ch * L::EPC < COLS)
+        r[i] = *reinterpret_cast<const u32x4*>(base + row * stride + ch * L::EPC);
+    }
+  }
+  __device__ __forceinline__ void store(T* t, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = tid + i * NT, row = e / L::CH, ch = e % L::CH;
+      if (row < ROWS) *reinterpret_cast<u32x4*>(t + L::off(row, ch * L::EPC)) = r[i];
+    }
+  }
+};
+
+// Dispatch of workgroups to consecutive work items per XCD: the hardware deals workgroups to
+// the eight XCDs in turn; the returned index gives each XCD one contiguous run of items, so that
+// neighbours (the tiles of one head) share an L2.
+__device__ __forceinline__ int xcd_order(int id, int n) {
+  const int x = id & 7, per = n >> 3, rem = n & 7;
+  return x * per + (x < rem ? x : rem) + (id >> 3);
+}
+
+}  // namespace kda

@@ -1,0 +1,313 @@
+// kda_prompt_bwd.hip -- gradients of the packed prompts' causal attention.
+//
+// With P_ij = exp(scale q_i . k_j - lse_i), dP_ij = do_i . v_j, D_i = do_i . o_i,
+// dS_ij = P_ij (dP_ij - D_i):
+//   dv_j = sum_i P_ij do_i,   dk_j = scale sum_i dS_ij q_i,   dq_i = scale sum_j dS_ij k_j,
+// the sums of dk and dv running over the query heads of the group as well.
+//
+// Two kernels, so that every sum has one owner and a fixed order (no atomics: the same bits every
+// time), at the price of forming S and dP twice (seven products instead of five):
+//   - dk and dv: a workgroup owns 128 keys of one key head and walks the rows that see them, 64
+//     at a time, for every query head of the group; a wavefront owns 32 keys, whose K and V stay
+//     in registers;
+//   - dq: a workgroup owns 128 rows of one query head and walks the keys as the forward does.
+// Both form S and dP with the owned index in the lanes (columns) and the other in the registers
+// (rows), so that P and dS are in place as operands of the products that sum over the rows, and
+// write their sums transposed.  D comes from a small kernel before.  The sums are fp32; with bf16
+// elements P and dS are rounded to bf16 for the products that follow, 2^-9 relative each, as the
+// gradients may be.
+#include "kda_prompt.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int BM = 128;  // owned rows or keys
+constexpr int BN = 64;   // walked keys
+constexpr int BR = 64;   // walked rows
+
+// D [n, Hq]: eight lanes a row of a head.
+template <typename TO, typename TD>
+__global__ __launch_bounds__(256) void prompt_dot_kernel(const TO* o, const TD* d_o, float* D, int64_t rows, int d) {
+  const int64_t r = int64_t(blockIdx.x) * 32 + threadIdx.x / 8;
+  const int part = threadIdx.x % 8;
+  float s = 0.f;
+  if (r < rows)
+    for (int c = part * 4; c < d; c += 32)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s += io<TO>::load(o, r * d + c + j) * io<TD>::load(d_o, r * d + c + j);
+#pragma unroll
+  for (int x = 1; x < 8; x <<= 1) s += __shfl_xor(s, x);
+  if (r < rows && part == 0) D[r] = s;
+}
+
+template <typename T, int D>
+constexpr size_t kv_lds() { return size_t(2) * 2 * BR * D * sizeof(T) + 2 * 2 * BR * sizeof(float); }
+
+template <typename T, typename TG, int D>
+__global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs a, int ntile) {
+  using O = Op<T>;
+  using F = typename O::frag;
+  using TD = Tile<T, D>;
+  constexpr int NK = D / 16, ND = D / 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* const buf = reinterpret_cast<T*>(smem);                             // [2][Q tile, dO tile]
+  float* const stat = reinterpret_cast<float*>(buf + 2 * 2 * BR * D);    // [2][lse log2 e, D]
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int kvh = id / ntile, tile = id % ntile;  // keys with the most rows first
+  const int c0 = tile * BM;
+  const int used = rows_used(a.cu, a.nseq, a.n);
+  if (c0 >= used) return;
+  const int G = a.Hq / a.Hkv;
+  const int64_t qst = int64_t(a.Hq) * D, kst = int64_t(a.Hkv) * D;
+
+  const int clast = c0 + BM - 1 < used ? c0 + BM - 1 : used - 1;
+  const int hi = span_of(a.cu, a.nseq, a.n, clast).end < used ? span_of(a.cu, a.nseq, a.n, clast).end : used;
+  const int w0 = c0 + 32 * wave, kj = w0 + l32;
+  const int kr = kj < used ? kj : used - 1;
+  const int end = span_of(a.cu, a.nseq, a.n, kr).end;
+  const int emin = __shfl(end, 0), emax = __shfl(end, 31);
+  const float c = a.scale * kLog2e;
+
+  F kf[NK], vf[NK];
+  {
+    const T* kp = static_cast<const T*>(a.k) + int64_t(kr) * kst + int64_t(kvh) * D;
+    const T* vp = static_cast<const T*>(a.v) + int64_t(kr) * kst + int64_t(kvh) * D;
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      kf[kk] = O::load(kp + 16 * kk + 8 * h2);
+      vf[kk] = O::load(vp + 16 * kk + 8 * h2);
+    }
+  }
+  f32x16 dk[ND], dv[ND];
+#pragma unroll
+  for (int i = 0; i < ND; ++i) dk[i] = dv[i] = zero16();
+
+  const int nt = (hi - c0 + BR - 1) / BR, steps = nt * G;
+  auto fetch = [&](int t) {
+    const int head = kvh * G + t / nt, i0 = c0 + (t % nt) * BR;
+    T* qb = buf + (t & 1) * 2 * BR * D;
+    copy_rows<T, BR, D, 4>(qb, static_cast<const T*>(a.q) + int64_t(head) * D, qst, i0, hi, wave, lane);
+    copy_rows<T, BR, D, 4>(qb + BR * D, static_cast<const T*>(a.d_o) + int64_t(head) * D, qst, i0, hi, wave, lane);
+    if (tid < BR) {
+      const int r = i0 + tid < hi ? i0 + tid : hi - 1;
+      stat[(t & 1) * 2 * BR + tid] = a.lse[int64_t(r) * a.Hq + head] * kLog2e;
+      stat[(t & 1) * 2 * BR + BR + tid] = a.D[int64_t(r) * a.Hq + head];
+    }
+  };
+  fetch(0);
+  for (int t = 0; t < steps; ++t) {
+    copies_done();
+    if (t + 1 < steps) fetch(t + 1);
+    const T* Qs = buf + (t & 1) * 2 * BR * D;
+    const T* Os = Qs + BR * D;
+    const float* ls = stat + (t & 1) * 2 * BR;
+    const float* Ds = ls + BR;
+    const int i0 = c0 + (t % nt) * BR;
+#pragma unroll 1
+    for (int sub = 0; sub < BR / 32; ++sub) {
+      const int s0 = i0 + 32 * sub;
+      // some row at or past the wavefront's first key, before its last key's end
+      if (w0 >= used || s0 + 31 < w0 || s0 >= emax || s0 >= hi) continue;
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        s = O::mma32(TD::row8(Qs, 32 * sub + l32, 16 * kk + 8 * h2), kf[kk], s);
+        dp = O::mma32(TD::row8(Os, 32 * sub + l32, 16 * kk + 8 * h2), vf[kk], dp);
+      }
+      const bool whole = s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi;
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const int rr = 32 * sub + 8 * r4 + 4 * h2;
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + rr), D4 = *reinterpret_cast<const f32x4*>(Ds + rr);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + rr + j, e = 4 * r4 + j;
+          const bool in = whole || (i >= kj && i < end && i < hi);
+          const float p = in ? fast_exp2(s[e] * c - l4[j]) : 0.f;
+          s[e] = p;
+          dp[e] = in ? p * (dp[e] - D4[j]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const F pf = frag_of<T>(s, ks), df = frag_of<T>(dp, ks);
+        const int rr = 32 * sub + 16 * ks + 4 * h2;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+          dv[i] = O::mma32(TD::col44(Os, rr, rr + 8, 32 * i, lane), pf, dv[i]);
+          dk[i] = O::mma32(TD::col44(Qs, rr, rr + 8, 32 * i, lane), df, dk[i]);
+        }
+      }
+    }
+  }
+  if (kj < used) {
+    TG* kp = static_cast<TG*>(a.dk) + int64_t(kj) * kst + int64_t(kvh) * D;
+    TG* vp = static_cast<TG*>(a.dv) + int64_t(kj) * kst + int64_t(kvh) * D;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        f32x4 x, y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = dk[i][4 * r4 + j] * a.scale;
+          y[j] = dv[i][4 * r4 + j];
+        }
+        store4(kp + 32 * i + 8 * r4 + 4 * h2, x);
+        store4(vp + 32 * i + 8 * r4 + 4 * h2, y);
+      }
+  }
+}
+
+template <typename T, int D>
+constexpr size_t q_lds() { return size_t(sizeof(T) == 2 ? 2 : 1) * 2 * BN * D * sizeof(T); }
+
+template <typename T, typename TG, int D>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(const PromptBwdArgs a, int ntile) {
+  using O = Op<T>;
+  using F = typename O::frag;
+  using TD = Tile<T, D>;
+  constexpr int NK = D / 16, ND = D / 32;
+  constexpr bool DB = sizeof(T) == 2;  // two buffers
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* const buf = reinterpret_cast<T*>(smem);  // [1 or 2][K tile, V tile]
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int head = id / ntile, tile = ntile - 1 - id % ntile;
+  const int r0 = tile * BM;
+  const int used = rows_used(a.cu, a.nseq, a.n);
+  if (r0 >= used) return;
+  const int kvh = head / (a.Hq / a.Hkv);
+  const int64_t qst = int64_t(a.Hq) * D, kst = int64_t(a.Hkv) * D;
+  const T* kp = static_cast<const T*>(a.k) + int64_t(kvh) * D;
+  const T* vp = static_cast<const T*>(a.v) + int64_t(kvh) * D;
+
+  const int lo = span_of(a.cu, a.nseq, a.n, r0).start;
+  const int hi = r0 + BM < used ? r0 + BM : used;
+  const int w0 = r0 + 32 * wave, qi = w0 + l32;
+  const int wlast = w0 + 31 < used ? w0 + 31 : used - 1;
+  const int qr = qi < used ? qi : used - 1;
+  const int start = span_of(a.cu, a.nseq, a.n, qr).start;
+  const int smin = __shfl(start, 0), smax = __shfl(start, 31);
+  const float c = a.scale * kLog2e;
+  const float ls = a.lse[int64_t(qr) * a.Hq + head] * kLog2e, Di = a.D[int64_t(qr) * a.Hq + head];
+
+  F qf[NK], of[NK];
+  {
+    const T* qp = static_cast<const T*>(a.q) + int64_t(qr) * qst + int64_t(head) * D;
+    const T* op = static_cast<const T*>(a.d_o) + int64_t(qr) * qst + int64_t(head) * D;
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      qf[kk] = O::load(qp + 16 * kk + 8 * h2);
+      of[kk] = O::load(op + 16 * kk + 8 * h2);
+    }
+  }
+  f32x16 dq[ND];
+#pragma unroll
+  for (int i = 0; i < ND; ++i) dq[i] = zero16();
+
+  const int nt = (hi - lo + BN - 1) / BN;
+  auto fetch = [&](int t) {
+    T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
+    copy_rows<T, BN, D, 4>(kb, kp, kst, lo + t * BN, hi, wave, lane);
+    copy_rows<T, BN, D, 4>(kb + BN * D, vp, kst, lo + t * BN, hi, wave, lane);
+  };
+  fetch(0);
+  for (int t = 0; t < nt; ++t) {
+    copies_done();
+    if (DB && t + 1 < nt) fetch(t + 1);
+    const T* Ks = buf + (DB ? (t & 1) * 2 * BN * D : 0);
+    const T* Vs = Ks + BN * D;
+    const int k0 = lo + t * BN;
+#pragma unroll 1
+    for (int j = 0; j < BN / 32; ++j) {
+      const int s0 = k0 + 32 * j;
+      if (wlast < w0 || s0 > wlast || s0 + 32 <= smin) continue;
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        s = O::mma32(TD::row8(Ks, 32 * j + l32, 16 * kk + 8 * h2), qf[kk], s);
+        dp = O::mma32(TD::row8(Vs, 32 * j + l32, 16 * kk + 8 * h2), of[kk], dp);
+      }
+      const bool whole = s0 + 31 <= w0 && s0 >= smax;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = s0 + crow(i, h2);
+        const bool in = whole || (key <= qi && key >= start);
+        const float p = in ? fast_exp2(s[i] * c - ls) : 0.f;
+        dp[i] = in ? p * (dp[i] - Di) : 0.f;
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const F df = frag_of<T>(dp, ks);
+        const int kr = 32 * j + 16 * ks + 4 * h2;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44(Ks, kr, kr + 8, 32 * i, lane), df, dq[i]);
+      }
+    }
+    if (!DB) {
+      __syncthreads();
+      if (t + 1 < nt) fetch(t + 1);
+    }
+  }
+  if (qi < used) {
+    TG* p = static_cast<TG*>(a.dq) + int64_t(qi) * qst + int64_t(head) * D;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        f32x4 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = dq[i][4 * r4 + j] * a.scale;
+        store4(p + 32 * i + 8 * r4 + 4 * h2, x);
+      }
+  }
+}
+
+template <typename TO>
+hipError_t launch_dot_o(const PromptBwdArgs& a, hipStream_t st) {
+  const int64_t rows = int64_t(a.n) * a.Hq;
+  const dim3 grid(uint32_t((rows + 31) / 32));
+  if (a.in_bf16)
+    prompt_dot_kernel<<<grid, 256, 0, st>>>(static_cast<const TO*>(a.o), static_cast<const bf16_t*>(a.d_o), a.D, rows, a.d);
+  else
+    prompt_dot_kernel<<<grid, 256, 0, st>>>(static_cast<const TO*>(a.o), static_cast<const float*>(a.d_o), a.D, rows, a.d);
+  return hipGetLastError();
+}
+
+template <typename T, typename TG, int D>
+hipError_t launch(const PromptBwdArgs& a, hipStream_t st) {
+  auto kkv = prompt_dkv_kernel<T, TG, D>;
+  auto kq = prompt_dq_kernel<T, TG, D>;
+  constexpr size_t l1 = kv_lds<T, D>(), l2 = q_lds<T, D>();
+  static_assert(l1 <= 160 * 1024 && l2 <= 160 * 1024, "LDS of a compute unit");
+  static std::atomic<uint64_t> done1{0}, done2{0};
+  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kkv), int(l1), done1);
+  if (e == hipSuccess) e = set_lds_limit(reinterpret_cast<const void*>(kq), int(l2), done2);
+  if (e == hipSuccess) e = a.o_bf16 ? launch_dot_o<bf16_t>(a, st) : launch_dot_o<float>(a, st);
+  if (e != hipSuccess) return e;
+  const int ntile = (a.n + BM - 1) / BM;
+  kkv<<<dim3(uint32_t(int64_t(ntile) * a.Hkv)), 256, l1, st>>>(a, ntile);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, l2, st>>>(a, ntile);
+  return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_g(const PromptBwdArgs& a, hipStream_t st) {
+  return a.grad_bf16 ? launch<T, bf16_t, D>(a, st) : launch<T, float, D>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_prompt_bwd(const PromptBwdArgs& a, hipStream_t st) {
+  if (a.in_bf16) return a.d == 64 ? launch_g<bf16_t, 64>(a, st) : launch_g<bf16_t, 128>(a, st);
+  return a.d == 64 ? launch_g<float, 64>(a, st) : launch_g<float, 128>(a, st);
+}
+
+}  // namespace kda

@@ -1,0 +1,259 @@
+// kda_prompt_fwd.hip -- causal softmax attention over packed prompts, grouped heads.
+//
+//   o_i = sum_j P_ij v_j,  P_ij = exp(scale q_i . k_j - lse_i),  j in i's sequence, j <= i
+//   lse_i = log sum_j exp(scale q_i . k_j)
+//
+// Rows of all sequences lie behind one another; a workgroup takes 128 consecutive rows of one
+// query head, whichever sequences they belong to, and walks the keys from the start of its first
+// row's sequence to its last row in tiles of 64: short sequences share a tile instead of filling
+// one each, and the launch needs no list of lengths on the host.  Only tiles that a row's own
+// start or end cuts are masked.
+//
+// Four wavefronts of 32 rows.  Scores are formed transposed, S^T = K Q^T (keys x rows), so that
+// a lane holds 32 keys of one row: the softmax needs one exchange between the half-wavefronts,
+// and the probabilities are in place as the operand of O^T = V^T P^T (k steps over the keys in the
+// order the registers have, which the transposing reads of V follow).  The running maximum is
+// raised only when a tile exceeds it by 2^8 (any reference serves while nothing overflows), so
+// most tiles do not touch the accumulators.  Maximum, sum and accumulators are fp32; with bf16
+// elements P is rounded to bf16 for the second product, 2^-9 relative each, as the outputs are.
+#include "kda_prompt.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int BM = 128, BN = 64;
+
+// Non-finite elements of fragments: 16 (32) bit lanes that reach zero where an exponent is all
+// ones, over any number of fragments, and a fragment with those elements set to zero.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <typename T> struct Finite;
+template <> struct Finite<bf16_t> {
+  u16x2 low = {0xffff, 0xffff};
+  __device__ __forceinline__ void see(bf16x8 a) {
+    const u32x4 w = __builtin_bit_cast(u32x4, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) low = __builtin_elementwise_min(low, __builtin_bit_cast(u16x2, ~w[i] & 0x7f807f80u));
+  }
+  __device__ __forceinline__ bool all() const { return low[0] != 0 && low[1] != 0; }
+  __device__ __forceinline__ static bf16x8 only(bf16x8 a) {
+    u32x4 w = __builtin_bit_cast(u32x4, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((~w[i] & 0x7f80u) == 0) w[i] &= 0xffff0000u;
+      if ((~w[i] & 0x7f800000u) == 0) w[i] &= 0xffffu;
+    }
+    return __builtin_bit_cast(bf16x8, w);
+  }
+};
+template <> struct Finite<float> {
+  uint32_t low = 0xffffffffu;
+  __device__ __forceinline__ void see(f32x8 a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = ~__float_as_uint(a[i]) & 0x7f800000u;
+      low = x < low ? x : low;
+    }
+  }
+  __device__ __forceinline__ bool all() const { return low != 0; }
+  __device__ __forceinline__ static f32x8 only(f32x8 a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = (~__float_as_uint(a[i]) & 0x7f800000u) == 0 ? 0.f : a[i];
+    return a;
+  }
+};
+
+template <typename T, int D>
+constexpr size_t prompt_lds() { return size_t(2) * 2 * BN * D * sizeof(T); }
+
+template <typename T, typename TO, int D>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel(const PromptArgs a, int ntile) {
+  using O = Op<T>;
+  using F = typename O::frag;
+  using TD = Tile<T, D>;
+  constexpr int NK = D / 16, ND = D / 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T* const buf = reinterpret_cast<T*>(smem);  // [2][K tile, V tile]
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int head = id / ntile, tile = ntile - 1 - id % ntile;  // long rows first
+  const int r0 = tile * BM;
+  const int used = rows_used(a.cu, a.nseq, a.n);
+  if (r0 >= used) return;
+  const int kvh = head / (a.Hq / a.Hkv);
+  const int64_t kst = int64_t(a.Hkv) * D;
+  const T* kp = static_cast<const T*>(a.k) + int64_t(kvh) * D;
+  const T* vp = static_cast<const T*>(a.v) + int64_t(kvh) * D;
+
+  const int lo = span_of(a.cu, a.nseq, a.n, r0).start;
+  const int hi = r0 + BM < used ? r0 + BM : used;
+  const int w0 = r0 + 32 * wave, qi = w0 + l32;
+  const int wlast = w0 + 31 < used ? w0 + 31 : used - 1;  // the wavefront's last row (below w0: none)
+  const int qr = qi < used ? qi : used - 1;
+  const int start = span_of(a.cu, a.nseq, a.n, qr).start;
+  // starts rise with the rows: the wavefront's first and last
+  const int smin = __shfl(start, 0), smax = __shfl(start, 31);
+
+  // a negative scale is the positive one with the queries' signs turned; a scale of zero is the
+  // least normal number (a masked score, -inf, times zero would be NaN)
+  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.1754944e-38f);
+  F qf[NK];
+  {
+    const T* qp = static_cast<const T*>(a.q) + (int64_t(qr) * a.Hq + head) * D;
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      qf[kk] = O::load(qp + 16 * kk + 8 * h2);
+      if (a.scale < 0.f) qf[kk] = O::neg(qf[kk]);
+    }
+  }
+  f32x16 acc[ND];
+#pragma unroll
+  for (int i = 0; i < ND; ++i) acc[i] = zero16();
+  float m = -INFINITY, l = 0.f;
+
+  const int nt = (hi - lo + BN - 1) / BN;
+  auto fetch = [&](int t) {
+    T* kb = buf + (t & 1) * 2 * BN * D;
+    copy_rows<T, BN, D, 4>(kb, kp, kst, lo + t * BN, hi, wave, lane);
+    copy_rows<T, BN, D, 4>(kb + BN * D, vp, kst, lo + t * BN, hi, wave, lane);
+  };
+  fetch(0);
+  for (int t = 0; t < nt; ++t) {
+    copies_done();
+    if (t + 1 < nt) fetch(t + 1);
+    const T* Ks = buf + (t & 1) * 2 * BN * D;
+    const T* Vs = Ks + BN * D;
+    const int k0 = lo + t * BN;
+    if (wlast >= w0 && k0 <= wlast && k0 + BN > smin) {
+      f32x16 s[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s[j] = zero16();
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) s[j] = O::mma32(TD::row8(Ks, 32 * j + l32, 16 * kk + 8 * h2), qf[kk], s[j]);
+      }
+      const bool masked = !(k0 + BN - 1 <= w0 && k0 >= smax);
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = k0 + 32 * j + crow(i, h2);
+            s[j][i] = key <= qi && key >= start ? s[j][i] : -INFINITY;
+          }
+      }
+      float mt = s[0][0];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[j][i]);
+      mt = c * max_halves(mt);
+      if (__any(mt > m + 8.f)) {
+        const float mn = fmaxf(m, mt);
+        const float ref = mn == -INFINITY ? 0.f : mn;  // a row that has met no key yet
+        const float al = fast_exp2(m - ref);
+        l *= al;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][r] *= al;
+        m = mn;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[j][i] = fast_exp2(s[j][i] * c - ref);
+          l += s[j][i];
+        }
+      }
+      // A masked probability is zero, but zero times a NaN or infinity is not: where a tile is
+      // masked and holds such values, they leave the product and reach only the rows that see them.
+      if (masked) {
+        Finite<T> fin;
+#pragma unroll
+        for (int e = 0; e < 4 * ND; ++e)
+          fin.see(TD::col44(Vs, 16 * (e & 3) + 4 * h2, 16 * (e & 3) + 4 * h2 + 8, 32 * (e >> 2), lane));
+        if (__any(!fin.all())) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              const F pf = frag_of<T>(s[j], ks);
+              const int kr = 32 * j + 16 * ks + 4 * h2;
+#pragma unroll
+              for (int i = 0; i < ND; ++i)
+                acc[i] = O::mma32(Finite<T>::only(TD::col44(Vs, kr, kr + 8, 32 * i, lane)), pf, acc[i]);
+            }
+          for (int key = 0; key < BN; ++key) {
+            const bool seen = k0 + key <= qi && k0 + key >= start;
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+              for (int r4 = 0; r4 < 4; ++r4) {
+                const f32x4 x = TD::get4(Vs, key, 32 * i + 8 * r4 + 4 * h2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (seen && !(fabsf(x[e]) < INFINITY)) acc[i][4 * r4 + e] += x[e];
+              }
+          }
+          continue;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const F pf = frag_of<T>(s[j], ks);
+          const int kr = 32 * j + 16 * ks + 4 * h2;
+#pragma unroll
+          for (int i = 0; i < ND; ++i) acc[i] = O::mma32(TD::col44(Vs, kr, kr + 8, 32 * i, lane), pf, acc[i]);
+        }
+    }
+  }
+  l = sum_halves(l);
+  if (qi < used) {
+    const float inv = 1.0f / l;
+    TO* op = static_cast<TO*>(a.o) + (int64_t(qi) * a.Hq + head) * D;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        f32x4 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = acc[i][4 * r4 + j] * inv;
+        store4(op + 32 * i + 8 * r4 + 4 * h2, x);
+      }
+    if (a.lse && h2 == 0) a.lse[int64_t(qi) * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <typename T, typename TO, int D>
+hipError_t launch(const PromptArgs& a, hipStream_t st) {
+  auto kern = prompt_fwd_kernel<T, TO, D>;
+  constexpr size_t lds = prompt_lds<T, D>();
+  static std::atomic<uint64_t> done{0};
+  if constexpr (lds > 65536) {
+    const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), int(lds), done);
+    if (e != hipSuccess) return e;
+  }
+  const int ntile = (a.n + BM - 1) / BM;
+  kern<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, lds, st>>>(a, ntile);
+  return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_o(const PromptArgs& a, hipStream_t st) {
+  return a.out_bf16 ? launch<T, bf16_t, D>(a, st) : launch<T, float, D>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_prompt_fwd(const PromptArgs& a, hipStream_t st) {
+  if (a.in_bf16) return a.d == 64 ? launch_o<bf16_t, 64>(a, st) : launch_o<bf16_t, 128>(a, st);
+  return a.d == 64 ? launch_o<float, 64>(a, st) : launch_o<float, 128>(a, st);
+}
+
+}  // namespace kda

@@ -73,7 +73,8 @@ typedef enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
 const char* kda_status_string(int status);
 
 /* Library ABI version (major * 100 + minor): 200 since the chunked prefill
- * takes a workspace and the status codes are negative. */
+ * takes a workspace and the status codes are negative, 201 with the linear,
+ * prompt and cache attention. */
 int kda_version(void);
 
 /* 1 when kda_chunk_fwd / kda_chunk_fwd_z run the bf16 matrix-core kernel
@@ -335,6 +336,151 @@ kda_status kda_decode_replay(const void* q, const void* k, const void* v,
                              const int* accepted, void* o, kda_dtype o_dtype,
                              float* S_commit, int n_draft, int N, int H, int dk,
                              int dv, float scale, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Linear attention with a decay per head
+ *
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ *
+ * per batch entry and head: the recurrence of the delta rule above without its
+ * erase term and with one decay per head instead of one per key channel.
+ * Layouts, dtypes and the supported dk, dv are those of the chunked prefill.
+ *
+ *   q, k [B,T,H,dk] in_dtype    v [B,T,H,dv] in_dtype
+ *   g    fp32 log-decays, at most 0: [B,T,H] (g_per_head == 0), or [H], the
+ *        same for every token (g_per_head == 1).  Values below -10000 act as
+ *        -10000 (a decay of zero); -inf clears the state.  A positive g is not
+ *        an error, but sums beyond 80 in a chunk overflow fp32.
+ *
+ * A non-finite q, k or v reaches outputs of its own and later tokens, and may
+ * reach any output of its 64-token chunk.
+ */
+
+/*
+ * kda_linear_chunk_fwd -- chunked prefill with state in and out.
+ *
+ *   S_in   [B,H,dk,dv] fp32 or NULL (zero)      o [B,T,H,dv] o_dtype (written)
+ *   S_out  [B,H,dk,dv] fp32 or NULL; may equal S_in, not partially overlap it
+ *   workspace  device memory of kda_linear_chunk_fwd_workspace_bytes bytes,
+ *          16-byte aligned (NULL when that is 0); contents do not matter
+ *
+ * The state is held to fp32 whatever in_dtype is.  Few, long sequences are cut
+ * into segments that run side by side and are joined by a scan.
+ */
+size_t kda_linear_chunk_fwd_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype in_dtype);
+kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const float* g,
+                                int g_per_head, const float* S_in, void* o, kda_dtype o_dtype, float* S_out, int B,
+                                int T, int H, int dk, int dv, float scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * kda_linear_chunk_bwd -- gradients of kda_linear_chunk_fwd.
+ *
+ *   d_o    [B,T,H,dv] in_dtype        dS_out [B,H,dk,dv] fp32 or NULL (zero)
+ *   dq, dk [B,T,H,dk], dv [B,T,H,dv] in grad_dtype (written)
+ *   dg     fp32, in g's layout ([H]: summed over batch and tokens)
+ *   dS_in  [B,H,dk,dv] fp32 or NULL
+ *   workspace  kda_linear_chunk_bwd_workspace_bytes bytes, 16-byte aligned
+ *
+ * No output may overlap an input, another output or the workspace.  Every sum
+ * has a fixed order: two calls on the same inputs give the same bits.
+ */
+size_t kda_linear_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype in_dtype, int g_per_head);
+kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const float* g,
+                                int g_per_head, const float* S_in, const void* d_o, const float* dS_out, void* dq,
+                                void* dk, void* dv, kda_dtype grad_dtype, float* dg, float* dS_in, int B, int T, int H,
+                                int dk_dim, int dv_dim, float scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * kda_linear_decode_step -- one token per sequence: q, k [N,H,dk], v [N,H,dv],
+ * g [N,H] or [H].  S_out may equal S_in (update in place) but not partially
+ * overlap it; with another S_out the state in S_in is kept.
+ */
+kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, kda_dtype in_dtype, const float* g,
+                                  int g_per_head, const float* S_in, float* S_out, void* o, kda_dtype o_dtype, int N,
+                                  int H, int dk, int dv, float scale, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Causal softmax attention over packed prompts, grouped heads
+ *
+ *   o_i = sum_j P_ij v_j,  P_ij = exp(scale q_i . k_j - lse_i),
+ *   j in the sequence of row i, j <= i
+ *
+ *   q   [n,Hq,d] in_dtype    k, v [n,Hkv,d] in_dtype; Hkv divides Hq, and query
+ *       head h reads key head h / (Hq / Hkv).  d is 64 or 128.
+ *   cu_seqlens [n_seqs+1] int32, device memory, not decreasing, from 0 to at
+ *       most n: sequence s has rows cu_seqlens[s] .. cu_seqlens[s+1] - 1.
+ *       Sequences may be empty.  Rows at or past the last entry belong to no
+ *       sequence: they are not read, and their outputs are left as they were.
+ *       (Entries outside [0, n] or out of order give meaningless results, but
+ *       no access outside the arrays.)
+ *   o   [n,Hq,d] o_dtype (written)       lse [n,Hq] fp32 (written) or NULL
+ */
+kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
+                               void* o, kda_dtype o_dtype, float* lse, int n, int n_seqs, int Hq, int Hkv, int d,
+                               float scale, void* stream);
+
+/*
+ * kda_attn_prompt_bwd -- its gradients, from the forward's o and lse.
+ *   d_o [n,Hq,d] in_dtype;  dq [n,Hq,d], dk, dv [n,Hkv,d] in grad_dtype
+ *   (written; dk and dv summed over the query heads of a group)
+ *   workspace  kda_attn_prompt_bwd_workspace_bytes bytes, 16-byte aligned
+ * Every sum has one owner and a fixed order: the same bits every time.  A
+ * non-finite value in one sequence may reach gradients of its neighbours in
+ * the packed buffer.
+ */
+size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq);
+kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
+                               const void* o, kda_dtype o_dtype, const float* lse, const void* d_o, void* dq, void* dk,
+                               void* dv, kda_dtype grad_dtype, int n, int n_seqs, int Hq, int Hkv, int d, float scale,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Attention over a paged key-value cache held in 8 bits
+ *
+ *   k_cache [n_pages,Hkv,page,d], v_cache [n_pages,Hkv,d,page]: e4m3 codes
+ *       (one byte; 4 exponent and 3 mantissa bits, no infinities); page is 16,
+ *       32 or 64 tokens, d 64 or 128
+ *   k_scale, v_scale [n_pages,Hkv] fp32: a value is code * scale.  A scale is a
+ *       power of two, the smallest with max |x| <= 448 scale (at least 2^-100).
+ *   block_table [N,max_pages] int32: the page of tokens p page .. of sequence n
+ *       is block_table[n,p].  Each page belongs to one sequence.
+ *   context_len [N] int32: the tokens a sequence holds.
+ * All of them in device memory.
+ *
+ * kda_kv_cache_append -- quantises new tokens into their pages: k, v [n,Hkv,d]
+ * in_dtype, rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 behind the context_len[i]
+ * tokens that sequence i holds already (context_len is not changed).  Where a
+ * page already begun needs a larger scale, its earlier values are rounded again
+ * at that scale.  Rounding is to nearest even; infinities become the largest
+ * value, NaN stays NaN (neither enters the scale).  Tokens whose place lies
+ * past max_pages pages, or whose page id is outside [0, n_pages), are dropped.
+ */
+kda_status kda_kv_cache_append(const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
+                               const int* context_len, const int* block_table, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, int n, int N, int Hkv, int d, int page, int n_pages,
+                               int max_pages, void* stream);
+
+/*
+ * kda_attn_decode_step -- attention of one query token per sequence over all
+ * tokens it holds (append the token's own key and value first):
+ *   q [N,Hq,d] in_dtype -> o [N,Hq,d] o_dtype, lse [N,Hq] fp32 or NULL.
+ * A sequence with no tokens gets o = 0, lse = -inf.  Tokens past max_pages
+ * pages, or in a page whose id is outside [0, n_pages), are left out.  What
+ * lies in a page behind the last token is not used, whatever it holds.
+ *   workspace  kda_attn_decode_step_workspace_bytes bytes, 16-byte aligned
+ *          (NULL when that is 0)
+ */
+size_t kda_attn_decode_step_workspace_bytes(int N, int Hq, int Hkv, int d, int page, int max_pages);
+kda_status kda_attn_decode_step(const void* q, kda_dtype in_dtype, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, const int* block_table,
+                                const int* context_len, void* o, kda_dtype o_dtype, float* lse, int N, int Hq, int Hkv,
+                                int d, int page, int n_pages, int max_pages, float scale, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
