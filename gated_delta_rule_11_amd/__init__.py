@@ -104,7 +104,7 @@ def lib() -> ctypes.CDLL:
     L.kda_linear_decode_step.restype = I
     L.kda_attn_prompt_fwd.argtypes = [P, P, P, I, P, P, I, P, I, I, I, I, I, F, P]
     L.kda_attn_prompt_fwd.restype = I
-    L.kda_attn_prompt_bwd_workspace_bytes.argtypes = [I, I]
+    L.kda_attn_prompt_bwd_workspace_bytes.argtypes = [I] * 4
     L.kda_attn_prompt_bwd_workspace_bytes.restype = Z
     L.kda_attn_prompt_bwd.argtypes = [P, P, P, I, P, P, I, P, P, P, P, P, I, I, I, I, I, I, F, P, Z, P]
     L.kda_attn_prompt_bwd.restype = I
@@ -640,9 +640,9 @@ def attn_prompt_fwd(q, k, v, cu_seqlens, scale: Optional[float] = None, o=None, 
     return o, lse
 
 
-def attn_prompt_bwd_workspace_bytes(n: int, Hq: int) -> int:
-    """Device bytes ``attn_prompt_bwd`` needs as workspace for n rows of Hq query heads."""
-    return int(lib().kda_attn_prompt_bwd_workspace_bytes(int(n), int(Hq)))
+def attn_prompt_bwd_workspace_bytes(n: int, Hq: int, Hkv: int, d: int) -> int:
+    """Device bytes ``attn_prompt_bwd`` needs as workspace for n rows."""
+    return int(lib().kda_attn_prompt_bwd_workspace_bytes(int(n), int(Hq), int(Hkv), int(d)))
 
 
 @_run_on_stream
@@ -658,7 +658,7 @@ def attn_prompt_bwd(q, k, v, cu_seqlens, o, lse, d_o, scale: Optional[float] = N
     out = {"dq": torch.zeros((n, Hq, d), dtype=grad_dtype, device=q.device),
            "dk": torch.zeros((n, Hkv, d), dtype=grad_dtype, device=q.device),
            "dv": torch.zeros((n, Hkv, d), dtype=grad_dtype, device=q.device)}
-    wp, wb, _keep = _need(workspace, attn_prompt_bwd_workspace_bytes(n, Hq), q.device)
+    wp, wb, _keep = _need(workspace, attn_prompt_bwd_workspace_bytes(n, Hq, Hkv, d), q.device)
     _check(lib().kda_attn_prompt_bwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(cu_seqlens), _p(o), _dtype_code(o), _p(lse),
                                      _p(d_o), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _dtype_code(out["dq"]), n, ns,
                                      Hq, Hkv, d, _softmax_scale(scale, d), wp, wb, _stream(None)), what)

@@ -376,23 +376,43 @@ __global__ __launch_bounds__(256, 2) void cache_step_kernel(const CacheStepArgs 
   }
 }
 
-// Joins the parts of a context: one workgroup of d threads per (sequence, query head).
-template <typename TO>
-__global__ void cache_join_kernel(const float* part, TO* o, float* lse, int splits, int d) {
+// Joins the parts of a context: one workgroup per (sequence, query head).  256 / D groups of
+// D threads take the parts in turn, so that the loads of many are in flight.
+template <typename TO, int D>
+__global__ __launch_bounds__(256) void cache_join_kernel(const float* part, TO* o, float* lse, int splits) {
+  constexpr int NG = 256 / D;
+  __shared__ float sm[4], sl[NG][D], sx[NG][D];
+  const int tid = threadIdx.x, d = tid % D, grp = tid / D;
   const int64_t row = blockIdx.x;
-  const float* p = part + row * splits * (d + 2);
+  const float* p = part + row * splits * (D + 2);
   float m = -INFINITY;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, p[int64_t(s) * (d + 2)]);
+  for (int s = tid; s < splits; s += 256) m = fmaxf(m, p[int64_t(s) * (D + 2)]);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+  if ((tid & 63) == 0) sm[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
   const float ref = m == -INFINITY ? 0.f : m;
   float l = 0.f, x = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float* ps = p + int64_t(s) * (d + 2);
+#pragma unroll 8
+  for (int s = grp; s < splits; s += NG) {
+    const float* ps = p + int64_t(s) * (D + 2);
     const float f = fast_exp2(ps[0] - ref);
     l += f * ps[1];
-    x += f * ps[2 + threadIdx.x];
+    x += f * ps[2 + d];
   }
-  io<TO>::store(o, row * d + threadIdx.x, l == 0.f ? 0.f : x / l);
-  if (lse && threadIdx.x == 0) lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+  sl[grp][d] = l;
+  sx[grp][d] = x;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int g = 1; g < NG; ++g) {
+      l += sl[g][d];
+      x += sx[g][d];
+    }
+    io<TO>::store(o, row * D + d, l == 0.f ? 0.f : x / l);
+    if (lse && d == 0) lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+  }
 }
 
 template <typename T, typename TO, int D>
@@ -401,8 +421,8 @@ hipError_t launch_step(const CacheStepArgs& a, hipStream_t st) {
   cache_step_kernel<T, TO, D><<<dim3(uint32_t(int64_t(a.N) * a.Hkv * GT * a.splits)), 256, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  cache_join_kernel<TO><<<dim3(uint32_t(int64_t(a.N) * a.Hq)), D, 0, st>>>(a.part, static_cast<TO*>(a.o), a.lse,
-                                                                          a.splits, D);
+  cache_join_kernel<TO, D><<<dim3(uint32_t(int64_t(a.N) * a.Hq)), 256, 0, st>>>(a.part, static_cast<TO*>(a.o), a.lse,
+                                                                               a.splits);
   return hipGetLastError();
 }
 

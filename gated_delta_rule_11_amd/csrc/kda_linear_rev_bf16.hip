@@ -1,0 +1,9 @@
+// kda_linear_rev_bf16.hip -- the backward walks of kda_linear_walk.hpp for bf16 elements (one of four files
+// that compile side by side).
+#include <type_traits>
+
+#include "kda_linear_walk.hpp"
+
+namespace kda {
+hipError_t launch_linear_rev_bf16(const LinearArgs& a, hipStream_t st) { return launch_walk_t<bf16_t, true>(a, st); }
+}  // namespace kda

@@ -1,0 +1,431 @@
+// kda_linear_walk.hpp -- linear attention with a decay per head, chunked: the kernel that walks a
+// sequence's chunks, forwards for the outputs and for dq, backwards for dk and dv.
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// per (b, h), g_t <= 0 a scalar.  In a chunk of C tokens with entry state S and in-chunk sums
+// G_t = g_1 + .. + g_t,
+//   o_t   = scale (e^{G_t} S^T q_t + sum_{s <= t} e^{G_t - G_s} (q_t . k_s) v_s)
+//   S_out = e^{G_C} S + sum_s e^{G_C - G_s} k_s v_s^T.
+// Every exponent is a difference of sums over later tokens, so at most 0: nothing overflows,
+// whatever the decays.  The sums are formed in 64 bits and kept as two fp32 parts, so a strong
+// decay earlier in the chunk does not cost the later differences their low bits.
+//
+// The gradients are the same computation with the tensors in other roles.  With R = dL/dS,
+//   dq_t = scale sum_{s <= t} e^{G_t - G_s} (do_t . v_s) k_s + ..   forwards,  (q, k, v) <- (do, v, k)
+//   dk_s = scale sum_{t >= s} e^{G_t - G_s} (v_s . do_t) q_t + ..   backwards, (q, k, v) <- (v, do, q)
+//   dv_s = scale sum_{t >= s} e^{G_t - G_s} (k_s . q_t) do_t + ..   backwards, (q, k, v) <- (k, q, do)
+// where the backward walk (REV) holds R_in = e^{G_C} R + scale sum_t e^{G_t} q_t do_t^T (or its
+// transpose) and its outputs take e^{G_C - G_s} of it.  A log-decay scales all that crosses it, so
+//   dg_t = <R_c, S_c> + sum_{t <= u, u before c} (q_u . dq_u - k_u . dk_u)
+// for any boundary c at or behind t.  The walks for dq and dk (DOT) leave those dot products, of
+// the unrounded gradients, and every kBlockChunks chunks the one keeps S, the other multiplies its
+// R with it: the sums above then never run over more than one such block, and cancel no more than it holds.
+//
+// One workgroup per (b, h, slice of up to 64 value columns, segment).  Wavefronts 0 .. NSW - 1 each
+// own 16 value columns and hold that dk x 16 block of the state in their accumulators; with
+// outputs, the others (one per 16 tokens of a chunk) form the decayed scores P of the next chunk
+// and copy the one after it into LDS, three chunks in rotation, so that a step has one barrier
+// and both the copies' and the scores' latency pass beside the state's products.  All products are
+// 16x16x32 with fp32 accumulation: (S^T q) takes the state straight from the accumulators (their
+// layout is an operand's), the values' transposing reads serve both P V and the update.
+//
+// With bf16 elements P, and the copy of S that the outputs read, are rounded to bf16, half a unit
+// of the last place that the outputs have anyway.  The state takes its rows e^{G_C - G_s} v_s as
+// three bf16 parts (24 bits), so it is fp32-accurate however long the sequence; with DOT, P and
+// S too.  These products are not what bounds the walk: its bytes are.
+//
+// Few, long sequences are cut into segments (the ABI layer's rule).  The decay being a scalar, a
+// segment's transition is one number: a first walk leaves every segment's end state from zero, a
+// scan joins them, a second walk from the true entry states writes the outputs.
+#pragma once
+
+#include "kda_mix_launch.hpp"
+#include "kda_mma.hpp"
+
+namespace kda {
+
+namespace {
+
+// A decay below this is zero in fp32 whatever follows; -inf (a reset) would make differences NaN.
+constexpr float kLeastLog = -1.0e4f;
+
+// OUT: 0 the state only, 1 outputs, 2 outputs and their dot products, unrounded
+template <typename T, int DK, int DV, int OUT>
+struct WalkShape {
+  static constexpr int C = linear_chunk(sizeof(T) == 2);
+  static constexpr int DKP = DK < 32 ? 32 : DK;    // key channels in LDS
+  static constexpr int DVS = DV < 64 ? DV : 64;    // value columns of a workgroup
+  static constexpr int VC = DVS < 32 ? 32 : DVS;   // and in LDS
+  static constexpr int NSL = DV / DVS, NSW = DVS / 16, TT = C / 16, U = C / 32;
+  static constexpr int NPW = OUT ? TT : 1;         // scoring and copying wavefronts
+  static constexpr int NT = 64 * (NSW + NPW);
+  static constexpr int NKK = DKP / 32, NKT = DK / 16;
+  static constexpr bool PF = OUT == 2 || sizeof(T) == 4;  // P in fp32
+  static constexpr int kK = C * DKP * int(sizeof(T)), kV = C * VC * int(sizeof(T)), kP = C * C * (PF ? 4 : 2);
+  static constexpr int kG = (4 * C + 4) * 4;  // G hi, G lo, the outputs' and the update's weights, e^{G_C}
+  static constexpr int oQ = 3 * kK, oV = oQ + (OUT ? 3 * kK : 0), oP = oV + 3 * kV, oG = oP + (OUT ? 2 * kP : 0);
+  static constexpr size_t lds = size_t(oG) + 3 * kG;
+  static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+};
+
+// x as parts of the element type whose sum is x to 8 (16, 24) bits.
+template <typename T, int N>
+struct Parts {
+  typename Op<T>::frag p[N];
+  __device__ __forceinline__ explicit Parts(f32x8 x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      p[i] = Op<T>::pack(x);
+      if (i + 1 < N) x -= Op<T>::unpack(p[i]);
+    }
+  }
+  __device__ __forceinline__ f32x4 left(typename Op<T>::frag b, f32x4 c) const {  // sum over parts of p b
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) c = Op<T>::mma16(p[i], b, c);
+    return c;
+  }
+  __device__ __forceinline__ f32x4 right(typename Op<T>::frag a, f32x4 c) const {  // .. of a p
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i) c = Op<T>::mma16(a, p[i], c);
+    return c;
+  }
+};
+
+template <typename T, typename TO, int DK, int DV, int OUT, bool REV>
+__global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_kernel(const LinearArgs a) {
+  using W = WalkShape<T, DK, DV, OUT>;
+  using O = Op<T>;
+  using F = typename O::frag;
+  using TK = Tile<T, W::DKP>;
+  using TV = Tile<T, W::VC>;
+  using PT = std::conditional_t<W::PF, float, T>;
+  using TP = Tile<PT, W::C>;
+  constexpr int C = W::C, NSW = W::NSW, TT = W::TT, U = W::U, NKK = W::NKK, NKT = W::NKT;
+  constexpr int kExact = sizeof(T) == 2 ? 3 : 1;           // parts of an fp32-accurate operand
+  constexpr int kOut = OUT == 2 ? kExact : 1;              // of P and S in the outputs
+  extern __shared__ __align__(1024) unsigned char smem[];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15,
+            g4 = lane >> 4;
+  int id = xcd_order(blockIdx.x, gridDim.x);
+  const int slice = id % W::NSL;
+  id /= W::NSL;
+  const int seg = id % a.nseg;
+  const int64_t bh = id / a.nseg;
+  const int64_t b = bh / a.H, head = bh % a.H;
+  const int nch = (a.T + C - 1) / C;
+  const int n0 = seg * a.seg_chunks, n1 = n0 + a.seg_chunks < nch ? n0 + a.seg_chunks : nch;
+  const int64_t tok = b * a.T;  // the sequence's first row
+  auto chunk_of = [&](int n) { return REV ? nch - 1 - n : n; };
+  auto Ks = [&](int n) { return reinterpret_cast<T*>(smem + (n % 3) * W::kK); };
+  auto Qs = [&](int n) { return reinterpret_cast<T*>(smem + W::oQ + (n % 3) * W::kK); };
+  auto Vs = [&](int n) { return reinterpret_cast<T*>(smem + W::oV + (n % 3) * W::kV); };
+  auto Ps = [&](int n) { return reinterpret_cast<PT*>(smem + W::oP + (n & 1) * W::kP); };
+  auto gates = [&](int n) { return reinterpret_cast<float*>(smem + W::oG + (n % 3) * W::kG); };
+
+  // key channels 16 .. 31 of a 16-channel head are zero in LDS; the copies leave them alone
+  if constexpr (DK < 32) {
+    for (int i = tid * 4; i < (OUT ? 2 : 1) * 3 * W::kK; i += W::NT * 4) *reinterpret_cast<uint32_t*>(smem + i) = 0u;
+    __syncthreads();
+  }
+
+  if (wave >= NSW) {
+    // ---- scores, gates and copies ----
+    const int p = wave - NSW;
+    const int64_t kst = int64_t(a.H) * DK, vst = int64_t(a.H) * DV;
+    const T* kp = static_cast<const T*>(a.k) + (tok * a.H + head) * DK;
+    const T* qp = OUT ? static_cast<const T*>(a.q) + (tok * a.H + head) * DK : nullptr;
+    const T* vp = static_cast<const T*>(a.v) + (tok * a.H + head) * DV + slice * W::DVS;
+    // rows at or past the sequence's end repeat its last row (their weights are zero)
+    auto copy = [&](auto tile_tag, T* tile, const T* base, int64_t stride, int64_t t0, int cols) {
+      using L = decltype(tile_tag);
+      constexpr int PER = 64 / L::CH;
+#pragma unroll
+      for (int r0 = 0; r0 < C; r0 += PER * W::NPW) {
+        const int rw = r0 + p * PER;
+        if (rw >= C) break;
+        const int r = rw + lane / L::CH, ch = (lane % L::CH) ^ L::swz(r);
+        int64_t t = t0 + r;
+        t = t < a.T ? t : a.T - 1;
+        if (ch * L::EPC < cols) lds_copy16(base + t * stride + ch * L::EPC, lds_offset(tile + rw * (L::CH * L::EPC)));
+      }
+    };
+    auto fetch = [&](int n) {
+      const int64_t t0 = int64_t(chunk_of(n)) * C;
+      copy(TK{}, Ks(n), kp, kst, t0, DK);
+      if constexpr (OUT > 0) copy(TK{}, Qs(n), qp, kst, t0, DK);
+      copy(TV{}, Vs(n), vp, vst, t0, W::DVS);
+    };
+    // the gate wavefront has the fewest scores
+    const bool gate = p == (REV ? W::NPW - 1 : 0);
+    const float* gp = a.g_head ? a.g + head : a.g + tok * a.H + head;
+    const int64_t gst = a.g_head ? 0 : a.H;
+    auto gate_of = [&](int n) -> float {
+      const int64_t t = int64_t(chunk_of(n)) * C + lane;
+      const float g = (n < n1 && lane < C && t < a.T) ? gp[t * gst] : 0.f;
+      return g < kLeastLog ? kLeastLog : g;
+    };
+    double total = 0.0;  // log2 of the walk's decay
+    auto gate_sums = [&](int n, float g) {
+      double G = double(g) * 1.4426950408889634;
+#pragma unroll
+      for (int d = 1; d < C; d <<= 1) {
+        const double up = __shfl_up(G, d);
+        if (lane >= d) G += up;
+      }
+      const double Gc = __shfl(G, C - 1);
+      total += Gc;
+      const bool live = int64_t(chunk_of(n)) * C + lane < a.T;
+      if (lane < C) {
+        float* ga = gates(n);
+        const float hi = float(G), to_end = fast_exp2(float(Gc - G)), from_start = fast_exp2(float(G));
+        ga[lane] = hi;
+        ga[C + lane] = float(G - double(hi));
+        ga[2 * C + lane] = REV ? to_end : from_start;
+        ga[3 * C + lane] = live ? (REV ? a.scale * from_start : to_end) : 0.f;
+        if (lane == C - 1) ga[4 * C] = from_start;
+      }
+    };
+    const uint32_t brow = TK::b_row8_16(lane);
+    // scores of 16 tokens (columns t) with the source tokens s that they take from, transposed: rows s
+    auto scores = [&](int n) {
+      if constexpr (OUT > 0) {
+        const uint32_t kb = TK::at(Ks(n)) + brow, qb = TK::at(Qs(n)) + brow;
+        const float* ga = gates(n);
+        PT* P = Ps(n);
+        F qf[NKK];
+#pragma unroll
+        for (int kk = 0; kk < NKK; ++kk) qf[kk] = TK::row8_16(qb + 16 * p * TK::ROWB, 0, kk);
+        const int t = 16 * p + l16;
+        const int64_t live = a.T - int64_t(chunk_of(n)) * C;
+        const float thi = ga[t], tlo = ga[C + t];
+#pragma unroll
+        for (int si = 0; si < TT; ++si) {
+          const bool on = REV ? si >= p : si <= p;
+          if (!on && si / 2 != p / 2) continue;  // never read
+          f32x4 c = {0, 0, 0, 0}, x = c;
+          const int s = 16 * si + 4 * g4;
+          if (on) {
+#pragma unroll
+            for (int kk = 0; kk < NKK; ++kk) c = O::mma16(TK::row8_16(kb, si, kk), qf[kk], c);
+            const f32x4 shi = *reinterpret_cast<const f32x4*>(ga + s), slo = *reinterpret_cast<const f32x4*>(ga + C + s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float d = (thi - shi[j]) + (tlo - slo[j]);
+              // backwards the sources lie behind t, and may lie behind the sequence
+              if constexpr (REV) x[j] = s + j >= t && s + j < live ? a.scale * fast_exp2(-d) * c[j] : 0.f;
+              else x[j] = s + j <= t ? fast_exp2(d) * c[j] : 0.f;
+            }
+          }
+          TP::put4(P, t, s, x);
+        }
+      }
+    };
+    if (n0 < n1) {
+      fetch(n0);
+      if (n0 + 1 < n1) fetch(n0 + 1);
+      float g = 0.f;
+      if (gate) {
+        gate_sums(n0, gate_of(n0));
+        if (n0 + 1 < n1) gate_sums(n0 + 1, gate_of(n0 + 1));
+        g = gate_of(n0 + 2);
+      }
+      copies_landed();
+      lds_barrier();
+      scores(n0);
+      lds_barrier();
+      for (int n = n0; n < n1; ++n) {
+        if (n + 2 < n1) {
+          fetch(n + 2);
+          if (gate) {
+            gate_sums(n + 2, g);
+            g = gate_of(n + 3);
+          }
+        }
+        if (n + 1 < n1) scores(n + 1);
+        copies_landed();
+        lds_barrier();
+      }
+    }
+    if (a.seg_decay && gate && lane == 0 && slice == 0) a.seg_decay[bh * a.nseg + seg] = float(exp2(total));
+    return;
+  }
+
+  // ---- the state ----
+  const int col = slice * W::DVS + 16 * wave + l16;  // this lane's value column
+  f32x4 S[NKT];
+  {
+    const float* Sin = a.S_in ? a.S_in + (a.S_in_seg ? bh * a.nseg + seg : bh) * DK * DV : nullptr;
+    if (!a.S_in_seg && seg > 0) Sin = nullptr;  // a first walk's later segments start from zero
+    const bool tr = a.state_tr && !a.S_in_seg;
+#pragma unroll
+    for (int i = 0; i < NKT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * g4 + r;
+        S[i][r] = Sin ? Sin[tr ? col * DK + row : row * DV + col] : 0.f;
+      }
+  }
+  // states kept for dg, in the accumulators' order
+  const int nblk = (nch + kBlockChunks - 1) / kBlockChunks;
+  const int part = slice * NSW + wave;
+  auto kept = [&](int blk) {
+    return reinterpret_cast<f32x4*>(a.ckpt) + (((bh * (nblk + 1) + blk) * W::NSL + slice) * NSW + wave) * NKT * 64 + lane;
+  };
+  auto keep = [&](int blk) {
+    f32x4* c = kept(blk);
+#pragma unroll
+    for (int i = 0; i < NKT; ++i) c[i * 64] = S[i];
+  };
+  auto meet = [&](int blk) {  // <R, S> at the end of block blk - 1
+    const f32x4* c = kept(blk);
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < NKT; ++i) {
+      const f32x4 s = c[i * 64];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x += s[r] * S[i][r];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    if (lane == 0) a.bsum[(bh * nblk + blk - 1) * (W::NSL * NSW) + part] = x;
+  };
+  if constexpr (OUT == 2 && REV)
+    if (seg == 0 && nch > 0) meet(nblk);
+
+  if (n0 < n1) {
+    lds_barrier();
+    lds_barrier();
+    const uint32_t qrow = TK::b_row44_16(lane), kcol = TK::b_col8_16(lane), vcol = TV::b_col8_16(lane),
+                   prow = TP::b_row8_16(lane);
+    const int64_t ost = int64_t(a.H) * DV;
+    const int64_t obase = (tok * a.H + head) * DV + slice * W::DVS + 16 * wave + 4 * g4;
+    for (int n = n0; n < n1; ++n) {
+      const int c = chunk_of(n);
+      const int64_t t0 = int64_t(c) * C;
+      const float* ga = gates(n);
+      const uint32_t kb = TK::at(Ks(n)) + kcol, vb = TV::at(Vs(n)) + vcol;
+      if constexpr (OUT == 2 && !REV)
+        if (c % kBlockChunks == 0) keep(c / kBlockChunks);
+      // the chunk's values in this wavefront's columns, tokens along k
+      F vf[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) vf[u] = TV::col8_16(vb, u, wave);
+
+      if constexpr (OUT > 0) {
+        f32x4 dots[TT];  // the tensor that the outputs meet, at the outputs' places
+        if constexpr (OUT == 2)
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt) {
+            const int64_t t = t0 + 16 * tt + l16;
+            const T* dp = static_cast<const T*>(a.dot) + obase + (t < a.T ? t : a.T - 1) * ost;
+            if constexpr (sizeof(T) == 2) dots[tt] = __builtin_convertvector(*reinterpret_cast<const bf16x4*>(dp), f32x4);
+            else dots[tt] = *reinterpret_cast<const f32x4*>(dp);
+          }
+        const uint32_t qb = TK::at(Qs(n)) + qrow, pb = TP::at(Ps(n)) + prow;
+        f32x4 acc[TT];
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < NKK; ++kk) {
+          const f32x4 hi = 2 * kk + 1 < NKT ? S[(2 * kk + 1) % NKT] : f32x4{0, 0, 0, 0};
+          const Parts<T, kOut> sf(__builtin_shufflevector(S[2 * kk], hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt) acc[tt] = sf.left(TK::row44_16(qb, tt, kk), acc[tt]);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          acc[tt] *= ga[2 * C + 16 * tt + l16];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (REV ? u < tt / 2 : u > tt / 2) continue;
+            if constexpr (W::PF && sizeof(T) == 2) acc[tt] = Parts<T, kOut>(TP::row8_16(pb, tt, u)).right(vf[u], acc[tt]);
+            else acc[tt] = O::mma16(vf[u], TP::row8_16(pb, tt, u), acc[tt]);
+          }
+          const int64_t t = t0 + 16 * tt + l16;
+          f32x4 x = acc[tt];
+          if constexpr (!REV) x *= a.scale;
+          if (t < a.T) store4(static_cast<TO*>(a.o) + obase + t * ost, x);
+          if constexpr (OUT == 2) {
+            x *= dots[tt];
+            float d = (x[0] + x[1]) + (x[2] + x[3]);
+            d += __shfl_xor(d, 16);
+            d += __shfl_xor(d, 32);
+            if (g4 == 0 && t < a.T) a.x[(int64_t(part) * a.B * a.H + bh) * a.T + t] = d;
+          }
+        }
+      }
+
+      const float ec = ga[4 * C];
+#pragma unroll
+      for (int i = 0; i < NKT; ++i) S[i] *= ec;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* w = ga + 3 * C + 32 * u + 8 * g4;
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(w), w1 = *reinterpret_cast<const f32x4*>(w + 4);
+        const Parts<T, kExact> x(O::unpack(vf[u]) * __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int i = 0; i < NKT; ++i) S[i] = x.right(TK::col8_16(kb, u, i), S[i]);
+      }
+      if constexpr (OUT == 2 && REV)
+        if (c % kBlockChunks == 0 && c > 0) meet(c / kBlockChunks);
+      lds_barrier();
+    }
+  }
+
+  if constexpr (OUT == 2 && !REV)
+    if (seg == a.nseg - 1) keep(nblk);
+  if (a.S_out && (a.S_out_seg || seg == a.nseg - 1)) {
+    float* So = a.S_out + (a.S_out_seg ? bh * a.nseg + seg : bh) * DK * DV;
+#pragma unroll
+    for (int i = 0; i < NKT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) So[(16 * i + 4 * g4 + r) * DV + col] = S[i][r];
+  }
+}
+
+template <typename T, typename TO, int DK, int DV, int OUT, bool REV>
+hipError_t launch_walk(const LinearArgs& a, hipStream_t st) {
+  using W = WalkShape<T, DK, DV, OUT>;
+  auto kern = linear_walk_kernel<T, TO, DK, DV, OUT, REV>;
+  static std::atomic<uint64_t> done{0};
+  if constexpr (W::lds > 65536) {
+    const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), int(W::lds), done);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t grid = int64_t(a.B) * a.H * a.nseg * W::NSL;
+  kern<<<dim3(uint32_t(grid)), W::NT, W::lds, st>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int DK, int DV, bool REV>
+hipError_t launch_walk_d(const LinearArgs& a, hipStream_t st) {
+  if (!a.o) return launch_walk<T, T, DK, DV, 0, REV>(a, st);
+  if (a.dot) return a.out_bf16 ? launch_walk<T, bf16_t, DK, DV, 2, REV>(a, st) : launch_walk<T, float, DK, DV, 2, REV>(a, st);
+  return a.out_bf16 ? launch_walk<T, bf16_t, DK, DV, 1, REV>(a, st) : launch_walk<T, float, DK, DV, 1, REV>(a, st);
+}
+
+template <typename T, int DK, bool REV>
+hipError_t launch_walk_k(const LinearArgs& a, hipStream_t st) {
+  switch (a.dv) {
+    case 16: return launch_walk_d<T, DK, 16, REV>(a, st);
+    case 32: return launch_walk_d<T, DK, 32, REV>(a, st);
+    case 64: return launch_walk_d<T, DK, 64, REV>(a, st);
+    default: return launch_walk_d<T, DK, 128, REV>(a, st);
+  }
+}
+
+template <typename T, bool REV>
+hipError_t launch_walk_t(const LinearArgs& a, hipStream_t st) {
+  switch (a.dk) {
+    case 16: return launch_walk_k<T, 16, REV>(a, st);
+    case 32: return launch_walk_k<T, 32, REV>(a, st);
+    case 64: return launch_walk_k<T, 64, REV>(a, st);
+    default: return launch_walk_k<T, 128, REV>(a, st);
+  }
+}
+
+}  // namespace
+
+}  // namespace kda

@@ -27,18 +27,17 @@ struct LinearForm {
 
 // A walk runs one workgroup per (b, h, slice of up to 64 value columns), chunk after chunk.  Where
 // that leaves compute units without work the sequence is cut into segments of at least
-// kMinSegChunks chunks, until kWantUnits workgroups exist: the end states then cost one more
-// pass over k and v.  `slices` is 1 where the chunk's state is walked in one piece.
-constexpr int64_t kWantUnits = 512;
-constexpr int64_t kMinUnits = 256;  // compute units: a walk that fills them is not cut
+// kMinSegChunks chunks, as many as keep to one workgroup per compute unit: the end states then
+// cost one more pass over k and v.
+constexpr int64_t kUnits = 256;
 constexpr int64_t kMinSegChunks = 4;
 LinearForm linear_form(int64_t B, int64_t T, int64_t H, int dv, bool bf16) {
   const int C = linear_chunk(bf16);
   LinearForm f{(T + C - 1) / C, 1, 0};
   f.seg_chunks = int(f.nch);
   const int64_t units = B * H * (dv > 64 ? 2 : 1);
-  if (units <= 0 || f.nch <= 0 || units >= kMinUnits) return f;
-  int64_t segs = kWantUnits / units;
+  if (units <= 0 || f.nch <= 0) return f;
+  int64_t segs = kUnits / units;
   segs = segs < f.nch / kMinSegChunks ? segs : f.nch / kMinSegChunks;
   if (segs < 2) return f;
   f.seg_chunks = int((f.nch + segs - 1) / segs);
@@ -63,35 +62,41 @@ hipError_t enter_segments(LinearArgs& a, const LinearForm& f, float* ws, hipStre
   float* E = St + bh * f.nseg * state;
   float* decay = E + bh * f.nseg * state;
   LinearArgs p = a;  // end states from zero
-  p.q = nullptr; p.o = nullptr; p.S_in = nullptr; p.ckpt = nullptr;
+  p.o = nullptr; p.S_in = nullptr; p.dot = nullptr;
   p.S_out = St; p.S_out_seg = true; p.seg_decay = decay;
   hipError_t e = launch_linear_walk(p, st);
   if (e != hipSuccess) return e;
-  e = launch_linear_scan(LinearScanArgs{a.S_in, St, decay, E, bh, f.nseg, int(state)}, st);
+  e = launch_linear_scan(LinearScanArgs{a.S_in, St, decay, E, bh, f.nseg, a.dk, a.dv, a.state_tr}, st);
   a.S_in = E;
   a.S_in_seg = true;
   return e;
 }
 
-// The gradient kernel's launch has one workgroup per chunk of every (b, h).
+// The largest launch of a backward, and sizes that keep its layout within 64 bits.
 bool bwd_grid_ok(int64_t B, int64_t T, int64_t H, bool bf16) {
-  const int C = linear_chunk(bf16);
-  const int64_t nch = (T + C - 1) / C;
-  return B * H * 2 <= kMaxGrid && B * H * nch <= kMaxGrid;
+  const int64_t nblk = (T + linear_chunk(bf16) * kBlockChunks - 1) / (linear_chunk(bf16) * kBlockChunks);
+  return B * H * 64 <= kMaxGrid && B * H * nblk <= kMaxGrid / 2;
 }
 
+// Workspace of the backward, in floats: kept states, dot products and boundary terms for dg, one
+// walk's segments at a time, dg per token when g is per head.
 struct BwdLayout {
-  LinearForm f;
-  int64_t ckpt, seg, dg, total;  // floats
+  LinearForm fk, fv;  // walks over value columns of dk, and of dv
+  int64_t nblk, ckpt, x, bsum, seg, dg, total;
 };
 BwdLayout bwd_layout(int64_t B, int64_t T, int64_t H, int dk, int dv, bool bf16, bool g_head) {
   BwdLayout l{};
-  l.f = linear_form(B, T, H, dv, bf16);
+  l.fk = linear_form(B, T, H, dk, bf16);
+  l.fv = linear_form(B, T, H, dv, bf16);
   const int64_t bh = B * H, state = int64_t(dk) * dv;
-  l.ckpt = bh * l.f.nch * state;
-  l.seg = seg_floats(l.f, bh, state);
+  l.nblk = (l.fk.nch + kBlockChunks - 1) / kBlockChunks;
+  l.ckpt = bh * (l.nblk + 1) * state;
+  l.x = align4(bh * T * (dk / 16));
+  l.bsum = align4(bh * l.nblk * (dk / 16));
+  const int64_t a = seg_floats(l.fk, bh, state), b = seg_floats(l.fv, bh, state);
+  l.seg = a > b ? a : b;
   l.dg = g_head ? align4(B * T * H) : 0;
-  l.total = 2 * l.ckpt + l.seg + l.dg;
+  l.total = T > 0 ? l.ckpt + 2 * l.x + l.bsum + l.seg + l.dg : 0;
   return l;
 }
 
@@ -106,6 +111,12 @@ kda_status heads_ok(int64_t n, int64_t Hq, int64_t Hkv, int64_t d) {
   if (!sizes_ok(n, 1, Hq, d, d) || Hkv < 1 || n > 0x7fffffffLL - 256) return KDA_ERR_SHAPE;
   if (!attn_dim_ok(int(d)) || Hq % Hkv != 0) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
+}
+
+// Workspace of the prompts' backward: D, and the parts of dk and dv.
+int64_t prompt_bwd_floats(int n, int Hq, int Hkv, int d) {
+  const int parts = prompt_bwd_parts(n, Hq, Hkv);
+  return align4(int64_t(n) * Hq) + (parts > 1 ? int64_t(parts) * 2 * n * Hkv * d : 0);
 }
 
 }  // namespace
@@ -197,30 +208,42 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, kda
       if (&o2 != &o && overlap(o, o2)) return KDA_ERR_ALIAS;
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
-  float* S = static_cast<float*>(workspace);
-  float* R = S + l.ckpt;
-  float* seg = R + l.ckpt;
+  float* ckpt = static_cast<float*>(workspace);
+  float* xq = ckpt + l.ckpt;
+  float* xk = xq + l.x;
+  float* bsum = xk + l.x;
+  float* seg = bsum + l.bsum;
   float* dgt = g_per_head ? seg + l.seg : dg;
   LinearArgs w{};
-  w.B = B; w.T = T; w.H = H; w.dk = dk_dim; w.dv = dv_dim; w.scale = scale;
-  w.in_bf16 = bf16; w.g_head = g_per_head != 0; w.g = g;
+  w.B = B; w.T = T; w.H = H; w.scale = scale; w.g = g;
+  w.in_bf16 = bf16; w.out_bf16 = grad_dtype == KDA_BF16; w.g_head = g_per_head != 0;
+  w.ckpt = ckpt; w.bsum = bsum;
   hipError_t err = hipSuccess;
+  auto walk = [&](LinearArgs x, const LinearForm& f) {
+    if (T == 0) x.o = nullptr;  // only the state passes through
+    err = enter_segments(x, f, seg, st);
+    if (err == hipSuccess) err = launch_linear_walk(x, st);
+  };
   if (bh > 0) {
-    if (T > 0) {  // the state entering every chunk
-      LinearArgs s = w;
-      s.k = k; s.v = v; s.S_in = S_in; s.ckpt = S;
-      err = enter_segments(s, l.f, seg, st);
-      if (err == hipSuccess) err = launch_linear_walk(s, st);
+    // dv, and the gradient of the entry state
+    LinearArgs x = w;
+    x.q = k; x.k = q; x.v = d_o; x.dk = dk_dim; x.dv = dv_dim; x.o = dv; x.reverse = true;
+    x.S_in = dS_out; x.S_out = dS_in;
+    if (T > 0 || dS_in) walk(x, l.fv);
+    if (err == hipSuccess && T > 0) {  // dq, and the states
+      LinearArgs y = w;
+      y.q = d_o; y.k = v; y.v = k; y.dk = dv_dim; y.dv = dk_dim; y.o = dq;
+      y.S_in = S_in; y.state_tr = true; y.dot = q; y.x = xq;
+      walk(y, l.fk);
     }
-    if (err == hipSuccess) {  // its gradient leaving every chunk, and at the start
-      LinearArgs r = w;
-      r.k = q; r.v = d_o; r.S_in = dS_out; r.ckpt = T > 0 ? R : nullptr; r.S_out = dS_in; r.reverse = true;
-      err = enter_segments(r, l.f, seg, st);
-      if (err == hipSuccess) err = launch_linear_walk(r, st);
+    if (err == hipSuccess && T > 0) {  // dk, and the states' products with their gradients
+      LinearArgs y = w;
+      y.q = v; y.k = d_o; y.v = q; y.dk = dv_dim; y.dv = dk_dim; y.o = dk; y.reverse = true;
+      y.S_in = dS_out; y.state_tr = true; y.dot = k; y.x = xk;
+      walk(y, l.fk);
     }
     if (err == hipSuccess && T > 0)
-      err = launch_linear_bwd(LinearBwdArgs{q, k, v, d_o, g, S, R, dq, dk, dv, dgt, B, T, H, dk_dim, dv_dim, scale,
-                                            bf16, grad_dtype == KDA_BF16, g_per_head != 0}, st);
+      err = launch_linear_dg(LinearDgArgs{xq, xk, bsum, dgt, bh, T, H, dk_dim / 16, linear_chunk(bf16) * kBlockChunks}, st);
   }
   if (err == hipSuccess && g_per_head) err = launch_linear_dg_sum(dgt, dg, int64_t(B) * T, H, st);
   return from_hip(err);
@@ -271,9 +294,9 @@ kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_
                                     static_cast<hipStream_t>(stream)));
 }
 
-size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq) {
-  if (n < 0 || Hq < 0) return 0;
-  return size_t(n) * size_t(Hq) * 4;
+size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq, int Hkv, int d) {
+  if (heads_ok(n, Hq, Hkv, d) != KDA_OK) return 0;
+  return size_t(prompt_bwd_floats(n, Hq, Hkv, d)) * 4;
 }
 
 kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
@@ -286,10 +309,11 @@ kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_
   if (s != KDA_OK || !isfinite(scale)) return KDA_ERR_UNSUPPORTED;
   if (n == 0 || n_seqs == 0) return KDA_OK;
   const int64_t nq = int64_t(n) * Hq, nk = int64_t(n) * Hkv;
-  if ((int64_t(n) + 127) / 128 * Hq > kMaxGrid || (nq + 31) / 32 > kMaxGrid) return KDA_ERR_SHAPE;
+  if ((int64_t(n) + 127) / 128 * Hq > kMaxGrid || (nq + 31) / 32 > kMaxGrid || nk * d / 1024 >= kMaxGrid)
+    return KDA_ERR_SHAPE;
   if (!q || !k || !v || !cu_seqlens || !o || !lse || !d_o || !dq || !dk || !dv || !workspace) return KDA_ERR_NULL;
   if (!all_aligned({q, k, v, o, d_o, dq, dk, dv, workspace}, cu_seqlens, 4) || !aligned(lse, 4)) return KDA_ERR_ALIGN;
-  const int64_t need = nq * 4;
+  const int64_t need = prompt_bwd_floats(n, Hq, Hkv, d) * 4;
   if (workspace_bytes < size_t(need)) return KDA_ERR_WORKSPACE;
   const int64_t e = int64_t(esize(in_dtype)), eg = int64_t(esize(grad_dtype)), eo = int64_t(esize(o_dtype));
   const Range ins[] = {{q, nq * d * e}, {k, nk * d * e}, {v, nk * d * e}, {cu_seqlens, (int64_t(n_seqs) + 1) * 4},
@@ -301,8 +325,9 @@ kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_
     for (const Range& y : outs)
       if (&y != &x && overlap(x, y)) return KDA_ERR_ALIAS;
   }
-  return from_hip(launch_prompt_bwd(PromptBwdArgs{q, k, v, o, d_o, lse, cu_seqlens, static_cast<float*>(workspace), dq,
-                                                  dk, dv, n, n_seqs, Hq, Hkv, d, scale, in_dtype == KDA_BF16,
+  return from_hip(launch_prompt_bwd(PromptBwdArgs{q, k, v, o, d_o, lse, cu_seqlens, static_cast<float*>(workspace),
+                                                  static_cast<float*>(workspace) + align4(nq), dq, dk, dv, n, n_seqs,
+                                                  Hq, Hkv, d, prompt_bwd_parts(n, Hq, Hkv), scale, in_dtype == KDA_BF16,
                                                   o_dtype == KDA_BF16, grad_dtype == KDA_BF16},
                                     static_cast<hipStream_t>(stream)));
 }

@@ -12,45 +12,52 @@ namespace kda {
 // Tokens of a chunk: the fp32 kernels' tiles of 64 tokens would not fit the LDS.
 __host__ __device__ constexpr int linear_chunk(bool bf16) { return bf16 ? 64 : 32; }
 
+// Chunks between the states that the backward keeps for dg.
+constexpr int kBlockChunks = 8;
+
+// A walk over the chunks (kda_linear_walk.hpp); q, k, v are roles there: dk is q's and k's size, dv v's.
 struct LinearArgs {
   const void *q, *k, *v;  // [B, T, H, d]
   const float* g;         // [B, T, H], or [H] when g_head
   const float* S_in;      // entry states (see S_in_seg), or nullptr
   void* o;                // [B, T, H, dv]; nullptr: no outputs
   float* S_out;           // [B, H, nseg, dk, dv] (S_out_seg) or [B, H, dk, dv] of the last segment, or nullptr
-  float* ckpt;            // [B, H, chunks, dk, dv]: the state entering each chunk, or nullptr
   int B, T, H, dk, dv;
   float scale;
   bool in_bf16, out_bf16, g_head;
-  int nseg = 1, seg_chunks = 0;  // segments of a sequence, chunks of each
+  bool reverse = false;           // from the last chunk to the first
+  bool state_tr = false;          // S_in (not a segment's) is [B, H, dv, dk]
+  int nseg = 1, seg_chunks = 0;   // segments of a sequence, chunks of each
   bool S_in_seg = false, S_out_seg = false;
-  float* seg_decay = nullptr;  // [B, H, nseg]: each segment's total decay (written with S_out_seg)
-  // the backward's state: walks the chunks from the last to the first, adding
-  // scale e^G q do^T (k = q, v = do), segment 0 being the sequence's last
-  bool reverse = false;
+  float* seg_decay = nullptr;     // [B, H, nseg]: each segment's total decay (written with S_out_seg)
+  // For dg: the outputs' dot products with `dot` ([B, T, H, dv]) into x [dv / 16, B, H, T]; a forward walk
+  // keeps its states every kBlockChunks chunks in ckpt [B, H, blocks + 1, dk dv], a reverse walk
+  // multiplies its own with them into bsum [B, H, blocks, dv / 16].
+  const void* dot = nullptr;
+  float *x = nullptr, *ckpt = nullptr, *bsum = nullptr;
 };
+hipError_t launch_linear_fwd_bf16(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_fwd_f32(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_rev_bf16(const LinearArgs& a, hipStream_t st);
+hipError_t launch_linear_rev_f32(const LinearArgs& a, hipStream_t st);
 hipError_t launch_linear_walk(const LinearArgs& a, hipStream_t st);
 
-// E_0 = S_in (or 0), E_{p+1} = decay_p E_p + St_p over a sequence's segments.
 struct LinearScanArgs {
-  const float *S_in, *St, *decay;  // [BH, n] or nullptr, [BH, nseg, n], [BH, nseg]
-  float* E;                        // [BH, nseg, n]
+  const float *S_in, *St, *decay;  // [BH, dk dv] or nullptr, [BH, nseg, dk dv], [BH, nseg]
+  float* E;                        // [BH, nseg, dk dv]
   int64_t BH;
-  int nseg, n;
+  int nseg, dk, dv;
+  bool state_tr;  // S_in is [BH, dv, dk]
 };
 hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t st);
 
-struct LinearBwdArgs {
-  const void *q, *k, *v, *d_o;
-  const float* g;
-  const float *S, *R;  // [B, H, chunks, dk, dv]: the state entering, and the gradient leaving, each chunk
-  void *dq, *dk_, *dv_;
-  float* dg;  // [B, T, H]
-  int B, T, H, dk, dv;
-  float scale;
-  bool in_bf16, grad_bf16, g_head;
+struct LinearDgArgs {
+  const float *xq, *xk, *bsum;  // [parts, BH, T], [BH, blocks, parts]
+  float* dg;                    // [B, T, H]
+  int64_t BH;
+  int T, H, parts, block;       // block: tokens, at most 512
 };
-hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t st);
+hipError_t launch_linear_dg(const LinearDgArgs& a, hipStream_t st);
 // dg [H] = sums of x [B, T, H] over batch and tokens
 hipError_t launch_linear_dg_sum(const float* x, float* dg, int64_t rows, int H, hipStream_t st);
 
@@ -83,12 +90,14 @@ struct PromptBwdArgs {
   const void *q, *k, *v, *o, *d_o;
   const float* lse;
   const int* cu;
-  float* D;  // [n, Hq] scratch
+  float* D;     // [n, Hq] scratch
+  float* part;  // [parts, 2, n, Hkv, d] scratch when parts > 1
   void *dq, *dk, *dv;
-  int n, nseq, Hq, Hkv, d;
+  int n, nseq, Hq, Hkv, d, parts;
   float scale;
   bool in_bf16, o_bf16, grad_bf16;  // d_o is in the inputs' type
 };
+int prompt_bwd_parts(int n, int Hq, int Hkv);
 hipError_t launch_prompt_bwd(const PromptBwdArgs& a, hipStream_t st);
 
 // ---- attention over a paged cache in 8 bits -------------------------------------------

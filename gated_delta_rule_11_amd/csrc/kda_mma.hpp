@@ -92,71 +92,135 @@ __device__ __forceinline__ typename Op<T>::frag frag_of(const f32x16& c, int s) 
   return Op<T>::pack(f);
 }
 
-// A tile of rows of COLS elements in LDS.  Each row's 16-byte chunks are permuted by the
-// row's number, so that reads of one chunk from 8 or 16 consecutive rows, and transposing
-// reads of 4 rows by 16 columns, spread over the banks.
+// A tile of rows of COLS elements in LDS, aligned to its rows.  Each row's 16-byte chunks are
+// permuted by the row's number, so that reads of one chunk from 8 or 16 consecutive rows, and
+// transposing reads of 4 rows by 16 columns, spread over the banks.
+//
+// The permutation is an exclusive or, and so are the steps from one fragment of a lane to the next:
+// a lane keeps one byte offset per kind of read (the b_* functions), and a fragment's address is
+// that, plus the tile's, xor a constant, plus a constant that fits the instruction.  (Written
+// as offsets of (row, column) the compiler kept an address register for every fragment.)
 template <typename T, int COLS>
 struct Tile {
-  static constexpr int EPC = 16 / int(sizeof(T));  // elements of a chunk
-  static constexpr int CH = COLS / EPC;            // chunks of a row
+  static constexpr int EPC = 16 / int(sizeof(T));   // elements of a chunk
+  static constexpr int CH = COLS / EPC;             // chunks of a row
+  static constexpr int ROWB = COLS * int(sizeof(T));  // bytes of a row
+  static constexpr bool B16 = sizeof(T) == 2;
   static_assert(COLS % EPC == 0 && (CH & (CH - 1)) == 0 && CH >= 4, "rows of a power of two of chunks");
-  __device__ __forceinline__ static int swz(int row) {
-    if constexpr (CH >= 16) return ((row << 1) & 14) | ((row >> 3) & 1);
-    else return row & (CH - 1);
+  typedef typename Op<T>::frag F;
+  __device__ __forceinline__ static constexpr int swz(int row) {
+    return CH >= 16 ? (((row << 1) & 14) | ((row >> 3) & 1)) : (row & (CH - 1));
   }
   // element offset of (row, col); `col` a multiple of 4 keeps 4 elements together
   __device__ __forceinline__ static int off(int row, int col) {
     return row * COLS + (((col / EPC) ^ swz(row)) * EPC) + col % EPC;
   }
-  // columns col .. col + 7 of a row (col a multiple of 8)
-  __device__ __forceinline__ static typename Op<T>::frag row8(const T* t, int row, int col) {
-    if constexpr (sizeof(T) == 2) {
-      return Op<T>::load(t + off(row, col));
+  template <typename V>
+  __device__ __forceinline__ static V rd(uint32_t a) {
+    return *(const __attribute__((address_space(3))) V*)(uintptr_t)a;
+  }
+  __device__ __forceinline__ static uint32_t at(const T* t) {
+    return uint32_t(uintptr_t(t));  // the low half of a generic pointer into LDS is the LDS offset
+  }
+  __device__ __forceinline__ static bf16x4 tr(uint32_t a) {
+    typedef s16x4 __attribute__((address_space(3)))* lds_ptr;
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)a));
+  }
+
+  // 32x32: row 32 j + lane % 32, columns 16 kk + 8 (lane / 32) .. + 7
+  __device__ __forceinline__ static uint32_t b_row8_32(int lane) {
+    const int r = lane & 31, h = lane >> 5;
+    return r * ROWB + (((B16 ? h : 2 * h) ^ swz(r)) << 4);
+  }
+  __device__ __forceinline__ static F row8_32(uint32_t b, int j, int kk) {
+    if constexpr (B16) {
+      return rd<bf16x8>((b ^ (kk << 5)) + 32 * j * ROWB);
     } else {
-      return Op<T>::join(*reinterpret_cast<const f32x4*>(t + off(row, col)),
-                         *reinterpret_cast<const f32x4*>(t + off(row, col + 4)));
+      return Op<T>::join(rd<f32x4>((b ^ (kk << 6)) + 32 * j * ROWB), rd<f32x4>((b ^ ((kk << 6) | 16)) + 32 * j * ROWB));
     }
   }
-  // columns a .. a + 3 and b .. b + 3 of a row
-  __device__ __forceinline__ static typename Op<T>::frag row44(const T* t, int row, int a, int b) {
-    if constexpr (sizeof(T) == 2) {
-      return Op<T>::join(*reinterpret_cast<const bf16x4*>(t + off(row, a)),
-                         *reinterpret_cast<const bf16x4*>(t + off(row, b)));
+  // 32x32, summing over rows in a result's order: rows r0 + 4 (lane / 32) .. + 3 and those + 8
+  // (r0 a multiple of 16), column 32 i + lane % 32.  With bf16 by two transposing reads
+  // (ds_read_b64_tr_b16): 16 lanes fetch 4 rows of 16 columns, 4 columns each, and lane i of
+  // them receives column i.
+  __device__ __forceinline__ static uint32_t b_col44_32(int lane) {
+    const int h = lane >> 5;
+    if constexpr (B16) {
+      const int r = 4 * h + ((lane & 15) >> 2), c = (lane & 16) + 4 * (lane & 3);
+      return r * ROWB + (((c >> 3) ^ swz(r)) << 4) + 2 * (c & 7);
     } else {
-      return Op<T>::join(*reinterpret_cast<const f32x4*>(t + off(row, a)),
-                         *reinterpret_cast<const f32x4*>(t + off(row, b)));
+      const int c = lane & 31;
+      return 4 * h * ROWB + (((c >> 2) ^ swz(4 * h)) << 4) + 4 * (c & 3);
     }
   }
-  // rows a .. a + 3 and b .. b + 3 of column c0 + lane % 32 (c0 a multiple of 32).  a and b may
-  // differ between the two halves of the wavefront.  With bf16 by two transposing reads
-  // (ds_read_b64_tr_b16): 16 lanes fetch 4 rows of 16 columns, 4 columns each, and lane i of them
-  // receives column i.
-  __device__ __forceinline__ static typename Op<T>::frag col44(const T* t, int a, int b, int c0, int lane) {
-    if constexpr (sizeof(T) == 2) {
-      typedef s16x4 __attribute__((address_space(3)))* lds_ptr;
-      const int r = (lane & 15) >> 2, c = c0 + (lane & 16) + 4 * (lane & 3);
-      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + off(a + r, c)));
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + off(b + r, c)));
-      return Op<T>::join(__builtin_bit_cast(bf16x4, x), __builtin_bit_cast(bf16x4, y));
+  __device__ __forceinline__ static F col44_32(uint32_t b, int r0, int i) {
+    if constexpr (B16) {
+      return Op<T>::join(tr((b ^ (i << 6)) + r0 * ROWB), tr((b ^ ((i << 6) ^ (swz(8) << 4))) + (r0 + 8) * ROWB));
     } else {
-      f32x8 f;
+      F f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = t[off(j < 4 ? a + j : b + j - 4, c0 + (lane & 31))];
+      for (int j = 0; j < 8; ++j) {
+        const int x = (j & 3) + 8 * (j >> 2);
+        f[j] = rd<float>((b ^ ((i << 7) ^ (swz(x) << 4))) + (r0 + x) * ROWB);
+      }
       return f;
     }
   }
+
+  // 16x16: row 16 t + lane % 16, columns 32 kk + 8 (lane / 16) .. + 7
+  __device__ __forceinline__ static uint32_t b_row8_16(int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    return r * ROWB + (((B16 ? g : 2 * g) ^ swz(r)) << 4);
+  }
+  __device__ __forceinline__ static F row8_16(uint32_t b, int t, int kk) {
+    if constexpr (B16) {
+      return rd<bf16x8>((b ^ (kk << 6)) + 16 * t * ROWB);
+    } else {
+      return Op<T>::join(rd<f32x4>((b ^ (kk << 7)) + 16 * t * ROWB), rd<f32x4>((b ^ ((kk << 7) | 16)) + 16 * t * ROWB));
+    }
+  }
+  // 16x16, the columns in the order of two results' rows: 32 kk + 4 (lane / 16) .. + 3 and those + 16
+  __device__ __forceinline__ static uint32_t b_row44_16(int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    return r * ROWB + (B16 ? ((((g >> 1) ^ swz(r)) << 4) + 8 * (g & 1)) : ((g ^ swz(r)) << 4));
+  }
+  __device__ __forceinline__ static F row44_16(uint32_t b, int t, int kk) {
+    if constexpr (B16) {
+      return Op<T>::join(rd<bf16x4>((b ^ (kk << 6)) + 16 * t * ROWB), rd<bf16x4>((b ^ ((kk << 6) | 32)) + 16 * t * ROWB));
+    } else {
+      return Op<T>::join(rd<f32x4>((b ^ (kk << 7)) + 16 * t * ROWB), rd<f32x4>((b ^ ((kk << 7) | 64)) + 16 * t * ROWB));
+    }
+  }
+  // 16x16, summing over rows: rows 32 u + 8 (lane / 16) .. + 7, column 16 t + lane % 16
+  __device__ __forceinline__ static uint32_t b_col8_16(int lane) {
+    const int g = lane >> 4;
+    if constexpr (B16) {
+      const int r = 8 * g + ((lane & 15) >> 2), c = 4 * (lane & 3);
+      return r * ROWB + (((c >> 3) ^ swz(r)) << 4) + 2 * (c & 7);
+    } else {
+      const int c = lane & 15;
+      return 8 * g * ROWB + (((c >> 2) ^ swz(8 * g)) << 4) + 4 * (c & 3);
+    }
+  }
+  __device__ __forceinline__ static F col8_16(uint32_t b, int u, int t) {
+    if constexpr (B16) {
+      return Op<T>::join(tr((b ^ (t << 5)) + 32 * u * ROWB), tr((b ^ ((t << 5) ^ (swz(4) << 4))) + (32 * u + 4) * ROWB));
+    } else {
+      F f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = rd<float>((b ^ ((t << 6) ^ (swz(j) << 4))) + (32 * u + j) * ROWB);
+      return f;
+    }
+  }
+
   // four consecutive columns of a row as fp32
   __device__ __forceinline__ static f32x4 get4(const T* t, int row, int col) {
-    if constexpr (sizeof(T) == 2)
-      return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(t + off(row, col)), f32x4);
-    else
-      return *reinterpret_cast<const f32x4*>(t + off(row, col));
+    if constexpr (B16) return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(t + off(row, col)), f32x4);
+    else return *reinterpret_cast<const f32x4*>(t + off(row, col));
   }
   __device__ __forceinline__ static void put4(T* t, int row, int col, f32x4 x) {
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<bf16x4*>(t + off(row, col)) = __builtin_convertvector(x, bf16x4);
-    else
-      *reinterpret_cast<f32x4*>(t + off(row, col)) = x;
+    if constexpr (B16) *reinterpret_cast<bf16x4*>(t + off(row, col)) = __builtin_convertvector(x, bf16x4);
+    else *reinterpret_cast<f32x4*>(t + off(row, col)) = x;
   }
 };
 
@@ -207,10 +271,47 @@ struct Stage {
 
 // Dispatch of workgroups to consecutive work items per XCD: the hardware deals workgroups to
 // the eight XCDs in turn; the returned index gives each XCD one contiguous run of items, so that
-// neighbours (the tiles of one head) share an L2.
+// neighbours share an L2.
 __device__ __forceinline__ int xcd_order(int id, int n) {
   const int x = id & 7, per = n >> 3, rem = n & 7;
   return x * per + (x < rem ? x : rem) + (id >> 3);
 }
+
+// The item of a launch of `n` tiles for each of `heads` heads: tiles in the outer order, so that
+// the longest, given first, start first on every XCD; where the heads divide by eight, each XCD
+// keeps to its own consecutive heads.
+struct HeadTile {
+  int head, tile;
+};
+__device__ __forceinline__ HeadTile head_tile(int id, int heads) {
+  const int h = id % heads;
+  return {(heads & 7) == 0 ? (h & 7) * (heads >> 3) + (h >> 3) : h, id / heads};
+}
+
+// Copies from memory straight into LDS, 16 (4) bytes a lane: the wavefront's lanes land behind one
+// another at `lds`, whatever their source addresses (inactive lanes write nothing).  Written as
+// assembly without outputs, since the compiler, which cannot tell which LDS reads such a copy may
+// meet, would wait for it before the next one; copies_landed() is the wait that they need.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return uint32_t(uintptr_t(p));  // the low half of a generic pointer into LDS
+}
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_copy16(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_copy4(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+__device__ __forceinline__ void copies_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// A barrier for LDS contents: waits for this wavefront's LDS accesses, not for its stores to memory.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 }  // namespace kda

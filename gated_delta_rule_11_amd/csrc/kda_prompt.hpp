@@ -32,31 +32,32 @@ __device__ __forceinline__ int rows_used(const int* cu, int nseq, int n) {
   return e < 0 ? 0 : (e > n ? n : e);
 }
 
-// ROWS rows of D elements copied straight from memory into a Tile (16 bytes a lane,
-// global_load_lds_dwordx4: no registers in between).  The LDS side of such a copy is one run of
-// 1024 bytes per wavefront, so each lane picks the source chunk that belongs at its place.  Rows
-// at or past `last` repeat row `last - 1`: no row outside [0, last) is read.
+// ROWS rows of D elements copied from memory into a Tile, without registers in between.  The LDS
+// side of such a copy is one run of 1024 bytes per wavefront, so each lane picks the source chunk
+// that belongs at its place.  Rows at or past `last` repeat row `last - 1`: no row outside
+// [0, last) is read.
 template <typename T, int ROWS, int D, int NW>
 __device__ __forceinline__ void copy_rows(T* tile, const T* base, int64_t stride, int row0, int last, int wave,
                                           int lane) {
   typedef Tile<T, D> L;
-  constexpr int PER = 64 / L::CH > 0 ? 64 / L::CH : 1;  // rows of one wavefront's copy
+  constexpr int PER = 64 / L::CH;  // rows of one wavefront's copy
   static_assert(64 % L::CH == 0 && ROWS % (PER * NW) == 0, "whole copies");
+  // the addresses are formed again at every call: held over a loop they would cost more than they save
+  int lr = wave * PER + lane / L::CH;
+  asm volatile("" : "+v"(lr));
 #pragma unroll
   for (int i = 0; i < ROWS / (PER * NW); ++i) {
-    const int r0 = (i * NW + wave) * PER, r = r0 + lane / L::CH;
+    const int r = i * NW * PER + lr;
     int g = row0 + r;
     g = g < last ? g : last - 1;
-    const T* src = base + g * stride + ((lane % L::CH) ^ L::swz(r)) * L::EPC;
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)(tile + r0 * D), 16, 0, 0);
+    lds_copy16(base + g * stride + ((lane % L::CH) ^ L::swz(r)) * L::EPC, lds_offset(tile + (i * NW + wave) * PER * D));
   }
 }
 
-// Waits for this wavefront's copies; a barrier behind it makes every wavefront's visible.
+// Waits for this wavefront's copies; behind the barrier every wavefront's are there.
 __device__ __forceinline__ void copies_done() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  __syncthreads();
+  copies_landed();
+  lds_barrier();
 }
 
 }  // namespace kda

@@ -52,15 +52,15 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
   constexpr int NK = D / 16, ND = D / 32;
   extern __shared__ __align__(16) unsigned char smem[];
   T* const buf = reinterpret_cast<T*>(smem);                             // [2][Q tile, dO tile]
-  float* const stat = reinterpret_cast<float*>(buf + 2 * 2 * BR * D);    // [2][lse log2 e, D]
+  float* const stat = reinterpret_cast<float*>(buf + 2 * 2 * BR * D);    // [2][lse, D]
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
-  const int kvh = id / ntile, tile = id % ntile;  // keys with the most rows first
-  const int c0 = tile * BM;
+  const HeadTile ht = head_tile(blockIdx.x, a.Hkv * a.parts);
+  const int kvh = ht.head / a.parts, part = ht.head % a.parts;
+  const int c0 = ht.tile * BM;  // keys with the most rows first
   const int used = rows_used(a.cu, a.nseq, a.n);
   if (c0 >= used) return;
-  const int G = a.Hq / a.Hkv;
+  const int GP = a.Hq / (a.Hkv * a.parts), h0 = kvh * (a.Hq / a.Hkv) + part * GP;  // this part's query heads
   const int64_t qst = int64_t(a.Hq) * D, kst = int64_t(a.Hkv) * D;
 
   const int clast = c0 + BM - 1 < used ? c0 + BM - 1 : used - 1;
@@ -85,16 +85,16 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
 #pragma unroll
   for (int i = 0; i < ND; ++i) dk[i] = dv[i] = zero16();
 
-  const int nt = (hi - c0 + BR - 1) / BR, steps = nt * G;
+  const uint32_t brow = TD::b_row8_32(lane), bcol = TD::b_col44_32(lane);
+  const int nt = (hi - c0 + BR - 1) / BR, steps = nt * GP;
   auto fetch = [&](int t) {
-    const int head = kvh * G + t / nt, i0 = c0 + (t % nt) * BR;
+    const int head = h0 + t / nt, i0 = c0 + (t % nt) * BR;
     T* qb = buf + (t & 1) * 2 * BR * D;
     copy_rows<T, BR, D, 4>(qb, static_cast<const T*>(a.q) + int64_t(head) * D, qst, i0, hi, wave, lane);
     copy_rows<T, BR, D, 4>(qb + BR * D, static_cast<const T*>(a.d_o) + int64_t(head) * D, qst, i0, hi, wave, lane);
-    if (tid < BR) {
-      const int r = i0 + tid < hi ? i0 + tid : hi - 1;
-      stat[(t & 1) * 2 * BR + tid] = a.lse[int64_t(r) * a.Hq + head] * kLog2e;
-      stat[(t & 1) * 2 * BR + BR + tid] = a.D[int64_t(r) * a.Hq + head];
+    if (wave < 2) {  // lse by the first wavefront, D by the second
+      const int r = i0 + lane < hi ? i0 + lane : hi - 1;
+      lds_copy4((wave ? a.D : a.lse) + int64_t(r) * a.Hq + head, lds_offset(stat + (t & 1) * 2 * BR + wave * BR));
     }
   };
   fetch(0);
@@ -105,8 +105,9 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
     const T* Os = Qs + BR * D;
     const float* ls = stat + (t & 1) * 2 * BR;
     const float* Ds = ls + BR;
+    const uint32_t qrow = TD::at(Qs) + brow, orow = TD::at(Os) + brow, qcol = TD::at(Qs) + bcol, ocol = TD::at(Os) + bcol;
     const int i0 = c0 + (t % nt) * BR;
-#pragma unroll 1
+#pragma unroll
     for (int sub = 0; sub < BR / 32; ++sub) {
       const int s0 = i0 + 32 * sub;
       // some row at or past the wavefront's first key, before its last key's end
@@ -114,8 +115,8 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
-        s = O::mma32(TD::row8(Qs, 32 * sub + l32, 16 * kk + 8 * h2), kf[kk], s);
-        dp = O::mma32(TD::row8(Os, 32 * sub + l32, 16 * kk + 8 * h2), vf[kk], dp);
+        s = O::mma32(TD::row8_32(qrow, sub, kk), kf[kk], s);
+        dp = O::mma32(TD::row8_32(orow, sub, kk), vf[kk], dp);
       }
       const bool whole = s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi;
 #pragma unroll
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
         for (int j = 0; j < 4; ++j) {
           const int i = i0 + rr + j, e = 4 * r4 + j;
           const bool in = whole || (i >= kj && i < end && i < hi);
-          const float p = in ? fast_exp2(s[e] * c - l4[j]) : 0.f;
+          const float p = in ? fast_exp2(s[e] * c - l4[j] * kLog2e) : 0.f;
           s[e] = p;
           dp[e] = in ? p * (dp[e] - D4[j]) : 0.f;
         }
@@ -134,18 +135,19 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const F pf = frag_of<T>(s, ks), df = frag_of<T>(dp, ks);
-        const int rr = 32 * sub + 16 * ks + 4 * h2;
+        const int rr = 32 * sub + 16 * ks;
 #pragma unroll
         for (int i = 0; i < ND; ++i) {
-          dv[i] = O::mma32(TD::col44(Os, rr, rr + 8, 32 * i, lane), pf, dv[i]);
-          dk[i] = O::mma32(TD::col44(Qs, rr, rr + 8, 32 * i, lane), df, dk[i]);
+          dv[i] = O::mma32(TD::col44_32(ocol, rr, i), pf, dv[i]);
+          dk[i] = O::mma32(TD::col44_32(qcol, rr, i), df, dk[i]);
         }
       }
     }
   }
   if (kj < used) {
-    TG* kp = static_cast<TG*>(a.dk) + int64_t(kj) * kst + int64_t(kvh) * D;
-    TG* vp = static_cast<TG*>(a.dv) + int64_t(kj) * kst + int64_t(kvh) * D;
+    const int64_t at = int64_t(kj) * kst + int64_t(kvh) * D;
+    TG* kp = (a.parts == 1 ? static_cast<TG*>(a.dk) : reinterpret_cast<TG*>(a.part + (2 * part) * a.n * kst)) + at;
+    TG* vp = (a.parts == 1 ? static_cast<TG*>(a.dv) : reinterpret_cast<TG*>(a.part + (2 * part + 1) * a.n * kst)) + at;
 #pragma unroll
     for (int i = 0; i < ND; ++i)
 #pragma unroll
@@ -176,8 +178,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   T* const buf = reinterpret_cast<T*>(smem);  // [1 or 2][K tile, V tile]
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
-  const int head = id / ntile, tile = ntile - 1 - id % ntile;
+  const HeadTile ht = head_tile(blockIdx.x, a.Hq);
+  const int head = ht.head, tile = ntile - 1 - ht.tile;
   const int r0 = tile * BM;
   const int used = rows_used(a.cu, a.nseq, a.n);
   if (r0 >= used) return;
@@ -210,6 +212,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
 #pragma unroll
   for (int i = 0; i < ND; ++i) dq[i] = zero16();
 
+  const uint32_t brow = TD::b_row8_32(lane), bcol = TD::b_col44_32(lane);
   const int nt = (hi - lo + BN - 1) / BN;
   auto fetch = [&](int t) {
     T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
@@ -222,16 +225,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
     if (DB && t + 1 < nt) fetch(t + 1);
     const T* Ks = buf + (DB ? (t & 1) * 2 * BN * D : 0);
     const T* Vs = Ks + BN * D;
+    const uint32_t krow = TD::at(Ks) + brow, vrow = TD::at(Vs) + brow, kcol = TD::at(Ks) + bcol;
     const int k0 = lo + t * BN;
-#pragma unroll 1
+#pragma unroll
     for (int j = 0; j < BN / 32; ++j) {
       const int s0 = k0 + 32 * j;
       if (wlast < w0 || s0 > wlast || s0 + 32 <= smin) continue;
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
-        s = O::mma32(TD::row8(Ks, 32 * j + l32, 16 * kk + 8 * h2), qf[kk], s);
-        dp = O::mma32(TD::row8(Vs, 32 * j + l32, 16 * kk + 8 * h2), of[kk], dp);
+        s = O::mma32(TD::row8_32(krow, j, kk), qf[kk], s);
+        dp = O::mma32(TD::row8_32(vrow, j, kk), of[kk], dp);
       }
       const bool whole = s0 + 31 <= w0 && s0 >= smax;
 #pragma unroll
@@ -244,9 +248,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const F df = frag_of<T>(dp, ks);
-        const int kr = 32 * j + 16 * ks + 4 * h2;
 #pragma unroll
-        for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44(Ks, kr, kr + 8, 32 * i, lane), df, dq[i]);
+        for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44_32(kcol, 32 * j + 16 * ks, i), df, dq[i]);
       }
     }
     if (!DB) {
@@ -268,6 +271,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   }
 }
 
+// dk and dv from the parts of their groups' heads, in order.
+template <typename TG>
+__global__ __launch_bounds__(256) void prompt_join_kernel(const PromptBwdArgs a, int64_t count) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= rows_used(a.cu, a.nseq, a.n) * int64_t(a.Hkv) * a.d) return;
+  f32x4 x = {0, 0, 0, 0}, y = x;
+  for (int p = 0; p < a.parts; ++p) {
+    x += *reinterpret_cast<const f32x4*>(a.part + 2 * p * count + i);
+    y += *reinterpret_cast<const f32x4*>(a.part + (2 * p + 1) * count + i);
+  }
+  store4(static_cast<TG*>(a.dk) + i, x);
+  store4(static_cast<TG*>(a.dv) + i, y);
+}
+
 template <typename TO>
 hipError_t launch_dot_o(const PromptBwdArgs& a, hipStream_t st) {
   const int64_t rows = int64_t(a.n) * a.Hq;
@@ -280,21 +297,35 @@ hipError_t launch_dot_o(const PromptBwdArgs& a, hipStream_t st) {
 }
 
 template <typename T, typename TG, int D>
+hipError_t launch_dkv(const PromptBwdArgs& a, int ntile, hipStream_t st) {
+  auto kern = prompt_dkv_kernel<T, TG, D>;
+  constexpr size_t lds = kv_lds<T, D>();
+  static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), int(lds), done);
+  if (e != hipSuccess) return e;
+  kern<<<dim3(uint32_t(int64_t(ntile) * a.Hkv * a.parts)), 256, lds, st>>>(a, ntile);
+  return hipGetLastError();
+}
+
+template <typename T, typename TG, int D>
 hipError_t launch(const PromptBwdArgs& a, hipStream_t st) {
-  auto kkv = prompt_dkv_kernel<T, TG, D>;
   auto kq = prompt_dq_kernel<T, TG, D>;
-  constexpr size_t l1 = kv_lds<T, D>(), l2 = q_lds<T, D>();
-  static_assert(l1 <= 160 * 1024 && l2 <= 160 * 1024, "LDS of a compute unit");
-  static std::atomic<uint64_t> done1{0}, done2{0};
-  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kkv), int(l1), done1);
-  if (e == hipSuccess) e = set_lds_limit(reinterpret_cast<const void*>(kq), int(l2), done2);
+  constexpr size_t lds = q_lds<T, D>();
+  static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kq), int(lds), done);
   if (e == hipSuccess) e = a.o_bf16 ? launch_dot_o<bf16_t>(a, st) : launch_dot_o<float>(a, st);
   if (e != hipSuccess) return e;
   const int ntile = (a.n + BM - 1) / BM;
-  kkv<<<dim3(uint32_t(int64_t(ntile) * a.Hkv)), 256, l1, st>>>(a, ntile);
-  e = hipGetLastError();
+  e = a.parts == 1 ? launch_dkv<T, TG, D>(a, ntile, st) : launch_dkv<T, float, D>(a, ntile, st);
+  if (e == hipSuccess && a.parts > 1) {
+    const int64_t count = int64_t(a.n) * a.Hkv * a.d;
+    prompt_join_kernel<TG><<<dim3(uint32_t((count / 4 + 255) / 256)), 256, 0, st>>>(a, count);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return e;
-  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, l2, st>>>(a, ntile);
+  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, lds, st>>>(a, ntile);
   return hipGetLastError();
 }
 
@@ -304,6 +335,18 @@ hipError_t launch_g(const PromptBwdArgs& a, hipStream_t st) {
 }
 
 }  // namespace
+
+// Parts that the query heads of a group are cut into for dk and dv.  The key tiles of a long
+// sequence differ in length by as much as its length, so the GPU wants several times as many
+// workgroups as compute units; each part beyond the first writes and rereads fp32 sums.
+int prompt_bwd_parts(int n, int Hq, int Hkv) {
+  const int64_t units = (int64_t(n) + BM - 1) / BM * Hkv;
+  const int G = Hq / Hkv;
+  int parts = 1;
+  for (int p = 2; p <= G; ++p)
+    if (G % p == 0 && units * parts < 1024) parts = p;
+  return parts;
+}
 
 hipError_t launch_prompt_bwd(const PromptBwdArgs& a, hipStream_t st) {
   if (a.in_bf16) return a.d == 64 ? launch_g<bf16_t, 64>(a, st) : launch_g<bf16_t, 128>(a, st);

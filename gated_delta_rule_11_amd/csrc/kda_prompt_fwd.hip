@@ -76,8 +76,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
   T* const buf = reinterpret_cast<T*>(smem);  // [2][K tile, V tile]
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
-  const int head = id / ntile, tile = ntile - 1 - id % ntile;  // long rows first
+  const HeadTile ht = head_tile(blockIdx.x, a.Hq);
+  const int head = ht.head, tile = ntile - 1 - ht.tile;  // long rows first
   const int r0 = tile * BM;
   const int used = rows_used(a.cu, a.nseq, a.n);
   if (r0 >= used) return;
@@ -111,6 +111,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
 #pragma unroll
   for (int i = 0; i < ND; ++i) acc[i] = zero16();
   float m = -INFINITY, l = 0.f;
+  int bad_lo = hi, bad_hi = 0;  // keys of masked tiles with non-finite values
+  const uint32_t krow = TD::b_row8_32(lane), vcol = TD::b_col44_32(lane);
 
   const int nt = (hi - lo + BN - 1) / BN;
   auto fetch = [&](int t) {
@@ -124,6 +126,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
     if (t + 1 < nt) fetch(t + 1);
     const T* Ks = buf + (t & 1) * 2 * BN * D;
     const T* Vs = Ks + BN * D;
+    const uint32_t kb = TD::at(Ks) + krow, vb = TD::at(Vs) + vcol;
     const int k0 = lo + t * BN;
     if (wlast >= w0 && k0 <= wlast && k0 + BN > smin) {
       f32x16 s[2];
@@ -131,7 +134,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
       for (int j = 0; j < 2; ++j) {
         s[j] = zero16();
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) s[j] = O::mma32(TD::row8(Ks, 32 * j + l32, 16 * kk + 8 * h2), qf[kk], s[j]);
+        for (int kk = 0; kk < NK; ++kk) s[j] = O::mma32(TD::row8_32(kb, j, kk), qf[kk], s[j]);
       }
       const bool masked = !(k0 + BN - 1 <= w0 && k0 >= smax);
       if (masked) {
@@ -170,35 +173,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
         }
       }
       // A masked probability is zero, but zero times a NaN or infinity is not: where a tile is
-      // masked and holds such values, they leave the product and reach only the rows that see them.
+      // masked and holds such values, they leave the product, and after the loop reach the rows that
+      // see them.
       if (masked) {
         Finite<T> fin;
 #pragma unroll
         for (int e = 0; e < 4 * ND; ++e)
-          fin.see(TD::col44(Vs, 16 * (e & 3) + 4 * h2, 16 * (e & 3) + 4 * h2 + 8, 32 * (e >> 2), lane));
+          fin.see(TD::col44_32(vb, 16 * (e & 3), e >> 2));
         if (__any(!fin.all())) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
               const F pf = frag_of<T>(s[j], ks);
-              const int kr = 32 * j + 16 * ks + 4 * h2;
 #pragma unroll
               for (int i = 0; i < ND; ++i)
-                acc[i] = O::mma32(Finite<T>::only(TD::col44(Vs, kr, kr + 8, 32 * i, lane)), pf, acc[i]);
+                acc[i] = O::mma32(Finite<T>::only(TD::col44_32(vb, 32 * j + 16 * ks, i)), pf, acc[i]);
             }
-          for (int key = 0; key < BN; ++key) {
-            const bool seen = k0 + key <= qi && k0 + key >= start;
-#pragma unroll
-            for (int i = 0; i < ND; ++i)
-#pragma unroll
-              for (int r4 = 0; r4 < 4; ++r4) {
-                const f32x4 x = TD::get4(Vs, key, 32 * i + 8 * r4 + 4 * h2);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (seen && !(fabsf(x[e]) < INFINITY)) acc[i][4 * r4 + e] += x[e];
-              }
-          }
+          bad_lo = k0 < bad_lo ? k0 : bad_lo;
+          bad_hi = k0 + BN;
           continue;
         }
       }
@@ -207,11 +200,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           const F pf = frag_of<T>(s[j], ks);
-          const int kr = 32 * j + 16 * ks + 4 * h2;
 #pragma unroll
-          for (int i = 0; i < ND; ++i) acc[i] = O::mma32(TD::col44(Vs, kr, kr + 8, 32 * i, lane), pf, acc[i]);
+          for (int i = 0; i < ND; ++i) acc[i] = O::mma32(TD::col44_32(vb, 32 * j + 16 * ks, i), pf, acc[i]);
         }
     }
+  }
+  for (int key = bad_lo; key < bad_hi && key < hi; ++key) {
+    const bool seen = key <= qi && key >= start;
+    const T* row = vp + int64_t(key) * kst + 4 * h2;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = io<T>::load(row, 32 * i + 8 * r4 + e);
+          acc[i][4 * r4 + e] += seen && !(fabsf(x) < INFINITY) ? x : 0.f;
+        }
   }
   l = sum_halves(l);
   if (qi < used) {

@@ -432,7 +432,7 @@ kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_
  * non-finite value in one sequence may reach gradients of its neighbours in
  * the packed buffer.
  */
-size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq);
+size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq, int Hkv, int d);
 kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
                                const void* o, kda_dtype o_dtype, const float* lse, const void* d_o, void* dq, void* dk,
                                void* dv, kda_dtype grad_dtype, int n, int n_seqs, int Hq, int Hkv, int d, float scale,

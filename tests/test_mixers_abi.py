@@ -127,7 +127,8 @@ def test_prompt_aliases_and_workspace(L):  # noqa: F811
     for x in ("dq", "dk", "dv", "ws"):
         for at in (P(0), P(4), P(5), P(6)):
             assert prompt_bwd(L, **{x: at}) == ERR_ALIAS
-    assert prompt_bwd(L, dk=P(9)) == ERR_ALIAS and prompt_bwd(L, wsb=100 * 4 * 4 - 1) == ERR_WORKSPACE
+    assert prompt_bwd(L, dk=P(9)) == ERR_ALIAS and prompt_bwd(L, wsb=L.kda_attn_prompt_bwd_workspace_bytes(100, 4, 2, 64) - 1) == ERR_WORKSPACE
+    assert L.kda_attn_prompt_bwd_workspace_bytes(100, 5, 2, 64) == 0
     assert prompt_bwd(L, gt=2) == ERR_DTYPE
 
 
