@@ -24,9 +24,9 @@
 //
 // One workgroup per (b, h, slice of up to 64 value columns, segment).  Wavefronts 0 .. NSW - 1 each
 // own 16 value columns and hold that dk x 16 block of the state in their accumulators; with
-// outputs, the others (one per 16 tokens of a chunk) form the decayed scores P of the next chunk
-// and copy the one after it into LDS, three chunks in rotation, so that a step has one barrier
-// and both the copies' and the scores' latency pass beside the state's products.  All products are
+// outputs, the others (one per 16 tokens of a chunk) form the decayed scores P of the chunk while
+// the former take S^T q and the update, and copy later chunks into LDS, three in rotation: a copy has
+// two steps to land.  P V and the outputs follow behind a barrier.  All products are
 // 16x16x32 with fp32 accumulation: (S^T q) takes the state straight from the accumulators (their
 // layout is an operand's), the values' transposing reads serve both P V and the update.
 //
@@ -64,9 +64,16 @@ struct WalkShape {
   static constexpr bool PF = OUT == 2 || sizeof(T) == 4;  // P in fp32
   static constexpr int kK = C * DKP * int(sizeof(T)), kV = C * VC * int(sizeof(T)), kP = C * C * (PF ? 4 : 2);
   static constexpr int kG = (4 * C + 4) * 4;  // G hi, G lo, the outputs' and the update's weights, e^{G_C}
-  static constexpr int oQ = 3 * kK, oV = oQ + (OUT ? 3 * kK : 0), oP = oV + 3 * kV, oG = oP + (OUT ? 2 * kP : 0);
-  static constexpr size_t lds = size_t(oG) + 3 * kG;
+  // chunks in rotation: one in use, the others on their way (two, or three where only k and v are)
+  static constexpr int NS = OUT ? 3 : 4;
+  static constexpr int oQ = NS * kK, oV = oQ + (OUT ? NS * kK : 0), oP = oV + NS * kV, oG = oP + (OUT ? kP : 0),
+                       oR = oG + 2 * kG;  // raw log-decays of NS + 1 chunks
+  static constexpr size_t lds = size_t(oR) + (NS + 1) * 64 * 4;
   static_assert(lds <= 160 * 1024, "LDS of a compute unit");
+  // copies that each wavefront issues for a chunk
+  static constexpr int kCopies = (C / (64 / Tile<T, DKP>::CH) + NPW - 1) / NPW * (OUT ? 2 : 1) +
+                                 (C / (64 / Tile<T, VC>::CH) + NPW - 1) / NPW + 1;
+  static_assert(C % (64 / Tile<T, DKP>::CH * NPW) == 0 && C % (64 / Tile<T, VC>::CH * NPW) == 0, "the same for each");
 };
 
 // x as parts of the element type whose sum is x to 8 (16, 24) bits.
@@ -118,15 +125,16 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
   const int n0 = seg * a.seg_chunks, n1 = n0 + a.seg_chunks < nch ? n0 + a.seg_chunks : nch;
   const int64_t tok = b * a.T;  // the sequence's first row
   auto chunk_of = [&](int n) { return REV ? nch - 1 - n : n; };
-  auto Ks = [&](int n) { return reinterpret_cast<T*>(smem + (n % 3) * W::kK); };
-  auto Qs = [&](int n) { return reinterpret_cast<T*>(smem + W::oQ + (n % 3) * W::kK); };
-  auto Vs = [&](int n) { return reinterpret_cast<T*>(smem + W::oV + (n % 3) * W::kV); };
-  auto Ps = [&](int n) { return reinterpret_cast<PT*>(smem + W::oP + (n & 1) * W::kP); };
-  auto gates = [&](int n) { return reinterpret_cast<float*>(smem + W::oG + (n % 3) * W::kG); };
+  auto Ks = [&](int n) { return reinterpret_cast<T*>(smem + (n % W::NS) * W::kK); };
+  auto Qs = [&](int n) { return reinterpret_cast<T*>(smem + W::oQ + (n % W::NS) * W::kK); };
+  auto Vs = [&](int n) { return reinterpret_cast<T*>(smem + W::oV + (n % W::NS) * W::kV); };
+  PT* const P = reinterpret_cast<PT*>(smem + W::oP);
+  auto gates = [&](int n) { return reinterpret_cast<float*>(smem + W::oG + (n & 1) * W::kG); };
+  auto raw = [&](int n) { return reinterpret_cast<float*>(smem + W::oR) + (n % (W::NS + 1)) * 64; };
 
   // key channels 16 .. 31 of a 16-channel head are zero in LDS; the copies leave them alone
   if constexpr (DK < 32) {
-    for (int i = tid * 4; i < (OUT ? 2 : 1) * 3 * W::kK; i += W::NT * 4) *reinterpret_cast<uint32_t*>(smem + i) = 0u;
+    for (int i = tid * 4; i < (OUT ? 2 : 1) * W::NS * W::kK; i += W::NT * 4) *reinterpret_cast<uint32_t*>(smem + i) = 0u;
     __syncthreads();
   }
 
@@ -137,46 +145,65 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
     const T* kp = static_cast<const T*>(a.k) + (tok * a.H + head) * DK;
     const T* qp = OUT ? static_cast<const T*>(a.q) + (tok * a.H + head) * DK : nullptr;
     const T* vp = static_cast<const T*>(a.v) + (tok * a.H + head) * DV + slice * W::DVS;
-    // rows at or past the sequence's end repeat its last row (their weights are zero)
-    auto copy = [&](auto tile_tag, T* tile, const T* base, int64_t stride, int64_t t0, int cols) {
+    // A lane's byte offsets within a chunk's rows, per copy: the same for every chunk but a partial
+    // one, whose rows at or past the sequence's end repeat its last row (their weights are zero).
+    // The lane's chunk of 16 bytes is the one that belongs at its place in the tile.
+    auto rows_of = [&](auto tile_tag, int i, int64_t stride, int last) -> uint32_t {
       using L = decltype(tile_tag);
       constexpr int PER = 64 / L::CH;
-#pragma unroll
-      for (int r0 = 0; r0 < C; r0 += PER * W::NPW) {
-        const int rw = r0 + p * PER;
-        if (rw >= C) break;
-        const int r = rw + lane / L::CH, ch = (lane % L::CH) ^ L::swz(r);
-        int64_t t = t0 + r;
-        t = t < a.T ? t : a.T - 1;
-        if (ch * L::EPC < cols) lds_copy16(base + t * stride + ch * L::EPC, lds_offset(tile + rw * (L::CH * L::EPC)));
-      }
+      const int r = (i * W::NPW + p) * PER + lane / L::CH, ch = (lane % L::CH) ^ L::swz(r);
+      return uint32_t((r < last ? r : last) * stride * int64_t(sizeof(T))) + ch * 16;
     };
+    constexpr int kPerK = C / (64 / TK::CH * W::NPW), kPerV = C / (64 / TV::CH * W::NPW);
+    uint32_t offk[kPerK], offv[kPerV];
+#pragma unroll
+    for (int i = 0; i < kPerK; ++i) offk[i] = rows_of(TK{}, i, kst, C - 1);
+#pragma unroll
+    for (int i = 0; i < kPerV; ++i) offv[i] = rows_of(TV{}, i, vst, C - 1);
+    const float* gp = a.g_head ? a.g + head : a.g + tok * a.H + head;
+    const int64_t gst = a.g_head ? 0 : a.H;
+    auto fetch_gate = [&](int n) {
+      n = n < n1 ? n : n1 - 1;
+      const int64_t t0 = int64_t(chunk_of(n)) * C;
+      const int64_t t = t0 + lane < a.T ? lane : a.T - 1 - t0;
+      lds_copy4(gp + t0 * gst, uint32_t(t * gst * 4), lds_offset(raw(n)));
+    };
+    // chunk n's rows and the next chunk's log-decays: W::kCopies copies of every wavefront, and nothing
+    // else here reads memory, so that a count of copies is what to wait for
     auto fetch = [&](int n) {
       const int64_t t0 = int64_t(chunk_of(n)) * C;
-      copy(TK{}, Ks(n), kp, kst, t0, DK);
-      if constexpr (OUT > 0) copy(TK{}, Qs(n), qp, kst, t0, DK);
-      copy(TV{}, Vs(n), vp, vst, t0, W::DVS);
+      const T *kc = kp + t0 * kst, *qc = OUT ? qp + t0 * kst : nullptr, *vc = vp + t0 * vst;
+      const uint32_t ks = lds_offset(Ks(n)) + p * 1024, qs = lds_offset(Qs(n)) + p * 1024, vs = lds_offset(Vs(n)) + p * 1024;
+      const int last = a.T - t0 < C ? int(a.T - t0) - 1 : C - 1;
+      // in a tile wider than the head, the lanes of the columns that do not exist copy nothing
+      auto copy = [&](auto tile_tag, const T* from, uint32_t off, uint32_t to, int i, int64_t stride, int cols) {
+        using L = decltype(tile_tag);
+        if (last < C - 1) off = rows_of(tile_tag, i, stride, last);
+        bool on = true;
+        if (L::CH * L::EPC != cols) {
+          const int r = (i * W::NPW + p) * (64 / L::CH) + lane / L::CH;
+          on = ((lane % L::CH) ^ L::swz(r)) * L::EPC < cols;
+        }
+        if (on) lds_copy16(from, off, to + i * W::NPW * 1024);
+      };
+#pragma unroll
+      for (int i = 0; i < kPerK; ++i) copy(TK{}, kc, offk[i], ks, i, kst, DK);
+      if constexpr (OUT > 0)
+#pragma unroll
+        for (int i = 0; i < kPerK; ++i) copy(TK{}, qc, offk[i], qs, i, kst, DK);
+#pragma unroll
+      for (int i = 0; i < kPerV; ++i) copy(TV{}, vc, offv[i], vs, i, vst, W::DVS);
+      fetch_gate(n + 1);
     };
     // the gate wavefront has the fewest scores
     const bool gate = p == (REV ? W::NPW - 1 : 0);
-    const float* gp = a.g_head ? a.g + head : a.g + tok * a.H + head;
-    const int64_t gst = a.g_head ? 0 : a.H;
-    auto gate_of = [&](int n) -> float {
-      const int64_t t = int64_t(chunk_of(n)) * C + lane;
-      const float g = (n < n1 && lane < C && t < a.T) ? gp[t * gst] : 0.f;
-      return g < kLeastLog ? kLeastLog : g;
-    };
     double total = 0.0;  // log2 of the walk's decay
-    auto gate_sums = [&](int n, float g) {
-      double G = double(g) * 1.4426950408889634;
-#pragma unroll
-      for (int d = 1; d < C; d <<= 1) {
-        const double up = __shfl_up(G, d);
-        if (lane >= d) G += up;
-      }
-      const double Gc = __shfl(G, C - 1);
+    auto gate_sums = [&](int n) {
+      const bool live = lane < C && int64_t(chunk_of(n)) * C + lane < a.T;
+      float g = live ? raw(n)[lane] : 0.f;
+      g = g < kLeastLog ? kLeastLog : g;
+      const double G = wave_prefix(double(g) * 1.4426950408889634), Gc = lane_value(G, C - 1);
       total += Gc;
-      const bool live = int64_t(chunk_of(n)) * C + lane < a.T;
       if (lane < C) {
         float* ga = gates(n);
         const float hi = float(G), to_end = fast_exp2(float(Gc - G)), from_start = fast_exp2(float(G));
@@ -193,7 +220,6 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
       if constexpr (OUT > 0) {
         const uint32_t kb = TK::at(Ks(n)) + brow, qb = TK::at(Qs(n)) + brow;
         const float* ga = gates(n);
-        PT* P = Ps(n);
         F qf[NKK];
 #pragma unroll
         for (int kk = 0; kk < NKK; ++kk) qf[kk] = TK::row8_16(qb + 16 * p * TK::ROWB, 0, kk);
@@ -223,28 +249,21 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
       }
     };
     if (n0 < n1) {
-      fetch(n0);
-      if (n0 + 1 < n1) fetch(n0 + 1);
-      float g = 0.f;
-      if (gate) {
-        gate_sums(n0, gate_of(n0));
-        if (n0 + 1 < n1) gate_sums(n0 + 1, gate_of(n0 + 1));
-        g = gate_of(n0 + 2);
-      }
+      fetch_gate(n0);
+#pragma unroll
+      for (int i = 0; i < W::NS - 1; ++i)
+        if (n0 + i < n1) fetch(n0 + i);
       copies_landed();
-      lds_barrier();
-      scores(n0);
+      if (gate) gate_sums(n0);
       lds_barrier();
       for (int n = n0; n < n1; ++n) {
-        if (n + 2 < n1) {
-          fetch(n + 2);
-          if (gate) {
-            gate_sums(n + 2, g);
-            g = gate_of(n + 3);
-          }
-        }
-        if (n + 1 < n1) scores(n + 1);
-        copies_landed();
+        const bool more = n + W::NS - 1 < n1;
+        if (more) fetch(n + W::NS - 1);
+        scores(n);
+        if (gate && n + 1 < n1) gate_sums(n + 1);
+        if constexpr (OUT > 0) lds_barrier();
+        if (more) copies_landed<(W::NS - 2) * W::kCopies>();  // the next chunk is there
+        else copies_landed();
         lds_barrier();
       }
     }
@@ -296,7 +315,6 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
 
   if (n0 < n1) {
     lds_barrier();
-    lds_barrier();
     const uint32_t qrow = TK::b_row44_16(lane), kcol = TK::b_col8_16(lane), vcol = TV::b_col8_16(lane),
                    prow = TP::b_row8_16(lane);
     const int64_t ost = int64_t(a.H) * DV;
@@ -313,18 +331,17 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
 #pragma unroll
       for (int u = 0; u < U; ++u) vf[u] = TV::col8_16(vb, u, wave);
 
-      if constexpr (OUT > 0) {
-        f32x4 dots[TT];  // the tensor that the outputs meet, at the outputs' places
-        if constexpr (OUT == 2)
+      f32x4 acc[TT], dots[TT];  // dots: the tensor that the outputs meet, at the outputs' places
+      if constexpr (OUT == 2)
 #pragma unroll
-          for (int tt = 0; tt < TT; ++tt) {
-            const int64_t t = t0 + 16 * tt + l16;
-            const T* dp = static_cast<const T*>(a.dot) + obase + (t < a.T ? t : a.T - 1) * ost;
-            if constexpr (sizeof(T) == 2) dots[tt] = __builtin_convertvector(*reinterpret_cast<const bf16x4*>(dp), f32x4);
-            else dots[tt] = *reinterpret_cast<const f32x4*>(dp);
-          }
-        const uint32_t qb = TK::at(Qs(n)) + qrow, pb = TP::at(Ps(n)) + prow;
-        f32x4 acc[TT];
+        for (int tt = 0; tt < TT; ++tt) {
+          const int64_t t = t0 + 16 * tt + l16;
+          const T* dp = static_cast<const T*>(a.dot) + obase + (t < a.T ? t : a.T - 1) * ost;
+          if constexpr (sizeof(T) == 2) dots[tt] = __builtin_convertvector(*reinterpret_cast<const bf16x4*>(dp), f32x4);
+          else dots[tt] = *reinterpret_cast<const f32x4*>(dp);
+        }
+      if constexpr (OUT > 0) {
+        const uint32_t qb = TK::at(Qs(n)) + qrow;
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -335,8 +352,26 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
           for (int tt = 0; tt < TT; ++tt) acc[tt] = sf.left(TK::row44_16(qb, tt, kk), acc[tt]);
         }
 #pragma unroll
+        for (int tt = 0; tt < TT; ++tt) acc[tt] *= ga[2 * C + 16 * tt + l16];
+      }
+
+      const float ec = ga[4 * C];
+#pragma unroll
+      for (int i = 0; i < NKT; ++i) S[i] *= ec;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* w = ga + 3 * C + 32 * u + 8 * g4;
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(w), w1 = *reinterpret_cast<const f32x4*>(w + 4);
+        const Parts<T, kExact> x(O::unpack(vf[u]) * __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int i = 0; i < NKT; ++i) S[i] = x.right(TK::col8_16(kb, u, i), S[i]);
+      }
+
+      if constexpr (OUT > 0) {
+        lds_barrier();  // the scores are there
+        const uint32_t pb = TP::at(P) + prow;
+#pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
-          acc[tt] *= ga[2 * C + 16 * tt + l16];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (REV ? u < tt / 2 : u > tt / 2) continue;
@@ -355,18 +390,6 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
             if (g4 == 0 && t < a.T) a.x[(int64_t(part) * a.B * a.H + bh) * a.T + t] = d;
           }
         }
-      }
-
-      const float ec = ga[4 * C];
-#pragma unroll
-      for (int i = 0; i < NKT; ++i) S[i] *= ec;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* w = ga + 3 * C + 32 * u + 8 * g4;
-        const f32x4 w0 = *reinterpret_cast<const f32x4*>(w), w1 = *reinterpret_cast<const f32x4*>(w + 4);
-        const Parts<T, kExact> x(O::unpack(vf[u]) * __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int i = 0; i < NKT; ++i) S[i] = x.right(TK::col8_16(kb, u, i), S[i]);
       }
       if constexpr (OUT == 2 && REV)
         if (c % kBlockChunks == 0 && c > 0) meet(c / kBlockChunks);

@@ -30,6 +30,11 @@ struct LinearForm {
 // kMinSegChunks chunks, as many as keep to one workgroup per compute unit: the end states then
 // cost one more pass over k and v.
 constexpr int64_t kUnits = 256;
+// A chunk's rows of all heads stay within the 32-bit offsets of its copies.
+constexpr int64_t kMaxRow = int64_t(1) << 22;
+bool linear_sizes_ok(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv) {
+  return sizes_ok(B, T, H, dk, dv) && H * dk <= kMaxRow && H * dv <= kMaxRow;
+}
 constexpr int64_t kMinSegChunks = 4;
 LinearForm linear_form(int64_t B, int64_t T, int64_t H, int dv, bool bf16) {
   const int C = linear_chunk(bf16);
@@ -124,7 +129,7 @@ int64_t prompt_bwd_floats(int n, int Hq, int Hkv, int d) {
 extern "C" {
 
 size_t kda_linear_chunk_fwd_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype in_dtype) {
-  if (!dtype_ok(in_dtype) || !sizes_ok(B, T, H, dk, dv) || !dim_ok(dk) || !dim_ok(dv)) return 0;
+  if (!dtype_ok(in_dtype) || !linear_sizes_ok(B, T, H, dk, dv) || !dim_ok(dk) || !dim_ok(dv)) return 0;
   return size_t(seg_floats(linear_form(B, T, H, dv, in_dtype == KDA_BF16), int64_t(B) * H, int64_t(dk) * dv)) * 4;
 }
 
@@ -133,7 +138,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, kda
                                 int T, int H, int dk, int dv, float scale, void* workspace, size_t workspace_bytes,
                                 void* stream) {
   if (!dtype_ok(in_dtype) || !dtype_ok(o_dtype)) return KDA_ERR_DTYPE;
-  if (!sizes_ok(B, T, H, dk, dv)) return KDA_ERR_SHAPE;
+  if (!linear_sizes_ok(B, T, H, dk, dv)) return KDA_ERR_SHAPE;
   if (!dim_ok(dk) || !dim_ok(dv) || !isfinite(scale) || (g_per_head != 0 && g_per_head != 1))
     return KDA_ERR_UNSUPPORTED;
   const bool bf16 = in_dtype == KDA_BF16;
@@ -167,7 +172,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, kda
 }
 
 size_t kda_linear_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype in_dtype, int g_per_head) {
-  if (!dtype_ok(in_dtype) || !sizes_ok(B, T, H, dk, dv) || !dim_ok(dk) || !dim_ok(dv) ||
+  if (!dtype_ok(in_dtype) || !linear_sizes_ok(B, T, H, dk, dv) || !dim_ok(dk) || !dim_ok(dv) ||
       !bwd_grid_ok(B, T, H, in_dtype == KDA_BF16))
     return 0;
   return size_t(bwd_layout(B, T, H, dk, dv, in_dtype == KDA_BF16, g_per_head != 0).total) * 4;
@@ -179,7 +184,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, kda
                                 int dk_dim, int dv_dim, float scale, void* workspace, size_t workspace_bytes,
                                 void* stream) {
   if (!dtype_ok(in_dtype) || !dtype_ok(grad_dtype)) return KDA_ERR_DTYPE;
-  if (!sizes_ok(B, T, H, dk_dim, dv_dim)) return KDA_ERR_SHAPE;
+  if (!linear_sizes_ok(B, T, H, dk_dim, dv_dim)) return KDA_ERR_SHAPE;
   if (!dim_ok(dk_dim) || !dim_ok(dv_dim) || !isfinite(scale) || (g_per_head != 0 && g_per_head != 1))
     return KDA_ERR_UNSUPPORTED;
   const bool bf16 = in_dtype == KDA_BF16;

@@ -108,8 +108,13 @@ struct Tile {
   static constexpr bool B16 = sizeof(T) == 2;
   static_assert(COLS % EPC == 0 && (CH & (CH - 1)) == 0 && CH >= 4, "rows of a power of two of chunks");
   typedef typename Op<T>::frag F;
+  // The permutation, linear over the row's bits, from the LDS' 64 banks and the lanes that it serves
+  // together (16 of a 16-byte read: 0-3, 12-15, 20-23 and 24-27, and those + 4, + 32, + 36; 32 of an
+  // 8-byte one): with these images of bits 0 .. 3 every kind of read below is free of conflicts.
+  // Rows of 64 (128) bytes share 256 bytes of banks with three (one) neighbours, which stands in for
+  // the images of bits 0 and 1 (0).  Measured per read of a wavefront: 4 and 2 cycles, the width's own.
   __device__ __forceinline__ static constexpr int swz(int row) {
-    return CH >= 16 ? (((row << 1) & 14) | ((row >> 3) & 1)) : (row & (CH - 1));
+    return (CH >= 16 ? (row << 2) & 12 : (CH == 8 ? (row << 1) & 4 : 0)) ^ ((row >> 2) & 1) * 3 ^ ((row >> 3) & 1) * 2;
   }
   // element offset of (row, col); `col` a multiple of 4 keeps 4 elements together
   __device__ __forceinline__ static int off(int row, int col) {
@@ -309,9 +314,50 @@ __device__ __forceinline__ void lds_copy4(const void* src, uint32_t lds) {
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
                : "memory", "m0");
 }
+// The same from one base for the wavefront plus 32 bits of byte offset per lane.
+__device__ __forceinline__ void lds_copy16(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_copy4(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :
+               : "s"(lds), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
-__device__ __forceinline__ void copies_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int LATER = 0>  // all but the last LATER copies of this wavefront
+__device__ __forceinline__ void copies_landed() {
+  static_assert(LATER < 64, "the counter's range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+}
 // A barrier for LDS contents: waits for this wavefront's LDS accesses, not for its stores to memory.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The sum over lanes 0 .. l in lane l, in 64 bits, by lane shifts within the register file (rows of
+// 16 lanes, then the rows' last lanes broadcast).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_shifted(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, ROWS, 15, false));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), CTRL, ROWS, 15, false));
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_prefix(double x) {
+  x += dpp_shifted<0x111, 15>(x);  // row_shr by 1, 2, 4, 8
+  x += dpp_shifted<0x112, 15>(x);
+  x += dpp_shifted<0x114, 15>(x);
+  x += dpp_shifted<0x118, 15>(x);
+  x += dpp_shifted<0x142, 10>(x);  // row_bcast:15 into rows 1 and 3
+  x += dpp_shifted<0x143, 12>(x);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(u), lane), hi = __builtin_amdgcn_readlane(uint32_t(u >> 32), lane);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
 
 }  // namespace kda

@@ -345,7 +345,8 @@ kda_status kda_decode_replay(const void* q, const void* k, const void* v,
  *
  * per batch entry and head: the recurrence of the delta rule above without its
  * erase term and with one decay per head instead of one per key channel.
- * Layouts, dtypes and the supported dk, dv are those of the chunked prefill.
+ * Layouts, dtypes and the supported dk, dv are those of the chunked prefill;
+ * H*dk and H*dv are at most 2^22 in the chunked calls.
  *
  *   q, k [B,T,H,dk] in_dtype    v [B,T,H,dv] in_dtype
  *   g    fp32 log-decays, at most 0: [B,T,H] (g_per_head == 0), or [H], the
