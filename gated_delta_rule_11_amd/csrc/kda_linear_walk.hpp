@@ -61,8 +61,9 @@ struct WalkShape {
   static constexpr int NPW = OUT ? TT : 1;         // scoring and copying wavefronts
   static constexpr int NT = 64 * (NSW + NPW);
   static constexpr int NKK = DKP / 32, NKT = DK / 16;
-  static constexpr bool PF = OUT == 2 || sizeof(T) == 4;  // P in fp32
-  static constexpr int kK = C * DKP * int(sizeof(T)), kV = C * VC * int(sizeof(T)), kP = C * C * (PF ? 4 : 2);
+  static constexpr int kExact = sizeof(T) == 2 ? 3 : 1;  // parts of an fp32-accurate operand
+  static constexpr int kOut = OUT == 2 ? kExact : 1;     // parts of P and S in the outputs
+  static constexpr int kK = C * DKP * int(sizeof(T)), kV = C * VC * int(sizeof(T)), kP1 = C * C * int(sizeof(T)), kP = kP1 * kOut;
   static constexpr int kG = (4 * C + 4) * 4;  // G hi, G lo, the outputs' and the update's weights, e^{G_C}
   // chunks in rotation: one in use, the others on their way (two, or three where only k and v are)
   static constexpr int NS = OUT ? 3 : 4;
@@ -76,28 +77,41 @@ struct WalkShape {
   static_assert(C % (64 / Tile<T, DKP>::CH * NPW) == 0 && C % (64 / Tile<T, VC>::CH * NPW) == 0, "the same for each");
 };
 
-// x as parts of the element type whose sum is x to 8 (16, 24) bits.
-template <typename T, int N>
+// Two fp32 values' upper halves as a pair of bf16.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+
+// x as parts of the element type: one, rounded, or three bf16 whose sum is x (each takes the upper
+// half of what is left, 8 bits of significand at a time, and the rest is exact).
+template <typename T, int N, int W>
 struct Parts {
-  typename Op<T>::frag p[N];
-  __device__ __forceinline__ explicit Parts(f32x8 x) {
+  typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+  words p[N];
+  template <typename V>
+  __device__ __forceinline__ explicit Parts(V x) {
+    static_assert(N == 3 && sizeof(T) == 2, "the exact form");
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      p[i] = Op<T>::pack(x);
-      if (i + 1 < N) x -= Op<T>::unpack(p[i]);
-    }
-  }
-  __device__ __forceinline__ f32x4 left(typename Op<T>::frag b, f32x4 c) const {  // sum over parts of p b
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = N - 1; i >= 0; --i) c = Op<T>::mma16(p[i], b, c);
-    return c;
-  }
-  __device__ __forceinline__ f32x4 right(typename Op<T>::frag a, f32x4 c) const {  // .. of a p
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i) c = Op<T>::mma16(a, p[i], c);
-    return c;
+      for (int j = 0; j < W; j += 2) {
+        p[i][j / 2] = upper_halves(x[j], x[j + 1]);
+        if (i + 1 < N) {
+          x[j] -= __uint_as_float(__float_as_uint(x[j]) & 0xffff0000u);
+          x[j + 1] -= __uint_as_float(__float_as_uint(x[j + 1]) & 0xffff0000u);
+        }
+      }
   }
 };
+template <typename T>
+struct Parts<T, 1, 8> {
+  typename Op<T>::frag p[1];
+  __device__ __forceinline__ explicit Parts(f32x8 x) { p[0] = Op<T>::pack(x); }
+};
+template <typename T, int N>
+__device__ __forceinline__ typename Op<T>::frag part_of(const Parts<T, N, 8>& x, int i) {
+  return __builtin_bit_cast(typename Op<T>::frag, x.p[i]);
+}
 
 template <typename T, typename TO, int DK, int DV, int OUT, bool REV>
 __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_kernel(const LinearArgs a) {
@@ -106,11 +120,9 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
   using F = typename O::frag;
   using TK = Tile<T, W::DKP>;
   using TV = Tile<T, W::VC>;
-  using PT = std::conditional_t<W::PF, float, T>;
-  using TP = Tile<PT, W::C>;
+  using TP = Tile<T, W::C>;
   constexpr int C = W::C, NSW = W::NSW, TT = W::TT, U = W::U, NKK = W::NKK, NKT = W::NKT;
-  constexpr int kExact = sizeof(T) == 2 ? 3 : 1;           // parts of an fp32-accurate operand
-  constexpr int kOut = OUT == 2 ? kExact : 1;              // of P and S in the outputs
+  constexpr int kExact = W::kExact, kOut = W::kOut;
   extern __shared__ __align__(1024) unsigned char smem[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15,
@@ -128,7 +140,7 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
   auto Ks = [&](int n) { return reinterpret_cast<T*>(smem + (n % W::NS) * W::kK); };
   auto Qs = [&](int n) { return reinterpret_cast<T*>(smem + W::oQ + (n % W::NS) * W::kK); };
   auto Vs = [&](int n) { return reinterpret_cast<T*>(smem + W::oV + (n % W::NS) * W::kV); };
-  PT* const P = reinterpret_cast<PT*>(smem + W::oP);
+  T* const P = reinterpret_cast<T*>(smem + W::oP);  // [parts][C][C]
   auto gates = [&](int n) { return reinterpret_cast<float*>(smem + W::oG + (n & 1) * W::kG); };
   auto raw = [&](int n) { return reinterpret_cast<float*>(smem + W::oR) + (n % (W::NS + 1)) * 64; };
 
@@ -174,11 +186,9 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
       const int64_t t0 = int64_t(chunk_of(n)) * C;
       const T *kc = kp + t0 * kst, *qc = OUT ? qp + t0 * kst : nullptr, *vc = vp + t0 * vst;
       const uint32_t ks = lds_offset(Ks(n)) + p * 1024, qs = lds_offset(Qs(n)) + p * 1024, vs = lds_offset(Vs(n)) + p * 1024;
-      const int last = a.T - t0 < C ? int(a.T - t0) - 1 : C - 1;
       // in a tile wider than the head, the lanes of the columns that do not exist copy nothing
-      auto copy = [&](auto tile_tag, const T* from, uint32_t off, uint32_t to, int i, int64_t stride, int cols) {
+      auto copy = [&](auto tile_tag, const T* from, uint32_t off, uint32_t to, int i, int cols) {
         using L = decltype(tile_tag);
-        if (last < C - 1) off = rows_of(tile_tag, i, stride, last);
         bool on = true;
         if (L::CH * L::EPC != cols) {
           const int r = (i * W::NPW + p) * (64 / L::CH) + lane / L::CH;
@@ -186,13 +196,25 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
         }
         if (on) lds_copy16(from, off, to + i * W::NPW * 1024);
       };
+      if (a.T - t0 >= C) {
 #pragma unroll
-      for (int i = 0; i < kPerK; ++i) copy(TK{}, kc, offk[i], ks, i, kst, DK);
-      if constexpr (OUT > 0)
+        for (int i = 0; i < kPerK; ++i) copy(TK{}, kc, offk[i], ks, i, DK);
+        if constexpr (OUT > 0)
 #pragma unroll
-        for (int i = 0; i < kPerK; ++i) copy(TK{}, qc, offk[i], qs, i, kst, DK);
+          for (int i = 0; i < kPerK; ++i) copy(TK{}, qc, offk[i], qs, i, DK);
 #pragma unroll
-      for (int i = 0; i < kPerV; ++i) copy(TV{}, vc, offv[i], vs, i, vst, W::DVS);
+        for (int i = 0; i < kPerV; ++i) copy(TV{}, vc, offv[i], vs, i, W::DVS);
+      } else {
+        const int last = int(a.T - t0) - 1;
+#pragma unroll
+        for (int i = 0; i < kPerK; ++i) {
+          const uint32_t off = rows_of(TK{}, i, kst, last);
+          copy(TK{}, kc, off, ks, i, DK);
+          if constexpr (OUT > 0) copy(TK{}, qc, off, qs, i, DK);
+        }
+#pragma unroll
+        for (int i = 0; i < kPerV; ++i) copy(TV{}, vc, rows_of(TV{}, i, vst, last), vs, i, W::DVS);
+      }
       fetch_gate(n + 1);
     };
     // the gate wavefront has the fewest scores
@@ -244,7 +266,13 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
               else x[j] = s + j <= t ? fast_exp2(d) * c[j] : 0.f;
             }
           }
-          TP::put4(P, t, s, x);
+          if constexpr (kOut == 1) {
+            TP::put4(P, t, s, x);
+          } else {
+            const Parts<T, kOut, 4> xp(x);
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) *reinterpret_cast<u32x2v*>(P + i * C * C + TP::off(t, s)) = xp.p[i];
+          }
         }
       }
     };
@@ -347,9 +375,13 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
 #pragma unroll
         for (int kk = 0; kk < NKK; ++kk) {
           const f32x4 hi = 2 * kk + 1 < NKT ? S[(2 * kk + 1) % NKT] : f32x4{0, 0, 0, 0};
-          const Parts<T, kOut> sf(__builtin_shufflevector(S[2 * kk], hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          const Parts<T, kOut, 8> sf(__builtin_shufflevector(S[2 * kk], hi, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-          for (int tt = 0; tt < TT; ++tt) acc[tt] = sf.left(TK::row44_16(qb, tt, kk), acc[tt]);
+          for (int tt = 0; tt < TT; ++tt) {
+            const F qf = TK::row44_16(qb, tt, kk);
+#pragma unroll
+            for (int i = kOut - 1; i >= 0; --i) acc[tt] = O::mma16(part_of(sf, i), qf, acc[tt]);
+          }
         }
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) acc[tt] *= ga[2 * C + 16 * tt + l16];
@@ -362,9 +394,13 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
       for (int u = 0; u < U; ++u) {
         const float* w = ga + 3 * C + 32 * u + 8 * g4;
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(w), w1 = *reinterpret_cast<const f32x4*>(w + 4);
-        const Parts<T, kExact> x(O::unpack(vf[u]) * __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
+        const Parts<T, kExact, 8> x(O::unpack(vf[u]) * __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-        for (int i = 0; i < NKT; ++i) S[i] = x.right(TK::col8_16(kb, u, i), S[i]);
+        for (int i = 0; i < NKT; ++i) {
+          const F kf = TK::col8_16(kb, u, i);
+#pragma unroll
+          for (int j = kExact - 1; j >= 0; --j) S[i] = O::mma16(kf, part_of(x, j), S[i]);
+        }
       }
 
       if constexpr (OUT > 0) {
@@ -375,8 +411,8 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (REV ? u < tt / 2 : u > tt / 2) continue;
-            if constexpr (W::PF && sizeof(T) == 2) acc[tt] = Parts<T, kOut>(TP::row8_16(pb, tt, u)).right(vf[u], acc[tt]);
-            else acc[tt] = O::mma16(vf[u], TP::row8_16(pb, tt, u), acc[tt]);
+#pragma unroll
+            for (int i = kOut - 1; i >= 0; --i) acc[tt] = O::mma16(vf[u], TP::row8_16(pb + i * W::kP1, tt, u), acc[tt]);
           }
           const int64_t t = t0 + 16 * tt + l16;
           f32x4 x = acc[tt];

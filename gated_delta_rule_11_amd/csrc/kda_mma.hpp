@@ -189,9 +189,11 @@ struct Tile {
     const int r = lane & 15, g = lane >> 4;
     return r * ROWB + (B16 ? ((((g >> 1) ^ swz(r)) << 4) + 8 * (g & 1)) : ((g ^ swz(r)) << 4));
   }
+  // (volatile: merged into strided pairs, the two halves would have to be moved next to each other)
   __device__ __forceinline__ static F row44_16(uint32_t b, int t, int kk) {
     if constexpr (B16) {
-      return Op<T>::join(rd<bf16x4>((b ^ (kk << 6)) + 16 * t * ROWB), rd<bf16x4>((b ^ ((kk << 6) | 32)) + 16 * t * ROWB));
+      typedef const volatile __attribute__((address_space(3))) bf16x4* half;
+      return Op<T>::join(*(half)(uintptr_t)((b ^ (kk << 6)) + 16 * t * ROWB), *(half)(uintptr_t)((b ^ ((kk << 6) | 32)) + 16 * t * ROWB));
     } else {
       return Op<T>::join(rd<f32x4>((b ^ (kk << 7)) + 16 * t * ROWB), rd<f32x4>((b ^ ((kk << 7) | 64)) + 16 * t * ROWB));
     }
