@@ -102,11 +102,11 @@ def lib() -> ctypes.CDLL:
     L.kda_linear_chunk_bwd.restype = I
     L.kda_linear_decode_step.argtypes = [P, P, P, I, P, I, P, P, P, I, I, I, I, I, F, P]
     L.kda_linear_decode_step.restype = I
-    L.kda_attn_prompt_fwd.argtypes = [P, P, P, I, P, P, I, P, I, I, I, I, I, F, P]
+    L.kda_attn_prompt_fwd.argtypes = [P, P, P, I, P, P, I, P, I, I, I, I, I, F, I, P]
     L.kda_attn_prompt_fwd.restype = I
     L.kda_attn_prompt_bwd_workspace_bytes.argtypes = [I] * 4
     L.kda_attn_prompt_bwd_workspace_bytes.restype = Z
-    L.kda_attn_prompt_bwd.argtypes = [P, P, P, I, P, P, I, P, P, P, P, P, I, I, I, I, I, I, F, P, Z, P]
+    L.kda_attn_prompt_bwd.argtypes = [P, P, P, I, P, P, I, P, P, P, P, P, I, I, I, I, I, I, F, I, P, Z, P]
     L.kda_attn_prompt_bwd.restype = I
     L.kda_kv_cache_append.argtypes = [P, P, I, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
     L.kda_kv_cache_append.restype = I
@@ -461,18 +461,21 @@ def _run_on_stream(fn):
     would otherwise hand their memory on while the call still runs there)."""
     @functools.wraps(fn)
     def wrapper(*args, stream=None, **kwargs):
-        t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)), None)
+        t = args[0] if args and isinstance(args[0], torch.Tensor) else next(
+            (a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)), None)
         if t is None:
             raise KDAError(f"{fn.__name__}: no tensor given")
         if not t.is_cuda:
             raise KDAError("libkda runs on the GPU only: tensor is on the CPU")
-        if stream is not None and stream.device != t.device:
+        if stream is None:
+            if t.get_device() == torch.cuda.current_device():
+                return fn(*args, **kwargs)
+            with torch.cuda.device(t.device):
+                return fn(*args, **kwargs)
+        if stream.device != t.device:
             raise KDAError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {t.device}")
-        with torch.cuda.device(t.device):
-            if stream is None:
-                return fn(*args, **kwargs)
-            with torch.cuda.stream(stream):
-                return fn(*args, **kwargs)
+        with torch.cuda.device(t.device), torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
     return wrapper
 
 
@@ -483,16 +486,52 @@ def _dims(what: str, *specs):
             raise KDAError(f"{what}: {name} must be a tensor of {n} dimensions")
 
 
+def _match(what: str, *specs):
+    """One pass over (name, tensor or None, shape, allowed dtypes): what ``_shapes`` and ``_dev`` check."""
+    dev = None
+    for name, t, shape, dtypes in specs:
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise KDAError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype not in dtypes:
+            raise KDAError(f"{what}: {name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if not t.is_cuda:
+            raise KDAError("libkda runs on the GPU only: tensor is on the CPU")
+        if not t.is_contiguous():
+            raise KDAError(f"{what}: {name} must be contiguous")
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on cuda:{dev}")
+
+
+def _a(t: Optional[torch.Tensor]):
+    """A tensor's address, for a call's c_void_p argument."""
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(t: torch.Tensor) -> int:
+    """The current stream of t's device (current during a call)."""
+    if _raw_stream is not None:  # a few times cheaper than building a Stream
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
 def _need(workspace, need: int, device):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of ``need`` bytes."""
+    """(address, bytes, tensor) of the caller's workspace, or of a new one of ``need`` bytes."""
     if workspace is None:
         if need == 0:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _dev(workspace)
-    if workspace.device != device:
-        raise KDAError(f"the workspace is on {workspace.device}, the tensors on {device}")
-    return _p(workspace), workspace.numel() * workspace.element_size(), workspace
+    else:
+        _dev(workspace)
+        if workspace.device != device:
+            raise KDAError(f"the workspace is on {workspace.device}, the tensors on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _out_dtype(dtype, what: str, name: str) -> torch.dtype:
@@ -509,15 +548,13 @@ def _io_of(t) -> tuple:
 def _linear_shapes(what, q, k, v, g, **more):
     """(B, T, H, dk, dv, g is per head) after every tensor's check; ``more`` maps a name to
     (tensor or None, "o" / "k" / "S" layout, dtypes)."""
-    _dims(what, ("q", q, 4), ("v", v, 4))
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     per_head = isinstance(g, torch.Tensor) and g.dim() == 1
     layouts = {"o": (B, T, H, dv), "k": (B, T, H, dk), "S": (B, H, dk, dv)}
     io = _io_of(q)
-    _shapes(what, ("q", q, (B, T, H, dk), _IO), ("k", k, (B, T, H, dk), io), ("v", v, (B, T, H, dv), io),
-            ("g", g, (H,) if per_head else (B, T, H), _F32), *[(n, t, layouts[at], dt) for n, (t, at, dt) in more.items()])
-    _dev(q, k, v, g, *[t for t, _, _ in more.values()])
+    _match(what, ("q", q, (B, T, H, dk), _IO), ("k", k, (B, T, H, dk), io), ("v", v, (B, T, H, dv), io),
+           ("g", g, (H,) if per_head else (B, T, H), _F32), *[(n, t, layouts[at], dt) for n, (t, at, dt) in more.items()])
     return B, T, H, dk, dv, per_head
 
 
@@ -539,9 +576,9 @@ def linear_chunk_fwd(q, k, v, g, S_in=None, o=None, S_out=None, o_dtype=None, sc
     B, T, H, dk, dv, ph = _linear_shapes(what, q, k, v, g, S_in=(S_in, "S", _F32), o=(o, "o", _IO),
                                          S_out=(S_out, "S", _F32))
     wp, wb, _keep = _need(workspace, linear_chunk_fwd_workspace_bytes(B, T, H, dk, dv, q.dtype), q.device)
-    _check(lib().kda_linear_chunk_fwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(g), int(ph), _p(S_in), _p(o),
-                                      _dtype_code(o), _p(S_out), B, T, H, dk, dv, float(scale), wp, wb,
-                                      _stream(None)), what)
+    _check(lib().kda_linear_chunk_fwd(_a(q), _a(k), _a(v), _dtype_code(q), _a(g), int(ph), _a(S_in), _a(o),
+                                      _dtype_code(o), _a(S_out), B, T, H, dk, dv, float(scale), wp, wb,
+                                      _here(q)), what)
     return o, S_out
 
 
@@ -561,16 +598,17 @@ def linear_chunk_bwd(q, k, v, g, d_o, dS_out=None, S_in=None, scale: float = 1.0
     and dS_in (fp32, None unless ``want_dS_in``)."""
     what = "kda_linear_chunk_bwd"
     grad_dtype = _out_dtype(grad_dtype, what, "grad_dtype")
+    _dims(what, ("q", q, 4), ("v", v, 4))
     B, T, H, dk, dv, ph = _linear_shapes(what, q, k, v, g, d_o=(d_o, "o", _io_of(q)), dS_out=(dS_out, "S", _F32),
                                          S_in=(S_in, "S", _F32))
     new = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=q.device)  # noqa: E731
     out = {"dq": new(grad_dtype, B, T, H, dk), "dk": new(grad_dtype, B, T, H, dk), "dv": new(grad_dtype, B, T, H, dv),
            "dg": torch.empty_like(g), "dS_in": new(torch.float32, B, H, dk, dv) if want_dS_in else None}
     wp, wb, _keep = _need(workspace, linear_chunk_bwd_workspace_bytes(B, T, H, dk, dv, q.dtype, ph), q.device)
-    _check(lib().kda_linear_chunk_bwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(g), int(ph), _p(S_in), _p(d_o),
-                                      _p(dS_out), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _dtype_code(out["dq"]),
-                                      _p(out["dg"]), _p(out["dS_in"]), B, T, H, dk, dv, float(scale), wp, wb,
-                                      _stream(None)), what)
+    _check(lib().kda_linear_chunk_bwd(_a(q), _a(k), _a(v), _dtype_code(q), _a(g), int(ph), _a(S_in), _a(d_o),
+                                      _a(dS_out), _a(out["dq"]), _a(out["dk"]), _a(out["dv"]), _dtype_code(out["dq"]),
+                                      _a(out["dg"]), _a(out["dS_in"]), B, T, H, dk, dv, float(scale), wp, wb,
+                                      _here(q)), what)
     return out
 
 
@@ -590,12 +628,11 @@ def linear_decode_step(q, k, v, g, S, o=None, o_dtype=None, scale: float = 1.0,
         S_out = S
     ph = isinstance(g, torch.Tensor) and g.dim() == 1
     io = _io_of(q)
-    _shapes(what, ("q", q, (N, H, dk), _IO), ("k", k, (N, H, dk), io), ("v", v, (N, H, dv), io),
-            ("g", g, (H,) if ph else (N, H), _F32), ("S", S, (N, H, dk, dv), _F32), ("S_out", S_out, (N, H, dk, dv), _F32),
-            ("o", o, (N, H, dv), _IO))
-    _dev(q, k, v, g, S, S_out, o)
-    _check(lib().kda_linear_decode_step(_p(q), _p(k), _p(v), _dtype_code(q), _p(g), int(ph), _p(S), _p(S_out), _p(o),
-                                        _dtype_code(o), N, H, dk, dv, float(scale), _stream(None)), what)
+    _match(what, ("q", q, (N, H, dk), _IO), ("k", k, (N, H, dk), io), ("v", v, (N, H, dv), io),
+           ("g", g, (H,) if ph else (N, H), _F32), ("S", S, (N, H, dk, dv), _F32), ("S_out", S_out, (N, H, dk, dv), _F32),
+           ("o", o, (N, H, dv), _IO))
+    _check(lib().kda_linear_decode_step(_a(q), _a(k), _a(v), _dtype_code(q), _a(g), int(ph), _a(S), _a(S_out), _a(o),
+                                        _dtype_code(o), N, H, dk, dv, float(scale), _here(q)), what)
     return o, S_out
 
 
@@ -610,9 +647,8 @@ def _prompt_shapes(what, q, k, v, cu_seqlens, *more):
         raise KDAError(f"{what}: cu_seqlens has no entry (n_seqs + 1 are needed)")
     io = _io_of(q)
     at = {"q": (n, Hq, d), "k": (n, Hkv, d), "l": (n, Hq)}
-    _shapes(what, ("q", q, (n, Hq, d), _IO), ("k", k, (n, Hkv, d), io), ("v", v, (n, Hkv, d), io),
-            ("cu_seqlens", cu_seqlens, tuple(cu_seqlens.shape), _I32), *[(m, t, at[s], dt) for m, t, s, dt in more])
-    _dev(q, k, v, cu_seqlens, *[t for _, t, _, _ in more])
+    _match(what, ("q", q, (n, Hq, d), _IO), ("k", k, (n, Hkv, d), io), ("v", v, (n, Hkv, d), io),
+           ("cu_seqlens", cu_seqlens, cu_seqlens.shape, _I32), *[(m, t, at[s], dt) for m, t, s, dt in more])
     return n, cu_seqlens.shape[0] - 1, Hq, Hkv, d
 
 
@@ -630,13 +666,14 @@ def attn_prompt_fwd(q, k, v, cu_seqlens, scale: Optional[float] = None, o=None, 
     what = "kda_attn_prompt_fwd"
     _dims(what, ("q", q, 3))
     n, Hq, d = q.shape
+    given = o is not None or lse is not None
     if o is None:
-        o = torch.zeros((n, Hq, d), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
+        o = (torch.zeros if given else torch.empty)((n, Hq, d), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
     if lse is None and want_lse:
-        lse = torch.zeros((n, Hq), dtype=torch.float32, device=q.device)
+        lse = (torch.zeros if given else torch.empty)((n, Hq), dtype=torch.float32, device=q.device)
     n, ns, Hq, Hkv, d = _prompt_shapes(what, q, k, v, cu_seqlens, ("o", o, "q", _IO), ("lse", lse, "l", _F32))
-    _check(lib().kda_attn_prompt_fwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(cu_seqlens), _p(o), _dtype_code(o), _p(lse),
-                                     n, ns, Hq, Hkv, d, _softmax_scale(scale, d), _stream(None)), what)
+    _check(lib().kda_attn_prompt_fwd(_a(q), _a(k), _a(v), _dtype_code(q), _a(cu_seqlens), _a(o), _dtype_code(o), _a(lse),
+                                     n, ns, Hq, Hkv, d, _softmax_scale(scale, d), int(not given), _here(q)), what)
     return o, lse
 
 
@@ -655,13 +692,13 @@ def attn_prompt_bwd(q, k, v, cu_seqlens, o, lse, d_o, scale: Optional[float] = N
     grad_dtype = _out_dtype(grad_dtype, what, "grad_dtype")
     n, ns, Hq, Hkv, d = _prompt_shapes(what, q, k, v, cu_seqlens, ("o", o, "q", _IO), ("lse", lse, "l", _F32),
                                        ("d_o", d_o, "q", _io_of(q)))
-    out = {"dq": torch.zeros((n, Hq, d), dtype=grad_dtype, device=q.device),
-           "dk": torch.zeros((n, Hkv, d), dtype=grad_dtype, device=q.device),
-           "dv": torch.zeros((n, Hkv, d), dtype=grad_dtype, device=q.device)}
+    out = {"dq": torch.empty((n, Hq, d), dtype=grad_dtype, device=q.device),
+           "dk": torch.empty((n, Hkv, d), dtype=grad_dtype, device=q.device),
+           "dv": torch.empty((n, Hkv, d), dtype=grad_dtype, device=q.device)}
     wp, wb, _keep = _need(workspace, attn_prompt_bwd_workspace_bytes(n, Hq, Hkv, d), q.device)
-    _check(lib().kda_attn_prompt_bwd(_p(q), _p(k), _p(v), _dtype_code(q), _p(cu_seqlens), _p(o), _dtype_code(o), _p(lse),
-                                     _p(d_o), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _dtype_code(out["dq"]), n, ns,
-                                     Hq, Hkv, d, _softmax_scale(scale, d), wp, wb, _stream(None)), what)
+    _check(lib().kda_attn_prompt_bwd(_a(q), _a(k), _a(v), _dtype_code(q), _a(cu_seqlens), _a(o), _dtype_code(o), _a(lse),
+                                     _a(d_o), _a(out["dq"]), _a(out["dk"]), _a(out["dv"]), _dtype_code(out["dq"]), n, ns,
+                                     Hq, Hkv, d, _softmax_scale(scale, d), 1, wp, wb, _here(q)), what)
     return out
 
 
@@ -672,10 +709,9 @@ def _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table,
     _dims(what, ("k_cache", k_cache, 4), ("block_table", block_table, 2))
     pages, _, page, _ = k_cache.shape
     N, max_pages = block_table.shape
-    _shapes(what, *more, ("k_cache", k_cache, (pages, Hkv, page, d), _F8), ("v_cache", v_cache, (pages, Hkv, d, page), _F8),
-            ("k_scale", k_scale, (pages, Hkv), _F32), ("v_scale", v_scale, (pages, Hkv), _F32),
-            ("block_table", block_table, (N, max_pages), _I32), ("context_len", context_len, (N,), _I32))
-    _dev(k_cache, v_cache, k_scale, v_scale, block_table, context_len, *[m[1] for m in more])
+    _match(what, *more, ("k_cache", k_cache, (pages, Hkv, page, d), _F8), ("v_cache", v_cache, (pages, Hkv, d, page), _F8),
+           ("k_scale", k_scale, (pages, Hkv), _F32), ("v_scale", v_scale, (pages, Hkv), _F32),
+           ("block_table", block_table, (N, max_pages), _I32), ("context_len", context_len, (N,), _I32))
     return N, page, pages, max_pages
 
 
@@ -691,9 +727,9 @@ def kv_cache_append(k, v, cu_seqlens, context_len, block_table, k_cache, v_cache
     N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
                                        ("k", k, (n, Hkv, d), _IO), ("v", v, (n, Hkv, d), _io_of(k)),
                                        ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32))
-    _check(lib().kda_kv_cache_append(_p(k), _p(v), _dtype_code(k), _p(cu_seqlens), _p(context_len), _p(block_table),
-                                     _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), n, N, Hkv, d, page, pages, mp,
-                                     _stream(None)), what)
+    _check(lib().kda_kv_cache_append(_a(k), _a(v), _dtype_code(k), _a(cu_seqlens), _a(context_len), _a(block_table),
+                                     _a(k_cache), _a(v_cache), _a(k_scale), _a(v_scale), n, N, Hkv, d, page, pages, mp,
+                                     _here(k)), what)
 
 
 def attn_decode_step_workspace_bytes(N: int, Hq: int, Hkv: int, d: int, page: int, max_pages: int) -> int:
@@ -722,7 +758,7 @@ def attn_decode_step(q, k_cache, v_cache, k_scale, v_scale, block_table, context
     if Nt != N:
         raise KDAError(f"{what}: block_table has {Nt} rows, q {N}")
     wp, wb, _keep = _need(workspace, attn_decode_step_workspace_bytes(N, Hq, Hkv, d, page, mp), q.device)
-    _check(lib().kda_attn_decode_step(_p(q), _dtype_code(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
-                                      _p(block_table), _p(context_len), _p(o), _dtype_code(o), _p(lse), N, Hq, Hkv, d,
-                                      page, pages, mp, _softmax_scale(scale, d), wp, wb, _stream(None)), what)
+    _check(lib().kda_attn_decode_step(_a(q), _dtype_code(q), _a(k_cache), _a(v_cache), _a(k_scale), _a(v_scale),
+                                      _a(block_table), _a(context_len), _a(o), _dtype_code(o), _a(lse), N, Hq, Hkv, d,
+                                      page, pages, mp, _softmax_scale(scale, d), wp, wb, _here(q)), what)
     return o, lse

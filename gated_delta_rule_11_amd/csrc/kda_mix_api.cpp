@@ -279,12 +279,12 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, k
 
 kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
                                void* o, kda_dtype o_dtype, float* lse, int n, int n_seqs, int Hq, int Hkv, int d,
-                               float scale, void* stream) {
+                               float scale, int zero_tail, void* stream) {
   if (!dtype_ok(in_dtype) || !dtype_ok(o_dtype)) return KDA_ERR_DTYPE;
   const kda_status s = heads_ok(n, Hq, Hkv, d);
   if (s == KDA_ERR_SHAPE || n_seqs < 0) return KDA_ERR_SHAPE;
-  if (s != KDA_OK || !isfinite(scale)) return KDA_ERR_UNSUPPORTED;
-  if (n == 0 || n_seqs == 0) return KDA_OK;
+  if (s != KDA_OK || !isfinite(scale) || (zero_tail != 0 && zero_tail != 1)) return KDA_ERR_UNSUPPORTED;
+  if (n == 0 || (n_seqs == 0 && !zero_tail)) return KDA_OK;
   if ((int64_t(n) + 127) / 128 * Hq > kMaxGrid) return KDA_ERR_SHAPE;
   if (!q || !k || !v || !cu_seqlens || !o) return KDA_ERR_NULL;
   if (!all_aligned({q, k, v, o}, cu_seqlens, 4) || !aligned(lse, 4)) return KDA_ERR_ALIGN;
@@ -295,7 +295,7 @@ kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_
     if (overlap(ro, in) || overlap(rl, in)) return KDA_ERR_ALIAS;
   if (overlap(ro, rl)) return KDA_ERR_ALIAS;
   return from_hip(launch_prompt_fwd(PromptArgs{q, k, v, cu_seqlens, o, lse, n, n_seqs, Hq, Hkv, d, scale,
-                                               in_dtype == KDA_BF16, o_dtype == KDA_BF16},
+                                               in_dtype == KDA_BF16, o_dtype == KDA_BF16, zero_tail != 0},
                                     static_cast<hipStream_t>(stream)));
 }
 
@@ -307,12 +307,12 @@ size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq, int Hkv, int d) {
 kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
                                const void* o, kda_dtype o_dtype, const float* lse, const void* d_o, void* dq, void* dk,
                                void* dv, kda_dtype grad_dtype, int n, int n_seqs, int Hq, int Hkv, int d, float scale,
-                               void* workspace, size_t workspace_bytes, void* stream) {
+                               int zero_tail, void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(in_dtype) || !dtype_ok(o_dtype) || !dtype_ok(grad_dtype)) return KDA_ERR_DTYPE;
   const kda_status s = heads_ok(n, Hq, Hkv, d);
   if (s == KDA_ERR_SHAPE || n_seqs < 0) return KDA_ERR_SHAPE;
-  if (s != KDA_OK || !isfinite(scale)) return KDA_ERR_UNSUPPORTED;
-  if (n == 0 || n_seqs == 0) return KDA_OK;
+  if (s != KDA_OK || !isfinite(scale) || (zero_tail != 0 && zero_tail != 1)) return KDA_ERR_UNSUPPORTED;
+  if (n == 0 || (n_seqs == 0 && !zero_tail)) return KDA_OK;
   const int64_t nq = int64_t(n) * Hq, nk = int64_t(n) * Hkv;
   if ((int64_t(n) + 127) / 128 * Hq > kMaxGrid || (nq + 31) / 32 > kMaxGrid || nk * d / 1024 >= kMaxGrid)
     return KDA_ERR_SHAPE;
@@ -333,7 +333,7 @@ kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_
   return from_hip(launch_prompt_bwd(PromptBwdArgs{q, k, v, o, d_o, lse, cu_seqlens, static_cast<float*>(workspace),
                                                   static_cast<float*>(workspace) + align4(nq), dq, dk, dv, n, n_seqs,
                                                   Hq, Hkv, d, prompt_bwd_parts(n, Hq, Hkv), scale, in_dtype == KDA_BF16,
-                                                  o_dtype == KDA_BF16, grad_dtype == KDA_BF16},
+                                                  o_dtype == KDA_BF16, grad_dtype == KDA_BF16, zero_tail != 0},
                                     static_cast<hipStream_t>(stream)));
 }
 

@@ -83,6 +83,7 @@ struct PromptArgs {
   int n, nseq, Hq, Hkv, d;
   float scale;
   bool in_bf16, out_bf16;
+  bool zero_tail;  // outputs of rows behind the last sequence: set to zero, or left
 };
 hipError_t launch_prompt_fwd(const PromptArgs& a, hipStream_t st);
 
@@ -96,6 +97,7 @@ struct PromptBwdArgs {
   int n, nseq, Hq, Hkv, d, parts;
   float scale;
   bool in_bf16, o_bf16, grad_bf16;  // d_o is in the inputs' type
+  bool zero_tail;
 };
 int prompt_bwd_parts(int n, int Hq, int Hkv);
 hipError_t launch_prompt_bwd(const PromptBwdArgs& a, hipStream_t st);

@@ -32,6 +32,13 @@ __device__ __forceinline__ int rows_used(const int* cu, int nseq, int n) {
   return e < 0 ? 0 : (e > n ? n : e);
 }
 
+// Zeroes rows [first, last) of one head, by all threads of a workgroup of 256.
+template <typename T, int D>
+__device__ __forceinline__ void zero_rows(T* out, int64_t stride, int first, int last, int tid) {
+  for (int e = tid; e < (last - first) * (D / 4); e += 256)
+    store4(out + (first + e / (D / 4)) * stride + 4 * (e % (D / 4)), f32x4{0, 0, 0, 0});
+}
+
 // ROWS rows of D elements copied from memory into a Tile, without registers in between.  The LDS
 // side of such a copy is one run of 1024 bytes per wavefront, so each lane picks the source chunk
 // that belongs at its place.  Rows at or past `last` repeat row `last - 1`: no row outside

@@ -28,7 +28,12 @@ constexpr int BR = 64;   // walked rows
 
 // D [n, Hq]: eight lanes a row of a head.
 template <typename TO, typename TD>
-__global__ __launch_bounds__(256) void prompt_dot_kernel(const TO* o, const TD* d_o, float* D, int64_t rows, int d) {
+__global__ __launch_bounds__(256) void prompt_dot_kernel(const PromptBwdArgs a) {
+  const TO* o = static_cast<const TO*>(a.o);
+  const TD* d_o = static_cast<const TD*>(a.d_o);
+  float* D = a.D;
+  const int d = a.d;
+  const int64_t rows = int64_t(rows_used(a.cu, a.nseq, a.n)) * a.Hq;
   const int64_t r = int64_t(blockIdx.x) * 32 + threadIdx.x / 8;
   const int part = threadIdx.x % 8;
   float s = 0.f;
@@ -59,6 +64,11 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
   const int kvh = ht.head / a.parts, part = ht.head % a.parts;
   const int c0 = ht.tile * BM;  // keys with the most rows first
   const int used = rows_used(a.cu, a.nseq, a.n);
+  if (a.zero_tail && a.parts == 1 && c0 + BM > used) {
+    const int first = c0 > used ? c0 : used, last = c0 + BM < a.n ? c0 + BM : a.n;
+    zero_rows<TG, D>(static_cast<TG*>(a.dk) + int64_t(kvh) * D, int64_t(a.Hkv) * D, first, last, tid);
+    zero_rows<TG, D>(static_cast<TG*>(a.dv) + int64_t(kvh) * D, int64_t(a.Hkv) * D, first, last, tid);
+  }
   if (c0 >= used) return;
   const int GP = a.Hq / (a.Hkv * a.parts), h0 = kvh * (a.Hq / a.Hkv) + part * GP;  // this part's query heads
   const int64_t qst = int64_t(a.Hq) * D, kst = int64_t(a.Hkv) * D;
@@ -182,6 +192,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   const int head = ht.head, tile = ntile - 1 - ht.tile;
   const int r0 = tile * BM;
   const int used = rows_used(a.cu, a.nseq, a.n);
+  if (a.zero_tail && r0 + BM > used)
+    zero_rows<TG, D>(static_cast<TG*>(a.dq) + int64_t(head) * D, int64_t(a.Hq) * D, r0 > used ? r0 : used,
+                     r0 + BM < a.n ? r0 + BM : a.n, tid);
   if (r0 >= used) return;
   const int kvh = head / (a.Hq / a.Hkv);
   const int64_t qst = int64_t(a.Hq) * D, kst = int64_t(a.Hkv) * D;
@@ -275,9 +288,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
 template <typename TG>
 __global__ __launch_bounds__(256) void prompt_join_kernel(const PromptBwdArgs a, int64_t count) {
   const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= rows_used(a.cu, a.nseq, a.n) * int64_t(a.Hkv) * a.d) return;
+  const bool tail = i >= rows_used(a.cu, a.nseq, a.n) * int64_t(a.Hkv) * a.d;
+  if (i >= count || (tail && !a.zero_tail)) return;
   f32x4 x = {0, 0, 0, 0}, y = x;
-  for (int p = 0; p < a.parts; ++p) {
+  for (int p = 0; p < (tail ? 0 : a.parts); ++p) {
     x += *reinterpret_cast<const f32x4*>(a.part + 2 * p * count + i);
     y += *reinterpret_cast<const f32x4*>(a.part + (2 * p + 1) * count + i);
   }
@@ -289,10 +303,8 @@ template <typename TO>
 hipError_t launch_dot_o(const PromptBwdArgs& a, hipStream_t st) {
   const int64_t rows = int64_t(a.n) * a.Hq;
   const dim3 grid(uint32_t((rows + 31) / 32));
-  if (a.in_bf16)
-    prompt_dot_kernel<<<grid, 256, 0, st>>>(static_cast<const TO*>(a.o), static_cast<const bf16_t*>(a.d_o), a.D, rows, a.d);
-  else
-    prompt_dot_kernel<<<grid, 256, 0, st>>>(static_cast<const TO*>(a.o), static_cast<const float*>(a.d_o), a.D, rows, a.d);
+  if (a.in_bf16) prompt_dot_kernel<TO, bf16_t><<<grid, 256, 0, st>>>(a);
+  else prompt_dot_kernel<TO, float><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

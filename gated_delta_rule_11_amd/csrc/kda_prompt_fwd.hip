@@ -80,6 +80,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
   const int head = ht.head, tile = ntile - 1 - ht.tile;  // long rows first
   const int r0 = tile * BM;
   const int used = rows_used(a.cu, a.nseq, a.n);
+  if (a.zero_tail && r0 + BM > used) {
+    const int first = r0 > used ? r0 : used, last = r0 + BM < a.n ? r0 + BM : a.n;
+    zero_rows<TO, D>(static_cast<TO*>(a.o) + int64_t(head) * D, int64_t(a.Hq) * D, first, last, tid);
+    if (a.lse && first + tid < last) a.lse[int64_t(first + tid) * a.Hq + head] = 0.f;
+  }
   if (r0 >= used) return;
   const int kvh = head / (a.Hq / a.Hkv);
   const int64_t kst = int64_t(a.Hkv) * D;

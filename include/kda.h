@@ -415,14 +415,15 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, k
  *   cu_seqlens [n_seqs+1] int32, device memory, not decreasing, from 0 to at
  *       most n: sequence s has rows cu_seqlens[s] .. cu_seqlens[s+1] - 1.
  *       Sequences may be empty.  Rows at or past the last entry belong to no
- *       sequence: they are not read, and their outputs are left as they were.
+ *       sequence: they are not read; their outputs are left as they were
+ *       (zero_tail == 0) or set to zero (zero_tail == 1).
  *       (Entries outside [0, n] or out of order give meaningless results, but
  *       no access outside the arrays.)
  *   o   [n,Hq,d] o_dtype (written)       lse [n,Hq] fp32 (written) or NULL
  */
 kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
                                void* o, kda_dtype o_dtype, float* lse, int n, int n_seqs, int Hq, int Hkv, int d,
-                               float scale, void* stream);
+                               float scale, int zero_tail, void* stream);
 
 /*
  * kda_attn_prompt_bwd -- its gradients, from the forward's o and lse.
@@ -437,7 +438,7 @@ size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq, int Hkv, int d);
 kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
                                const void* o, kda_dtype o_dtype, const float* lse, const void* d_o, void* dq, void* dk,
                                void* dv, kda_dtype grad_dtype, int n, int n_seqs, int Hq, int Hkv, int d, float scale,
-                               void* workspace, size_t workspace_bytes, void* stream);
+                               int zero_tail, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * ---------------------------------------------------------------------------

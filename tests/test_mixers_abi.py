@@ -36,13 +36,14 @@ def lin_step(L, q=P(0), k=P(1), v=P(2), it=BF16, g=P(3), ph=0, S_in=P(4), S_out=
 
 
 def prompt_fwd(L, q=P(0), k=P(1), v=P(2), it=BF16, cu=P(3), o=P(4), ot=F32, lse=P(5), n=100, ns=2, Hq=4, Hkv=2, d=64,  # noqa: F811
-               scale=1.0):
-    return L.kda_attn_prompt_fwd(q, k, v, it, cu, o, ot, lse, n, ns, Hq, Hkv, d, scale, None)
+               scale=1.0, tail=0):
+    return L.kda_attn_prompt_fwd(q, k, v, it, cu, o, ot, lse, n, ns, Hq, Hkv, d, scale, tail, None)
 
 
 def prompt_bwd(L, q=P(0), k=P(1), v=P(2), it=BF16, cu=P(3), o=P(4), ot=F32, lse=P(5), do=P(6), dq=P(7), dk=P(8), dv=P(9),  # noqa: F811
-               gt=F32, n=100, ns=2, Hq=4, Hkv=2, d=64, scale=1.0, ws=P(10), wsb=HUGE):
-    return L.kda_attn_prompt_bwd(q, k, v, it, cu, o, ot, lse, do, dq, dk, dv, gt, n, ns, Hq, Hkv, d, scale, ws, wsb, None)
+               gt=F32, n=100, ns=2, Hq=4, Hkv=2, d=64, scale=1.0, tail=0, ws=P(10), wsb=HUGE):
+    return L.kda_attn_prompt_bwd(q, k, v, it, cu, o, ot, lse, do, dq, dk, dv, gt, n, ns, Hq, Hkv, d, scale, tail, ws, wsb,
+                                 None)
 
 
 def append(L, k=P(0), v=P(1), it=BF16, cu=P(2), ctx=P(3), table=P(4), kc=P(5), vc=P(6), ks=P(7), vs=P(8), n=10, N=2, Hkv=2,  # noqa: F811
@@ -114,6 +115,7 @@ def test_prompt_refusals(L, call):  # noqa: F811
     assert call(L, n=(1 << 31) - 1, Hq=1, Hkv=1) == ERR_SHAPE
     assert call(L, d=32) == ERR_UNSUPPORTED and call(L, d=96) == ERR_UNSUPPORTED and call(L, Hq=5) == ERR_UNSUPPORTED
     assert call(L, Hq=2, Hkv=4) == ERR_UNSUPPORTED and call(L, scale=math.inf) == ERR_UNSUPPORTED
+    assert call(L, tail=2) == ERR_UNSUPPORTED
     for x in ("q", "k", "v", "cu", "o"):
         assert call(L, **{x: None}) == ERR_NULL
         assert call(L, **{x: P(20, 2)}) == ERR_ALIGN
