@@ -16,6 +16,8 @@
 // write their sums transposed.  D comes from a small kernel before.  The sums are fp32; with bf16
 // elements P and dS are rounded to bf16 for the products that follow, 2^-9 relative each, as the
 // gradients may be.
+#include <type_traits>
+
 #include "kda_prompt.hpp"
 
 namespace kda {
@@ -79,6 +81,7 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
   const int kr = kj < used ? kj : used - 1;
   const int end = span_of(a.cu, a.nseq, a.n, kr).end;
   const int emin = __shfl(end, 0), emax = __shfl(end, 31);
+  const int lim = kj < used ? (end < hi ? end : hi) : kj;
   const float c = a.scale * kLog2e;
 
   F kf[NK], vf[NK];
@@ -128,20 +131,27 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
         s = O::mma32(TD::row8_32(qrow, sub, kk), kf[kk], s);
         dp = O::mma32(TD::row8_32(orow, sub, kk), vf[kk], dp);
       }
-      const bool whole = s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi;
+      auto probabilities = [&](auto whole) {
 #pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int rr = 32 * sub + 8 * r4 + 4 * h2;
-        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + rr), D4 = *reinterpret_cast<const f32x4*>(Ds + rr);
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const int rr = 32 * sub + 8 * r4 + 4 * h2;
+          const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + rr), D4 = *reinterpret_cast<const f32x4*>(Ds + rr);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = i0 + rr + j, e = 4 * r4 + j;
-          const bool in = whole || (i >= kj && i < end && i < hi);
-          const float p = in ? fast_exp2(s[e] * c - l4[j] * kLog2e) : 0.f;
-          s[e] = p;
-          dp[e] = in ? p * (dp[e] - D4[j]) : 0.f;
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * r4 + j;
+            float p = fast_exp2(s[e] * c - l4[j] * kLog2e), d = p * (dp[e] - D4[j]);
+            if constexpr (!decltype(whole)::value) {  // rows kj .. lim - 1 see the key
+              const bool in = unsigned(i0 + rr + j - kj) < unsigned(lim - kj);
+              p = in ? p : 0.f;
+              d = in ? d : 0.f;
+            }
+            s[e] = p;
+            dp[e] = d;
+          }
         }
-      }
+      };
+      if (s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi) probabilities(std::true_type{});
+      else probabilities(std::false_type{});
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const F pf = frag_of<T>(s, ks), df = frag_of<T>(dp, ks);
@@ -250,14 +260,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
         s = O::mma32(TD::row8_32(krow, j, kk), qf[kk], s);
         dp = O::mma32(TD::row8_32(vrow, j, kk), of[kk], dp);
       }
-      const bool whole = s0 + 31 <= w0 && s0 >= smax;
+      auto gradients = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = s0 + crow(i, h2);
-        const bool in = whole || (key <= qi && key >= start);
-        const float p = in ? fast_exp2(s[i] * c - ls) : 0.f;
-        dp[i] = in ? p * (dp[i] - Di) : 0.f;
-      }
+        for (int i = 0; i < 16; ++i) {
+          const float p = fast_exp2(s[i] * c - ls);
+          dp[i] = p * (dp[i] - Di);
+          if constexpr (!decltype(whole)::value)  // the row sees keys start .. qi
+            dp[i] = unsigned(s0 + crow(i, h2) - start) <= unsigned(qi - start) ? dp[i] : 0.f;
+        }
+      };
+      if (s0 + 31 <= w0 && s0 >= smax) gradients(std::true_type{});
+      else gradients(std::false_type{});
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const F df = frag_of<T>(dp, ks);

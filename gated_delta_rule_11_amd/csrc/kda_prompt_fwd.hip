@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_fwd_kernel
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int key = k0 + 32 * j + crow(i, h2);
-            s[j][i] = key <= qi && key >= start ? s[j][i] : -INFINITY;
+            s[j][i] = unsigned(key - start) <= unsigned(qi - start) ? s[j][i] : -INFINITY;
           }
       }
       float mt = s[0][0];
