@@ -333,7 +333,10 @@ __device__ __forceinline__ void lds_copy4(const void* base, uint32_t offset, uin
 template <int LATER = 0>  // all but the last LATER copies of this wavefront
 __device__ __forceinline__ void copies_landed() {
   static_assert(LATER < 64, "the counter's range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+  // the builtin, so that the compiler knows that its own earlier loads are there too and does not
+  // wait for them, and the copies with them, inside the loop
+  __builtin_amdgcn_s_waitcnt((LATER & 15) | (LATER >> 4) << 14 | 0x0f70);
+  asm volatile("" ::: "memory");
 }
 // A barrier for LDS contents: waits for this wavefront's LDS accesses, not for its stores to memory.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }

@@ -28,6 +28,18 @@ constexpr int BM = 128;  // owned rows or keys
 constexpr int BN = 64;   // walked keys
 constexpr int BR = 64;   // walked rows
 
+// Asks for N products with V vector instructions, and the LDS reads of two fragments, after each.
+template <int N, int V>
+__device__ __forceinline__ void interleave() {
+  __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+  }
+}
+
 // D [n, Hq]: eight lanes a row of a head.
 template <typename TO, typename TD>
 __global__ __launch_bounds__(256) void prompt_dot_kernel(const PromptBwdArgs a) {
@@ -48,8 +60,15 @@ __global__ __launch_bounds__(256) void prompt_dot_kernel(const PromptBwdArgs a) 
   if (r < rows && part == 0) D[r] = s;
 }
 
+// Tiles of rows in rotation: one workgroup's registers fill a compute unit, so nothing else hides the
+// copies' latency, and the LDS is its own.
 template <typename T, int D>
-constexpr size_t kv_lds() { return size_t(2) * 2 * BR * D * sizeof(T) + 2 * 2 * BR * sizeof(float); }
+struct KvShape {
+  static constexpr int kTile = 2 * BR * D * int(sizeof(T)) + 4 * BR * 4;  // Q, dO, lse, D and two unused
+  static constexpr int NS = 4 * kTile <= 160 * 1024 ? 4 : 2;
+  static constexpr int kCopies = 2 * BR / (64 / Tile<T, D>::CH * 4) + 1;  // of each wavefront for a tile
+  static constexpr size_t lds = size_t(NS) * kTile;
+};
 
 template <typename T, typename TG, int D>
 __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs a, int ntile) {
@@ -58,8 +77,9 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
   using TD = Tile<T, D>;
   constexpr int NK = D / 16, ND = D / 32;
   extern __shared__ __align__(16) unsigned char smem[];
-  T* const buf = reinterpret_cast<T*>(smem);                             // [2][Q tile, dO tile]
-  float* const stat = reinterpret_cast<float*>(buf + 2 * 2 * BR * D);    // [2][lse, D]
+  using W = KvShape<T, D>;
+  T* const buf = reinterpret_cast<T*>(smem);                                // [NS][Q tile, dO tile]
+  float* const stat = reinterpret_cast<float*>(buf + W::NS * 2 * BR * D);   // [NS][lse, D, unused]
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h2 = lane >> 5, l32 = lane & 31;
   const HeadTile ht = head_tile(blockIdx.x, a.Hkv * a.parts);
@@ -102,65 +122,99 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
   const int nt = (hi - c0 + BR - 1) / BR, steps = nt * GP;
   auto fetch = [&](int t) {
     const int head = h0 + t / nt, i0 = c0 + (t % nt) * BR;
-    T* qb = buf + (t & 1) * 2 * BR * D;
+    T* qb = buf + (t % W::NS) * 2 * BR * D;
     copy_rows<T, BR, D, 4>(qb, static_cast<const T*>(a.q) + int64_t(head) * D, qst, i0, hi, wave, lane);
     copy_rows<T, BR, D, 4>(qb + BR * D, static_cast<const T*>(a.d_o) + int64_t(head) * D, qst, i0, hi, wave, lane);
-    if (wave < 2) {  // lse by the first wavefront, D by the second
-      const int r = i0 + lane < hi ? i0 + lane : hi - 1;
-      lds_copy4((wave ? a.D : a.lse) + int64_t(r) * a.Hq + head, lds_offset(stat + (t & 1) * 2 * BR + wave * BR));
-    }
+    // lse by the first wavefront, D by the second; the others repeat them into unused places, so that
+    // every wavefront has the same number of copies to count
+    const int r = i0 + lane < hi ? i0 + lane : hi - 1;
+    lds_copy4((wave & 1 ? a.D : a.lse) + int64_t(r) * a.Hq + head, lds_offset(stat + (t % W::NS) * 4 * BR + wave * BR));
   };
-  fetch(0);
+#pragma unroll
+  for (int i = 0; i < W::NS - 1; ++i)
+    if (i < steps) fetch(i);
   for (int t = 0; t < steps; ++t) {
-    copies_done();
-    if (t + 1 < steps) fetch(t + 1);
-    const T* Qs = buf + (t & 1) * 2 * BR * D;
+    if (t + W::NS - 2 < steps) copies_landed<(W::NS - 2) * W::kCopies>();  // tile t is there
+    else copies_landed();
+    lds_barrier();
+    if (t + W::NS - 1 < steps) fetch(t + W::NS - 1);
+    const T* Qs = buf + (t % W::NS) * 2 * BR * D;
     const T* Os = Qs + BR * D;
-    const float* ls = stat + (t & 1) * 2 * BR;
+    const float* ls = stat + (t % W::NS) * 4 * BR;
     const float* Ds = ls + BR;
     const uint32_t qrow = TD::at(Qs) + brow, orow = TD::at(Os) + brow, qcol = TD::at(Qs) + bcol, ocol = TD::at(Os) + bcol;
     const int i0 = c0 + (t % nt) * BR;
-#pragma unroll
-    for (int sub = 0; sub < BR / 32; ++sub) {
-      const int s0 = i0 + 32 * sub;
-      // some row at or past the wavefront's first key, before its last key's end
-      if (w0 >= used || s0 + 31 < w0 || s0 >= emax || s0 >= hi) continue;
-      f32x16 s = zero16(), dp = zero16();
+    f32x16 s[2], dp[2];
+    auto scores = [&](int sub) {
+      s[sub] = dp[sub] = zero16();
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
-        s = O::mma32(TD::row8_32(qrow, sub, kk), kf[kk], s);
-        dp = O::mma32(TD::row8_32(orow, sub, kk), vf[kk], dp);
+        s[sub] = O::mma32(TD::row8_32(qrow, sub, kk), kf[kk], s[sub]);
+        dp[sub] = O::mma32(TD::row8_32(orow, sub, kk), vf[kk], dp[sub]);
       }
-      auto probabilities = [&](auto whole) {
+    };
+    auto probabilities = [&](int sub, auto whole) {
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const int rr = 32 * sub + 8 * r4 + 4 * h2;
-          const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + rr), D4 = *reinterpret_cast<const f32x4*>(Ds + rr);
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const int rr = 32 * sub + 8 * r4 + 4 * h2;
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + rr), D4 = *reinterpret_cast<const f32x4*>(Ds + rr);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 4 * r4 + j;
-            float p = fast_exp2(s[e] * c - l4[j] * kLog2e), d = p * (dp[e] - D4[j]);
-            if constexpr (!decltype(whole)::value) {  // rows kj .. lim - 1 see the key
-              const bool in = unsigned(i0 + rr + j - kj) < unsigned(lim - kj);
-              p = in ? p : 0.f;
-              d = in ? d : 0.f;
-            }
-            s[e] = p;
-            dp[e] = d;
+        for (int j = 0; j < 4; ++j) {
+          const int e = 4 * r4 + j;
+          float p = fast_exp2(s[sub][e] * c - l4[j] * kLog2e), d = p * (dp[sub][e] - D4[j]);
+          if constexpr (!decltype(whole)::value) {  // rows kj .. lim - 1 see the key
+            const bool in = unsigned(i0 + rr + j - kj) < unsigned(lim - kj);
+            p = in ? p : 0.f;
+            d = in ? d : 0.f;
           }
+          s[sub][e] = p;
+          dp[sub][e] = d;
         }
-      };
-      if (s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi) probabilities(std::true_type{});
-      else probabilities(std::false_type{});
+      }
+    };
+    auto products = [&](int sub) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const F pf = frag_of<T>(s, ks), df = frag_of<T>(dp, ks);
+        const F pf = frag_of<T>(s[sub], ks), df = frag_of<T>(dp[sub], ks);
         const int rr = 32 * sub + 16 * ks;
 #pragma unroll
         for (int i = 0; i < ND; ++i) {
           dv[i] = O::mma32(TD::col44_32(ocol, rr, i), pf, dv[i]);
           dk[i] = O::mma32(TD::col44_32(qcol, rr, i), df, dk[i]);
         }
+      }
+    };
+    if (i0 >= w0 + 31 && i0 + BR <= emin && i0 + BR <= hi) {
+      // Every row sees every key.  One wavefront per SIMD fits, so its own products have to run beside
+      // its own exponentials: those of one half of the rows beside the other half's.
+      scores(0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      scores(1);
+      probabilities(0, std::true_type{});
+      if constexpr (sizeof(T) == 2) interleave<2 * NK, 9>();
+      __builtin_amdgcn_sched_barrier(0);
+      products(0);
+      probabilities(1, std::true_type{});
+      if constexpr (sizeof(T) == 2) interleave<4 * ND, 9>();
+      __builtin_amdgcn_sched_barrier(0);
+      products(1);
+    } else {
+#pragma unroll
+      for (int sub = 0; sub < BR / 32; ++sub) {
+        const int s0 = i0 + 32 * sub;
+        // some row at or past the wavefront's first key, before its last key's end
+        if (w0 >= used || s0 + 31 < w0 || s0 >= emax || s0 >= hi) continue;
+        scores(sub);
+        if (s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi) probabilities(sub, std::true_type{});
+        else probabilities(sub, std::false_type{});
+        products(sub);
       }
     }
   }
@@ -324,7 +378,7 @@ hipError_t launch_dot_o(const PromptBwdArgs& a, hipStream_t st) {
 template <typename T, typename TG, int D>
 hipError_t launch_dkv(const PromptBwdArgs& a, int ntile, hipStream_t st) {
   auto kern = prompt_dkv_kernel<T, TG, D>;
-  constexpr size_t lds = kv_lds<T, D>();
+  constexpr size_t lds = KvShape<T, D>::lds;
   static_assert(lds <= 160 * 1024, "LDS of a compute unit");
   static std::atomic<uint64_t> done{0};
   const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), int(lds), done);
