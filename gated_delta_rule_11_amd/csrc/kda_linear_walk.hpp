@@ -376,12 +376,14 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
         for (int kk = 0; kk < NKK; ++kk) {
           const f32x4 hi = 2 * kk + 1 < NKT ? S[(2 * kk + 1) % NKT] : f32x4{0, 0, 0, 0};
           const Parts<T, kOut, 8> sf(__builtin_shufflevector(S[2 * kk], hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          // a result's next addend waits for it: sums over different results in turn
+          F qf[TT];
 #pragma unroll
-          for (int tt = 0; tt < TT; ++tt) {
-            const F qf = TK::row44_16(qb, tt, kk);
+          for (int tt = 0; tt < TT; ++tt) qf[tt] = TK::row44_16(qb, tt, kk);
 #pragma unroll
-            for (int i = kOut - 1; i >= 0; --i) acc[tt] = O::mma16(part_of(sf, i), qf, acc[tt]);
-          }
+          for (int i = kOut - 1; i >= 0; --i)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) acc[tt] = O::mma16(part_of(sf, i), qf[tt], acc[tt]);
         }
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) acc[tt] *= ga[2 * C + 16 * tt + l16];
@@ -395,25 +397,29 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
         const float* w = ga + 3 * C + 32 * u + 8 * g4;
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(w), w1 = *reinterpret_cast<const f32x4*>(w + 4);
         const Parts<T, kExact, 8> x(O::unpack(vf[u]) * __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7));
+        F kf[NKT];
 #pragma unroll
-        for (int i = 0; i < NKT; ++i) {
-          const F kf = TK::col8_16(kb, u, i);
+        for (int i = 0; i < NKT; ++i) kf[i] = TK::col8_16(kb, u, i);
 #pragma unroll
-          for (int j = kExact - 1; j >= 0; --j) S[i] = O::mma16(kf, part_of(x, j), S[i]);
-        }
+        for (int j = kExact - 1; j >= 0; --j)
+#pragma unroll
+          for (int i = 0; i < NKT; ++i) S[i] = O::mma16(kf[i], part_of(x, j), S[i]);
       }
 
       if constexpr (OUT > 0) {
         lds_barrier();  // the scores are there
         const uint32_t pb = TP::at(P) + prow;
 #pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = kOut - 1; i >= 0; --i)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+              if (REV ? u < tt / 2 : u > tt / 2) continue;
+              acc[tt] = O::mma16(vf[u], TP::row8_16(pb + i * W::kP1, tt, u), acc[tt]);
+            }
+#pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (REV ? u < tt / 2 : u > tt / 2) continue;
-#pragma unroll
-            for (int i = kOut - 1; i >= 0; --i) acc[tt] = O::mma16(vf[u], TP::row8_16(pb + i * W::kP1, tt, u), acc[tt]);
-          }
           const int64_t t = t0 + 16 * tt + l16;
           f32x4 x = acc[tt];
           if constexpr (!REV) x *= a.scale;
