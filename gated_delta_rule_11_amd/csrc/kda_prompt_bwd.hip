@@ -27,6 +27,9 @@ namespace {
 constexpr int BM = 128;  // owned rows or keys
 constexpr int BN = 64;   // walked keys
 constexpr int BR = 64;   // walked rows
+// Rows closer than this to their sequence's start have D formed anew where o is rounded: behind it D's
+// error, 2^-9 |do| |o| with |o| falling as 1 / sqrt(keys), is lost in dS' own rounding.
+constexpr int kNear = 256;
 
 // Asks for N products with V vector instructions, and the LDS reads of two fragments, after each.
 template <int N, int V>
@@ -273,7 +276,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   const int start = span_of(a.cu, a.nseq, a.n, qr).start;
   const int smin = __shfl(start, 0), smax = __shfl(start, 31);
   const float c = a.scale * kLog2e;
-  const float ls = a.lse[int64_t(qr) * a.Hq + head] * kLog2e, Di = a.D[int64_t(qr) * a.Hq + head];
+  const float ls = a.lse[int64_t(qr) * a.Hq + head] * kLog2e;
+  float Di = a.D[int64_t(qr) * a.Hq + head];
 
   F qf[NK], of[NK];
   {
@@ -290,53 +294,73 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   for (int i = 0; i < ND; ++i) dq[i] = zero16();
 
   const uint32_t brow = TD::b_row8_32(lane), bcol = TD::b_col44_32(lane);
-  const int nt = (hi - lo + BN - 1) / BN;
-  auto fetch = [&](int t) {
-    T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
-    copy_rows<T, BN, D, 4>(kb, kp, kst, lo + t * BN, hi, wave, lane);
-    copy_rows<T, BN, D, 4>(kb + BN * D, vp, kst, lo + t * BN, hi, wave, lane);
-  };
-  fetch(0);
-  for (int t = 0; t < nt; ++t) {
-    copies_done();
-    if (DB && t + 1 < nt) fetch(t + 1);
-    const T* Ks = buf + (DB ? (t & 1) * 2 * BN * D : 0);
-    const T* Vs = Ks + BN * D;
-    const uint32_t krow = TD::at(Ks) + brow, vrow = TD::at(Vs) + brow, kcol = TD::at(Ks) + bcol;
-    const int k0 = lo + t * BN;
+  // Walks the keys from `from` on: the rows' dq, or (EXACT) the sums of P dP.
+  float dsum = 0.f;
+  auto walk = [&](int from, auto exact) {
+    constexpr bool EXACT = decltype(exact)::value;
+    const int nt = (hi - from + BN - 1) / BN;
+    auto fetch = [&](int t) {
+      T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
+      copy_rows<T, BN, D, 4>(kb, kp, kst, from + t * BN, hi, wave, lane);
+      copy_rows<T, BN, D, 4>(kb + BN * D, vp, kst, from + t * BN, hi, wave, lane);
+    };
+    fetch(0);
+    for (int t = 0; t < nt; ++t) {
+      copies_done();
+      if (DB && t + 1 < nt) fetch(t + 1);
+      const T* Ks = buf + (DB ? (t & 1) * 2 * BN * D : 0);
+      const T* Vs = Ks + BN * D;
+      const uint32_t krow = TD::at(Ks) + brow, vrow = TD::at(Vs) + brow, kcol = TD::at(Ks) + bcol;
+      const int k0 = from + t * BN;
 #pragma unroll
-    for (int j = 0; j < BN / 32; ++j) {
-      const int s0 = k0 + 32 * j;
-      if (wlast < w0 || s0 > wlast || s0 + 32 <= smin) continue;
-      f32x16 s = zero16(), dp = zero16();
+      for (int j = 0; j < BN / 32; ++j) {
+        const int s0 = k0 + 32 * j;
+        if (wlast < w0 || s0 > wlast || s0 + 32 <= smin) continue;
+        f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-        s = O::mma32(TD::row8_32(krow, j, kk), qf[kk], s);
-        dp = O::mma32(TD::row8_32(vrow, j, kk), of[kk], dp);
-      }
-      auto gradients = [&](auto whole) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = fast_exp2(s[i] * c - ls);
-          dp[i] = p * (dp[i] - Di);
-          if constexpr (!decltype(whole)::value)  // the row sees keys start .. qi
-            dp[i] = unsigned(s0 + crow(i, h2) - start) <= unsigned(qi - start) ? dp[i] : 0.f;
+        for (int kk = 0; kk < NK; ++kk) {
+          s = O::mma32(TD::row8_32(krow, j, kk), qf[kk], s);
+          dp = O::mma32(TD::row8_32(vrow, j, kk), of[kk], dp);
         }
-      };
-      if (s0 + 31 <= w0 && s0 >= smax) gradients(std::true_type{});
-      else gradients(std::false_type{});
+        auto gradients = [&](auto whole) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const F df = frag_of<T>(dp, ks);
+          for (int i = 0; i < 16; ++i) {
+            const float p = fast_exp2(s[i] * c - ls);
+            dp[i] = p * (EXACT ? dp[i] : dp[i] - Di);
+            if constexpr (!decltype(whole)::value)  // the row sees keys start .. qi
+              dp[i] = unsigned(s0 + crow(i, h2) - start) <= unsigned(qi - start) ? dp[i] : 0.f;
+            if constexpr (EXACT) dsum += dp[i];
+          }
+        };
+        if (s0 + 31 <= w0 && s0 >= smax) gradients(std::true_type{});
+        else gradients(std::false_type{});
+        if constexpr (!EXACT) {
 #pragma unroll
-        for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44_32(kcol, 32 * j + 16 * ks, i), df, dq[i]);
+          for (int ks = 0; ks < 2; ++ks) {
+            const F df = frag_of<T>(dp, ks);
+#pragma unroll
+            for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44_32(kcol, 32 * j + 16 * ks, i), df, dq[i]);
+          }
+        }
+      }
+      if (!DB) {
+        __syncthreads();
+        if (t + 1 < nt) fetch(t + 1);
       }
     }
-    if (!DB) {
-      __syncthreads();
-      if (t + 1 < nt) fetch(t + 1);
+  };
+  // Near its sequence's start a row has few keys, dP is close to D, and D from the rounded o costs
+  // dS its accuracy (the first row's dS is zero, and would be half a rounding of do . o).  There D is
+  // formed as the sum of P dP, before dk and dv read it.
+  if (a.o_bf16 && span_of(a.cu, a.nseq, a.n, hi - 1).start > r0 - kNear) {
+    walk(lo > r0 - kNear ? lo : r0 - kNear, std::true_type{});
+    lds_barrier();
+    if (qi < used && qi - start < kNear) {
+      Di = sum_halves(dsum);
+      if (h2 == 0) a.D[int64_t(qi) * a.Hq + head] = Di;
     }
   }
+  walk(lo, std::false_type{});
   if (qi < used) {
     TG* p = static_cast<TG*>(a.dq) + int64_t(qi) * qst + int64_t(head) * D;
 #pragma unroll
@@ -397,15 +421,15 @@ hipError_t launch(const PromptBwdArgs& a, hipStream_t st) {
   if (e == hipSuccess) e = a.o_bf16 ? launch_dot_o<bf16_t>(a, st) : launch_dot_o<float>(a, st);
   if (e != hipSuccess) return e;
   const int ntile = (a.n + BM - 1) / BM;
-  e = a.parts == 1 ? launch_dkv<T, TG, D>(a, ntile, st) : launch_dkv<T, float, D>(a, ntile, st);
+  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, lds, st>>>(a, ntile);  // may refine D
+  e = hipGetLastError();
+  if (e == hipSuccess) e = a.parts == 1 ? launch_dkv<T, TG, D>(a, ntile, st) : launch_dkv<T, float, D>(a, ntile, st);
   if (e == hipSuccess && a.parts > 1) {
     const int64_t count = int64_t(a.n) * a.Hkv * a.d;
     prompt_join_kernel<TG><<<dim3(uint32_t((count / 4 + 255) / 256)), 256, 0, st>>>(a, count);
     e = hipGetLastError();
   }
-  if (e != hipSuccess) return e;
-  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, lds, st>>>(a, ntile);
-  return hipGetLastError();
+  return e;
 }
 
 template <typename T, int D>

@@ -188,3 +188,29 @@ def test_no_sequences():
         assert not o.any() and not any(x.any() for x in got.values())
     o, _ = kda.attn_prompt_fwd(q[:0], k[:0], k[:0], c)
     assert o.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradients_at_a_sequences_start(dtype):
+    """A sequence of one row has probability one, whatever its score: dq and dk are zero but for fp32
+    roundings of do . v (64 terms and a few), also where o comes rounded to bf16; and short sequences'
+    dq and dk have the relative error of dS' rounding and their own, 2^-8 each at most."""
+    d = inputs([1] * 40, 4, 2, 64, dtype)
+    g = on(d)
+    o, lse = kda.attn_prompt_fwd(g["q"], g["k"], g["v"], g["cu"], o_dtype=dtype)
+    got = kda.attn_prompt_bwd(g["q"], g["k"], g["v"], g["cu"], o, lse, g["do"])
+    torch.cuda.synchronize()
+    f = {x: mx.f64(d[x]).abs() for x in ("q", "k", "v", "do")}
+    dov = (f["do"].view(40, 2, 2, 64) * f["v"][:, :, None]).sum(-1)  # [n, Hkv, group]
+    bound = 128 * 2.0 ** -24 * 64 ** -0.5
+    assert bool((mx.f64(got["dq"]).view(40, 2, 2, 64).abs() <= bound * dov[..., None] * f["k"][:, :, None] + 1e-30).all())
+    dk_mag = (dov[..., None] * f["q"].view(40, 2, 2, 64)).sum(2)
+    assert bool((mx.f64(got["dk"]).abs() <= bound * dk_mag + 1e-30).all())
+    d = inputs([3, 9, 2, 17, 30, 4], 4, 2, 64, dtype)
+    g = on(d)
+    o, lse = kda.attn_prompt_fwd(g["q"], g["k"], g["v"], g["cu"], o_dtype=dtype)
+    got = kda.attn_prompt_bwd(g["q"], g["k"], g["v"], g["cu"], o, lse, g["do"], grad_dtype=dtype)
+    torch.cuda.synchronize()
+    want, _ = mx.prompt(*(mx.f64(d[x]) for x in ("q", "k", "v")), d["cu"], 64 ** -0.5, mx.f64(d["do"]))
+    for x in ("dq", "dk", "dv"):
+        assert float((mx.f64(got[x]) - want[x]).norm() / want[x].norm()) <= 2 * (mx.U[dtype] if dtype == BF else 64 * mx.U[F32]), x
