@@ -25,16 +25,27 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinearScanArgs a
   }
 }
 
+// The sum over a workgroup of 256, in 64 bits and a fixed order, in every thread.
+__device__ __forceinline__ double sum_256(double v, double* lds) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
 // dg of one block of chunks (kBlockChunks of C tokens, one token a thread): the block's boundary
-// term and the sum from each token to the block's end, in 64 bits.
-__global__ __launch_bounds__(512) void linear_dg_kernel(const LinearDgArgs a) {
-  __shared__ double sums[8];
+// term and the sum from each token to the block's end, in 64 bits.  For a decay per head only
+// their sum over the block is kept.
+__global__ __launch_bounds__(256) void linear_dg_kernel(const LinearDgArgs a) {
+  __shared__ double sums[4], total[4];
   const int nblk = (a.T + a.block - 1) / a.block;
   const int64_t bh = blockIdx.x / nblk;
   const int blk = blockIdx.x % nblk, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t t = int64_t(blk) * a.block + tid, rows = a.BH * a.T;
+  const bool live = tid < a.block && t < a.T;
   double v = 0.0;
-  if (tid < a.block && t < a.T)
+  if (live)
     for (int p = 0; p < a.parts; ++p) v += double(a.xq[p * rows + bh * a.T + t]) - double(a.xk[p * rows + bh * a.T + t]);
   double edge = 0.0;
   for (int p = 0; p < a.parts; ++p) edge += double(a.bsum[(bh * nblk + blk) * a.parts + p]);
@@ -45,22 +56,23 @@ __global__ __launch_bounds__(512) void linear_dg_kernel(const LinearDgArgs a) {
   }
   if (lane == 0) sums[wave] = v;
   __syncthreads();
-  for (int w = wave + 1; w < 8; ++w) v += sums[w];
-  if (tid < a.block && t < a.T) a.dg[((bh / a.H) * a.T + t) * a.H + bh % a.H] = float(v + edge);
+  for (int w = wave + 1; w < 4; ++w) v += sums[w];
+  v += edge;
+  if (a.block_sum) {
+    v = sum_256(live ? v : 0.0, total);
+    if (tid == 0) a.block_sum[bh * nblk + blk] = v;
+  } else if (live) {
+    a.dg[((bh / a.H) * a.T + t) * a.H + bh % a.H] = float(v);
+  }
 }
 
-// dg [H] from x [rows, H]: one workgroup per head, sums in 64 bits, in a fixed order.
-__global__ __launch_bounds__(256) void linear_dg_sum_kernel(const float* x, float* dg, int64_t rows, int H) {
-  __shared__ double part[256];
+// dg [H] from the blocks' sums [B, H, nblk]: one workgroup per head.
+__global__ __launch_bounds__(256) void linear_dg_sum_kernel(const double* x, float* dg, int64_t B, int H, int64_t nblk) {
+  __shared__ double lds[4];
   double s = 0.0;
-  for (int64_t r = threadIdx.x; r < rows; r += 256) s += double(x[r * H + blockIdx.x]);
-  part[threadIdx.x] = s;
-  __syncthreads();
-  for (int d = 128; d > 0; d >>= 1) {
-    if (int(threadIdx.x) < d) part[threadIdx.x] += part[threadIdx.x + d];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) dg[blockIdx.x] = float(part[0]);
+  for (int64_t i = threadIdx.x; i < B * nblk; i += 256) s += x[((i / nblk) * H + blockIdx.x) * nblk + i % nblk];
+  s = sum_256(s, lds);
+  if (threadIdx.x == 0) dg[blockIdx.x] = float(s);
 }
 
 }  // namespace
@@ -78,12 +90,12 @@ hipError_t launch_linear_scan(const LinearScanArgs& a, hipStream_t st) {
 
 hipError_t launch_linear_dg(const LinearDgArgs& a, hipStream_t st) {
   const int64_t nblk = (a.T + a.block - 1) / a.block;
-  linear_dg_kernel<<<dim3(uint32_t(a.BH * nblk)), 512, 0, st>>>(a);
+  linear_dg_kernel<<<dim3(uint32_t(a.BH * nblk)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_linear_dg_sum(const float* x, float* dg, int64_t rows, int H, hipStream_t st) {
-  linear_dg_sum_kernel<<<dim3(uint32_t(H)), 256, 0, st>>>(x, dg, rows, H);
+hipError_t launch_linear_dg_sum(const double* x, float* dg, int64_t B, int H, int64_t nblk, hipStream_t st) {
+  linear_dg_sum_kernel<<<dim3(uint32_t(H)), 256, 0, st>>>(x, dg, B, H, nblk);
   return hipGetLastError();
 }
 

@@ -84,7 +84,7 @@ bool bwd_grid_ok(int64_t B, int64_t T, int64_t H, bool bf16) {
 }
 
 // Workspace of the backward, in floats: kept states, dot products and boundary terms for dg, one
-// walk's segments at a time, dg per token when g is per head.
+// walk's segments at a time, the blocks' sums of dg (64 bits) when g is per head.
 struct BwdLayout {
   LinearForm fk, fv;  // walks over value columns of dk, and of dv
   int64_t nblk, ckpt, x, bsum, seg, dg, total;
@@ -99,8 +99,8 @@ BwdLayout bwd_layout(int64_t B, int64_t T, int64_t H, int dk, int dv, bool bf16,
   l.x = align4(bh * T * (dk / 16));
   l.bsum = align4(bh * l.nblk * (dk / 16));
   const int64_t a = seg_floats(l.fk, bh, state), b = seg_floats(l.fv, bh, state);
-  l.seg = a > b ? a : b;
-  l.dg = g_head ? align4(B * T * H) : 0;
+  l.seg = align4(a > b ? a : b);
+  l.dg = g_head ? align4(bh * l.nblk * 2) : 0;
   l.total = T > 0 ? l.ckpt + 2 * l.x + l.bsum + l.seg + l.dg : 0;
   return l;
 }
@@ -218,7 +218,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, kda
   float* xk = xq + l.x;
   float* bsum = xk + l.x;
   float* seg = bsum + l.bsum;
-  float* dgt = g_per_head ? seg + l.seg : dg;
+  double* block_sum = g_per_head ? reinterpret_cast<double*>(seg + l.seg) : nullptr;
   LinearArgs w{};
   w.B = B; w.T = T; w.H = H; w.scale = scale; w.g = g;
   w.in_bf16 = bf16; w.out_bf16 = grad_dtype == KDA_BF16; w.g_head = g_per_head != 0;
@@ -248,9 +248,9 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, kda
       walk(y, l.fk);
     }
     if (err == hipSuccess && T > 0)
-      err = launch_linear_dg(LinearDgArgs{xq, xk, bsum, dgt, bh, T, H, dk_dim / 16, linear_chunk(bf16) * kBlockChunks}, st);
+      err = launch_linear_dg(LinearDgArgs{xq, xk, bsum, dg, block_sum, bh, T, H, dk_dim / 16, linear_chunk(bf16) * kBlockChunks}, st);
   }
-  if (err == hipSuccess && g_per_head) err = launch_linear_dg_sum(dgt, dg, int64_t(B) * T, H, st);
+  if (err == hipSuccess && g_per_head) err = launch_linear_dg_sum(block_sum, dg, B, H, l.nblk, st);
   return from_hip(err);
 }
 

@@ -98,7 +98,7 @@ def test_linear_backward_refusals(L):  # noqa: F811
     assert lin_bwd(L, dq=P(9)) == ERR_ALIAS and lin_bwd(L, ws=P(12)) == ERR_ALIAS
     need = L.kda_linear_chunk_bwd_workspace_bytes(2, 100, 3, 64, 64, BF16, 0)
     assert lin_bwd(L, wsb=need - 1) == ERR_WORKSPACE and lin_bwd(L, ws=None) == ERR_NULL
-    assert L.kda_linear_chunk_bwd_workspace_bytes(2, 100, 3, 64, 64, BF16, 1) >= need + 2 * 100 * 3 * 4
+    assert L.kda_linear_chunk_bwd_workspace_bytes(2, 100, 3, 64, 64, BF16, 1) > need
     assert lin_bwd(L, B=1 << 12, T=1 << 12, H=1 << 7) == ERR_SHAPE  # more chunks than a launch holds
     assert L.kda_linear_chunk_bwd_workspace_bytes(1 << 12, 1 << 12, 1 << 7, 64, 64, BF16, 0) == 0
 
