@@ -106,6 +106,41 @@ def test_non_finite_values_stay_in_their_sequence_and_later_rows(dtype):
         assert not torch.isfinite(o[50:75, :, 3]).any(), name
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv", [(6, 2), (96, 8)])
+def test_few_and_many_workgroups(Hq, Hkv, dtype):
+    """Launches that fill the device and such that do not divide the keys differently."""
+    d = inputs([190, 260, 1, 69], Hq, Hkv, 64, dtype, seed=5)
+    o, _ = check(f"{Hq}", d, backward=False)
+    for name, row, val in (("v", 300, math.nan), ("v", 191, math.inf), ("v", 449, -math.inf), ("k", 333, math.nan)):
+        e = {x: (y.clone() if x != "cu" else y) for x, y in d.items()}
+        e[name][row, :, 3] = val
+        g = on(e)
+        got, _ = kda.attn_prompt_fwd(g["q"], g["k"], g["v"], g["cu"], o_dtype=dtype)
+        torch.cuda.synchronize()
+        same = [*range(0, row), *range(450, 520)]
+        assert torch.equal(got[same], o[same]), (name, row)
+        assert not torch.isfinite(got[row:450, :, 3]).any(), (name, row)
+        if name == "v":
+            assert torch.equal(got[..., 4:], o[..., 4:]), (name, row)
+
+
+@pytest.mark.parametrize("Hq", [2, 96])
+def test_large_scores_over_many_keys(Hq):
+    """Maxima that differ widely between the parts of a row's keys."""
+    d = inputs([500], Hq, Hq // 2, 64, F32)
+    d["q"] *= torch.linspace(0.1, 12, 500)[:, None, None]
+    d["k"] *= torch.linspace(12, 0.1, 500)[:, None, None] ** 0.5
+    g = on(d)
+    want, mag = mx.prompt(*(mx.f64(d[x]) for x in ("q", "k", "v")), d["cu"], 0.5)
+    o, lse = kda.attn_prompt_fwd(g["q"], g["k"], g["v"], g["cu"], scale=0.5)
+    torch.cuda.synchronize()
+    # a score x is off by |x| 2^-24 for each of its roundings, and p by as much relative to itself
+    big = float((d["q"].abs().max() * d["k"].abs().max()) * 0.5 * 64)
+    mx.close("o", o, want["o"], mag["o"], F32, 2.0, 16 * big)
+    mx.close("lse", lse, want["lse"], want["lse"].abs() + 8, F32, 1.0, 256)
+
+
 def test_large_scores():
     """Scores in the hundreds: the running maximum moves often, and far."""
     d = inputs([150], 2, 1, 64, F32)
