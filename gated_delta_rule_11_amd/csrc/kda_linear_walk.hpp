@@ -77,42 +77,6 @@ struct WalkShape {
   static_assert(C % (64 / Tile<T, DKP>::CH * NPW) == 0 && C % (64 / Tile<T, VC>::CH * NPW) == 0, "the same for each");
 };
 
-// Two fp32 values' upper halves as a pair of bf16.
-__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-
-// x as parts of the element type: one, rounded, or three bf16 whose sum is x (each takes the upper
-// half of what is left, 8 bits of significand at a time, and the rest is exact).
-template <typename T, int N, int W>
-struct Parts {
-  typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
-  words p[N];
-  template <typename V>
-  __device__ __forceinline__ explicit Parts(V x) {
-    static_assert(N == 3 && sizeof(T) == 2, "the exact form");
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < W; j += 2) {
-        p[i][j / 2] = upper_halves(x[j], x[j + 1]);
-        if (i + 1 < N) {
-          x[j] -= __uint_as_float(__float_as_uint(x[j]) & 0xffff0000u);
-          x[j + 1] -= __uint_as_float(__float_as_uint(x[j + 1]) & 0xffff0000u);
-        }
-      }
-  }
-};
-template <typename T>
-struct Parts<T, 1, 8> {
-  typename Op<T>::frag p[1];
-  __device__ __forceinline__ explicit Parts(f32x8 x) { p[0] = Op<T>::pack(x); }
-};
-template <typename T, int N>
-__device__ __forceinline__ typename Op<T>::frag part_of(const Parts<T, N, 8>& x, int i) {
-  return __builtin_bit_cast(typename Op<T>::frag, x.p[i]);
-}
-
 template <typename T, typename TO, int DK, int DV, int OUT, bool REV>
 __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_kernel(const LinearArgs a) {
   using W = WalkShape<T, DK, DV, OUT>;
