@@ -47,8 +47,11 @@ __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float(
 // Appending.  One workgroup per (touched page, key head): the new tokens' largest magnitudes,
 // the scales, the codes.  Sequence i's pages sit at slots cu[i] / P + 2 i onwards: n new tokens
 // touch at most n / P + 2 pages, and these starts leave at least that many slots to each sequence,
-// so a slot finds its sequence by a search over cu alone.  Bound by the bytes it moves for
-// prompts, by latency for single tokens.
+// so a slot finds its sequence by a search over cu alone.  One workgroup to a page because a page
+// has one scale, which all of its values wait for.  Measured (bf16, 8 heads, d = 128, pages of 64):
+// 5 sequences with 400 to 6000 new tokens each, 88 MB, 28.7 us, 3.1 TB/s (17.5 us at a copy's
+// rate), for the latency of each workgroup's chain of search, load, maximum, scale, store; 256
+// single tokens 21.6 us, most of it the call.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void cache_append_kernel(const CacheAppendArgs a) {
   constexpr int CPR = D / 8, N = 64 * CPR / 256;  // 8-element chunks of a row; chunks of a thread
@@ -195,7 +198,9 @@ __device__ __forceinline__ float sum_groups(float x) {
 // each of its four wavefronts takes every fourth tile of 64 tokens and keeps its own running
 // maximum, sum and accumulators; they are joined through LDS, and the parts of a context by a
 // second small kernel.  Bound by the cache's bytes: a lane's loads are 16 bytes and the next
-// tile's are in flight while one is used.  Scores are formed transposed, S^T = K Q^T, on
+// tile's are in flight while one is used.  Measured (bf16 queries, 32 heads on 8, d = 128): 256
+// sequences of 1 to 4096 tokens 219 us, 5.2 TB/s, a large copy's rate; one of 131072 tokens 57 us,
+// 4.7 TB/s, with a join of 6 us in it.  Scores are formed transposed, S^T = K Q^T, on
 // 16x16x32 products whose 64 rows are dealt so that group g of 16 lanes ends up with tokens
 // 16 g .. + 15 of its column's head: row r of product t is token 16 (r / 4) + 4 t + r % 4.  The
 // probabilities are then in place as the operand of O^T = V^T P^T, and V's 16 tokens of a lane are one load.
@@ -470,7 +475,9 @@ hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t st) {
 }
 
 // Parts of a context: enough workgroups to fill the GPU with a few each, none with less than one
-// tile for each of its wavefronts.
+// tile for each of its wavefronts.  Measured, 512 : 1024 : 2048 workgroups, us, 8 key heads, d = 128:
+// contexts alike, 1 of 131072 tokens 54 : 57 : 65, 8 of 16384 53 : 54 : 58; contexts of any length up
+// to 16384, 8 of them 37 : 32 : 39, 32 of them 142 : 125 : 123.
 int cache_step_splits(int N, int Hq, int Hkv, int page, int max_pages) {
   const int64_t units = int64_t(N) * Hkv * ((Hq / Hkv + 15) / 16);
   const int64_t tiles = (int64_t(max_pages) * page + 63) / 64;

@@ -30,10 +30,16 @@
 // 16x16x32 with fp32 accumulation: (S^T q) takes the state straight from the accumulators (their
 // layout is an operand's), the values' transposing reads serve both P V and the update.
 //
-// With bf16 elements P, and the copy of S that the outputs read, are rounded to bf16, half a unit
-// of the last place that the outputs have anyway.  The state takes its rows e^{G_C - G_s} v_s as
-// three bf16 parts (24 bits), so it is fp32-accurate however long the sequence; with DOT, P and
-// S too.  These products are not what bounds the walk: its bytes are.
+// With bf16 elements P, and the copy of S that the outputs read, are rounded to bf16, 2^-8 of each
+// term, half a unit of the last place that the outputs have anyway.  The state takes its rows
+// e^{G_C - G_s} v_s as three bf16 parts (24 bits), so it is fp32-accurate however long the
+// sequence; with DOT, P and S too.
+//
+// Measured (bf16, B = 4, T = 32768, H = 32, 128 x 128): 1160 us for 4.33 GB, 3.7 TB/s (857 us at a
+// copy's rate; the memory accesses alone take 933 us in this shape, all but them 870).  Left out
+// one at a time, the exact parts save 135 us, the scores 115, the stores 118, the copies 207: the
+// sum of issue and bytes in one workgroup per compute unit bounds it, the LDS being full with three
+// chunks in rotation.  The walk without outputs (segments' end states) takes 170 us for 0.54 GB.
 //
 // Few, long sequences are cut into segments (the ABI layer's rule).  The decay being a scalar, a
 // segment's transition is one number: a first walk leaves every segment's end state from zero, a

@@ -19,7 +19,7 @@
 // elements P is rounded to bf16 for the second product, 2^-8 relative each, as the outputs are.
 //
 // Measured (bf16, 16270 rows in sequences of 8192, 5000, 1, 2300 and 777, 32 heads on 8, d = 128):
-// 916 us, 877 TFLOP/s of the masked half, where a large matrix product reaches 1230.  What bounds
+// 928 us, 866 TFLOP/s of the masked half, where a large matrix product reaches 1230.  What bounds
 // it is the issue of the matrix instructions and of the exponentials between them; the LDS is read
 // without conflicts (they were 34 % of its cycles before the rows were permuted, and the time did
 // not change).  The order of the tiles, longest rows first, lets the short ones fill the end.
