@@ -44,6 +44,8 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float f) {
 
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+__device__ __forceinline__ int page_shift(int page) { return page == 64 ? 6 : (page == 32 ? 5 : 4); }
+
 // Appending.  One workgroup per (touched page, key head): the new tokens' largest magnitudes,
 // the scales, the codes.  Sequence i's pages sit at slots cu[i] / P + 2 i onwards: n new tokens
 // touch at most n / P + 2 pages, and these starts leave at least that many slots to each sequence,
@@ -57,22 +59,25 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const CacheAppendArgs
   constexpr int CPR = D / 8, N = 64 * CPR / 256;  // 8-element chunks of a row; chunks of a thread
   __shared__ __align__(16) uint8_t image[D * 68];               // new V codes, [d][P + 4]
   __shared__ float red[8];
-  const int tid = threadIdx.x, P = a.page;
+  const int tid = threadIdx.x, P = a.page, ps = page_shift(P);
   const int h = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv;
 
+  // the last sequence whose pages start at or before this slot, 64 candidates at a time
   int lo = 0, up = a.N;
   while (up - lo > 1) {
-    const int mid = (lo + up) >> 1;
-    if (int64_t(a.cu[mid]) / P + 2 * int64_t(mid) <= slot) lo = mid;
-    else up = mid;
+    const int step = (up - lo + 63) / 64;
+    const int64_t mid = lo + int64_t(step) * ((tid & 63) + 1);
+    const bool before = mid < up && (a.cu[mid] >> ps) + 2 * mid <= slot;
+    lo += step * __popcll(__ballot(before));
+    up = lo + step < up ? lo + step : up;
   }
   int first = a.cu[lo], last = a.cu[lo + 1];
-  const int64_t base = int64_t(first) / P + 2 * int64_t(lo);
+  const int64_t base = (first >> ps) + 2 * int64_t(lo);
   first = first < 0 ? 0 : first;
   last = last > a.n ? a.n : last;
   if (first >= last || slot < base) return;
   const int64_t held = a.ctx[lo] < 0 ? 0 : a.ctx[lo];
-  const int64_t pi = held / P + (slot - base);
+  const int64_t pi = (held >> ps) + (slot - base);
   const int64_t p0 = pi * P > held ? pi * P : held;
   const int64_t end = held + (last - first), p1 = (pi + 1) * P < end ? (pi + 1) * P : end;
   if (p0 >= p1 || pi >= a.max_pages) return;
@@ -80,6 +85,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const CacheAppendArgs
   if (page < 0 || page >= a.pages) return;
   const int off = int(p0 - pi * P), cnt = int(p1 - p0);
   const int64_t row0 = first + (p0 - held);
+  const int64_t ph = int64_t(page) * a.Hkv + h;
+  const float old_k = a.ks[ph], old_v = a.vs[ph];
 
   f32x8 x[2][N];
   float amax[2] = {0.f, 0.f};
@@ -107,8 +114,6 @@ __global__ __launch_bounds__(256) void cache_append_kernel(const CacheAppendArgs
     red[tid >> 6] = amax[0];
     red[4 + (tid >> 6)] = amax[1];
   }
-  const int64_t ph = int64_t(page) * a.Hkv + h;
-  const float old_k = a.ks[ph], old_v = a.vs[ph];
   __syncthreads();  // every thread has read the scales
   float sk = scale_for(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
   float sv = scale_for(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
@@ -225,7 +230,7 @@ __global__ __launch_bounds__(256, 2) void cache_step_kernel(const CacheStepArgs 
   const int gt = id % GT;
   id /= GT;
   const int kvh = id % a.Hkv, n = id / a.Hkv;
-  const int P = a.page, ps = P == 64 ? 6 : (P == 32 ? 5 : 4);
+  const int P = a.page, ps = page_shift(P);
   const int64_t room = int64_t(a.max_pages) * P;
   int64_t ctx = a.ctx[n] < 0 ? 0 : a.ctx[n];
   ctx = ctx < room ? ctx : room;
