@@ -52,8 +52,9 @@ __device__ __forceinline__ int page_shift(int page) { return page == 64 ? 6 : (p
 // so a slot finds its sequence by a search over cu alone.  One workgroup to a page because a page
 // has one scale, which all of its values wait for.  Measured (bf16, 8 heads, d = 128, pages of 64):
 // 5 sequences with 400 to 6000 new tokens each, 88 MB, 28.7 us, 3.1 TB/s (17.5 us at a copy's
-// rate), for the latency of each workgroup's chain of search, load, maximum, scale, store; 256
-// single tokens 21.6 us, most of it the call.
+// rate), for the latency of each workgroup's chain of search, load, maximum, scale, store (more of
+// them at once, or wider LDS stores of V's codes, did not shorten it); 256 single tokens 17.7 us:
+// the same chain, and one byte to each of V's 262144 rows of tokens.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void cache_append_kernel(const CacheAppendArgs a) {
   constexpr int CPR = D / 8, N = 64 * CPR / 256;  // 8-element chunks of a row; chunks of a thread
