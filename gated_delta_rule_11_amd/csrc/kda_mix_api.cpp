@@ -40,12 +40,17 @@ bool linear_sizes_ok(int64_t B, int64_t T, int64_t H, int64_t dk, int64_t dv) {
   return sizes_ok(B, T, H, dk, dv) && H * dk <= kMaxRow && H * dv <= kMaxRow;
 }
 constexpr int64_t kMinSegChunks = 4;
+// Nor is a sequence of fewer chunks than this cut: two more launches cost what they save.  Measured,
+// cut : whole, us, 8 heads: 8 chunks, bf16, 24 : 19 (d = 128) and 23 : 16 (64), fp32 33 : 34 and 22 : 15
+// (32), with gradients 107 : 102, 86 : 84, 137 : 146 and 69 : 61; 12 chunks 24 : 27, 23 : 21, 34 : 49,
+// with gradients 110 : 144, 87 : 118, 140 : 210.
+constexpr int64_t kMinCutChunks = 12;
 LinearForm linear_form(int64_t B, int64_t T, int64_t H, int dv, bool bf16) {
   const int C = linear_chunk(bf16);
   LinearForm f{(T + C - 1) / C, 1, 0};
   f.seg_chunks = int(f.nch);
   const int64_t units = B * H * (dv > 64 ? 2 : 1);
-  if (units <= 0 || f.nch <= 0) return f;
+  if (units <= 0 || f.nch < kMinCutChunks) return f;
   int64_t segs = kUnits / units;
   segs = segs < f.nch / kMinSegChunks ? segs : f.nch / kMinSegChunks;
   if (segs < 2) return f;
