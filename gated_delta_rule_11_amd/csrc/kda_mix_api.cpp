@@ -418,10 +418,12 @@ kda_status kda_attn_decode_step(const void* q, kda_dtype in_dtype, const void* k
     for (const Range& y : outs)
       if (&y != &x && overlap(x, y)) return KDA_ERR_ALIAS;
   }
+  // a cache of no pages leaves every token out: the kernel then sees a table of no pages and does not
+  // read it (it may be NULL)
   return from_hip(launch_cache_step(
       CacheStepArgs{q, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale, v_scale,
                     block_table, context_len, o, lse, static_cast<float*>(workspace), N, Hq, Hkv, d, page, n_pages,
-                    max_pages, splits, scale, in_dtype == KDA_BF16, o_dtype == KDA_BF16},
+                    n_pages > 0 ? max_pages : 0, splits, scale, in_dtype == KDA_BF16, o_dtype == KDA_BF16},
       static_cast<hipStream_t>(stream)));
 }
 

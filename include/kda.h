@@ -473,7 +473,8 @@ kda_status kda_kv_cache_append(const void* k, const void* v, kda_dtype in_dtype,
  *   q [N,Hq,d] in_dtype -> o [N,Hq,d] o_dtype, lse [N,Hq] fp32 or NULL.
  * A sequence with no tokens gets o = 0, lse = -inf.  Tokens past max_pages
  * pages, or in a page whose id is outside [0, n_pages), are left out.  What
- * lies in a page behind the last token is not used, whatever it holds.
+ * lies in a page behind the last token is not used, whatever it holds.  With
+ * n_pages == 0 the cache, the scales and block_table are not read and may be NULL.
  *   workspace  kda_attn_decode_step_workspace_bytes bytes, 16-byte aligned
  *          (NULL when that is 0)
  */

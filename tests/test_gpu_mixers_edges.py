@@ -1,0 +1,37 @@
+"""Calls of the linear, prompt and cache entry points that their documentation allows at the ends of
+its ranges: a cache without pages."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_11_amd as kda
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("N,max_pages", [(3, 4), (1, 600)])
+def test_step_over_a_cache_without_pages(N, max_pages):
+    """Every token lies in a page outside the cache: o = 0, lse = -inf, and the table, which may be NULL,
+    is not read.  Through the C ABI with NULL, whole and in parts, and through the binding."""
+    Hq, Hkv, d, P = 4, 2, 64, 16
+    q = torch.randn(N, Hq, d, device=DEV)
+    ctx = torch.tensor([max_pages * P] * N, dtype=torch.int32, device=DEV)
+    o, lse = torch.full((N, Hq, d), 7.0, device=DEV), torch.full((N, Hq), 7.0, device=DEV)
+    need = kda.attn_decode_step_workspace_bytes(N, Hq, Hkv, d, P, max_pages)
+    assert (need > 0) == (max_pages > 4)
+    ws = torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = kda.lib().kda_attn_decode_step(p(q), 0, None, None, None, None, None, p(ctx), p(o), 0, p(lse), N, Hq, Hkv, d, P, 0,
+                                        max_pages, 0.125, p(ws), need, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and not o.any() and bool((lse == -math.inf).all())
+    code = torch.zeros(0, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    none = torch.zeros(0, Hkv, device=DEV)
+    table = torch.zeros(N, max_pages, dtype=torch.int32, device=DEV)
+    o, lse = kda.attn_decode_step(q, code.view(0, Hkv, P, d), code.view(0, Hkv, d, P), none, none, table, ctx, want_lse=True)
+    torch.cuda.synchronize()
+    assert not o.any() and bool((lse == -math.inf).all())
