@@ -66,6 +66,7 @@ struct WalkShape {
   static constexpr int NSL = DV / DVS, NSW = DVS / 16, TT = C / 16, U = C / 32;
   static constexpr int NPW = OUT ? TT : 1;         // scoring and copying wavefronts
   static constexpr int NT = 64 * (NSW + NPW);
+  static_assert(NT <= linear_threads(sizeof(T) == 2, DV) && NSL == linear_slices(DV), "what the ABI layer checks launches by");
   static constexpr int NKK = DKP / 32, NKT = DK / 16;
   static constexpr int kExact = sizeof(T) == 2 ? 3 : 1;  // parts of an fp32-accurate operand
   static constexpr int kOut = OUT == 2 ? kExact : 1;     // parts of P and S in the outputs

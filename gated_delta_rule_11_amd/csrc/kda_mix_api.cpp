@@ -14,7 +14,8 @@ using namespace kda;
 
 namespace {
 
-// A launch holds fewer than 2^32 threads; the largest workgroup here has 256.
+// A launch holds fewer than 2^32 threads.  In workgroups of 256, which all kernels here have but the
+// linear walks (linear_threads; see walk_grid_ok):
 constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
 
 // ---- linear attention -------------------------------------------------------------------
@@ -49,7 +50,7 @@ LinearForm linear_form(int64_t B, int64_t T, int64_t H, int dv, bool bf16) {
   const int C = linear_chunk(bf16);
   LinearForm f{(T + C - 1) / C, 1, 0};
   f.seg_chunks = int(f.nch);
-  const int64_t units = B * H * (dv > 64 ? 2 : 1);
+  const int64_t units = B * H * linear_slices(dv);
   if (units <= 0 || f.nch < kMinCutChunks) return f;
   int64_t segs = kUnits / units;
   segs = segs < f.nch / kMinSegChunks ? segs : f.nch / kMinSegChunks;
@@ -84,6 +85,12 @@ hipError_t enter_segments(LinearArgs& a, const LinearForm& f, float* ws, hipStre
   a.S_in = E;
   a.S_in_seg = true;
   return e;
+}
+
+// A walk's launch: one workgroup per (b, h, slice), or up to kUnits of them where sequences are cut.  (The
+// scan between walks runs for cut sequences only, at most kUnits / 2 heads.)
+bool walk_grid_ok(int64_t B, int64_t H, int dv, bool bf16) {
+  return B * H * linear_slices(dv) * linear_threads(bf16, dv) <= 0xffffffffLL;
 }
 
 // The largest launch of a backward, and sizes that keep its layout within 64 bits.
@@ -154,7 +161,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, kda
   const LinearForm f = linear_form(B, T, H, dv, bf16);
   const int64_t bh = int64_t(B) * H, ntok = bh * T, state = int64_t(dk) * dv;
   if (bh == 0) return KDA_OK;
-  if (bh * f.nseg * 2 > kMaxGrid) return KDA_ERR_SHAPE;
+  if (!walk_grid_ok(B, H, dv, bf16)) return KDA_ERR_SHAPE;
   const int64_t need = seg_floats(f, bh, state) * 4;
   if (ntok > 0 && (!q || !k || !v || !g || !o)) return KDA_ERR_NULL;
   if (need > 0 && !workspace) return KDA_ERR_NULL;

@@ -12,6 +12,13 @@ namespace kda {
 // Tokens of a chunk: the fp32 kernels' tiles of 64 tokens would not fit the LDS.
 __host__ __device__ constexpr int linear_chunk(bool bf16) { return bf16 ? 64 : 32; }
 
+// Threads of a walk's workgroup: a wavefront for every 16 value columns, of up to 64, and one for every
+// 16 tokens of a chunk (fewer where only the state is wanted).
+__host__ __device__ constexpr int linear_threads(bool bf16, int dv) {
+  return 64 * ((dv < 64 ? dv : 64) / 16 + linear_chunk(bf16) / 16);
+}
+__host__ __device__ constexpr int linear_slices(int dv) { return dv > 64 ? 2 : 1; }
+
 // Chunks between the states that the backward keeps for dg.  Within a block dg is a difference of
 // sums over the block's tokens.  B = 4, H = 32, T = 4001, d = 128, forward and backward: 773 us and dg within
 // 1.0e-6 of the 64-bit result at 8 chunks, 793 us and 0.67e-6 at 4, 832 us and 0.48e-6 at 2.
