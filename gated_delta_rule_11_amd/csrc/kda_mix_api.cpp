@@ -93,10 +93,11 @@ bool walk_grid_ok(int64_t B, int64_t H, int dv, bool bf16) {
   return B * H * linear_slices(dv) * linear_threads(bf16, dv) <= 0xffffffffLL;
 }
 
-// The largest launch of a backward, and sizes that keep its layout within 64 bits.
-bool bwd_grid_ok(int64_t B, int64_t T, int64_t H, bool bf16) {
+// The launches of a backward (the walks' value columns are those of k for dq and dk; dg has one workgroup
+// per block), and sizes that keep its layout within 64 bits.
+bool bwd_grid_ok(int64_t B, int64_t T, int64_t H, int dk, int dv, bool bf16) {
   const int64_t nblk = (T + linear_chunk(bf16) * kBlockChunks - 1) / (linear_chunk(bf16) * kBlockChunks);
-  return B * H * 64 <= kMaxGrid && B * H * nblk <= kMaxGrid / 2;
+  return walk_grid_ok(B, H, dk, bf16) && walk_grid_ok(B, H, dv, bf16) && B * H * nblk <= kMaxGrid / 2;
 }
 
 // Workspace of the backward, in floats: kept states, dot products and boundary terms for dg, one
@@ -189,7 +190,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, kda
 
 size_t kda_linear_chunk_bwd_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype in_dtype, int g_per_head) {
   if (!dtype_ok(in_dtype) || !linear_sizes_ok(B, T, H, dk, dv) || !dim_ok(dk) || !dim_ok(dv) ||
-      !bwd_grid_ok(B, T, H, in_dtype == KDA_BF16))
+      !bwd_grid_ok(B, T, H, dk, dv, in_dtype == KDA_BF16))
     return 0;
   return size_t(bwd_layout(B, T, H, dk, dv, in_dtype == KDA_BF16, g_per_head != 0).total) * 4;
 }
@@ -204,7 +205,7 @@ kda_status kda_linear_chunk_bwd(const void* q, const void* k, const void* v, kda
   if (!dim_ok(dk_dim) || !dim_ok(dv_dim) || !isfinite(scale) || (g_per_head != 0 && g_per_head != 1))
     return KDA_ERR_UNSUPPORTED;
   const bool bf16 = in_dtype == KDA_BF16;
-  if (!bwd_grid_ok(B, T, H, bf16)) return KDA_ERR_SHAPE;
+  if (!bwd_grid_ok(B, T, H, dk_dim, dv_dim, bf16)) return KDA_ERR_SHAPE;
   const BwdLayout l = bwd_layout(B, T, H, dk_dim, dv_dim, bf16, g_per_head != 0);
   const int64_t bh = int64_t(B) * H, ntok = bh * T, state = int64_t(dk_dim) * dv_dim;
   if (bh == 0 && !g_per_head) return KDA_OK;

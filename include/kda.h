@@ -349,7 +349,8 @@ kda_status kda_decode_replay(const void* q, const void* k, const void* v,
  * H*dk and H*dv are at most 2^22 in the chunked calls.  B*H below 2^22 always
  * fits their launches; larger products are taken while a launch stays under
  * 2^32 threads (bf16 with 128 channels needs 1024 for each head, other types
- * and sizes less).  Beyond any of these: KDA_ERR_SHAPE.
+ * and sizes less).  The backward also needs B*H*ceil(T/256), with fp32 inputs
+ * B*H*ceil(T/128), below 2^23.  Beyond any of these: KDA_ERR_SHAPE.
  *
  *   q, k [B,T,H,dk] in_dtype    v [B,T,H,dv] in_dtype
  *   g    fp32 log-decays, at most 0: [B,T,H] (g_per_head == 0), or [H], the

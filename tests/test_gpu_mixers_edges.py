@@ -1,5 +1,5 @@
 """Calls of the linear, prompt and cache entry points that their documentation allows at the ends of
-its ranges: a cache without pages."""
+its ranges: a cache without pages, many heads in one call."""
 import ctypes
 import math
 
@@ -35,3 +35,21 @@ def test_step_over_a_cache_without_pages(N, max_pages):
     o, lse = kda.attn_decode_step(q, code.view(0, Hkv, P, d), code.view(0, Hkv, d, P), none, none, table, ctx, want_lse=True)
     torch.cuda.synchronize()
     assert not o.any() and bool((lse == -math.inf).all())
+
+
+def test_linear_many_heads_of_one_call():
+    """B * H = 2^18 heads of two tokens, forward and backward: the same bits as those entries alone."""
+    B, T, H, d, n = 8192, 2, 32, 16, 4
+    gen = torch.Generator(DEV).manual_seed(0)
+    rn = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    q, k, v, do = (rn(B, T, H, d).to(BF) for _ in range(4))
+    g, S, dS = -rn(B, T, H).abs(), rn(B, H, d, d), rn(B, H, d, d)
+    o, So = kda.linear_chunk_fwd(q, k, v, g, S_in=S)
+    got = kda.linear_chunk_bwd(q, k, v, g, do, dS_out=dS, S_in=S)
+    for b in (0, B // 2 - 3, B - n):
+        x = [t[b:b + n].contiguous() for t in (q, k, v, g, do, dS, S)]
+        o1, S1 = kda.linear_chunk_fwd(*x[:4], S_in=x[6])
+        want = kda.linear_chunk_bwd(*x[:5], dS_out=x[5], S_in=x[6])
+        torch.cuda.synchronize()
+        assert torch.equal(o[b:b + n], o1) and torch.equal(So[b:b + n], S1)
+        assert all(torch.equal(got[y][b:b + n], want[y]) for y in want)
