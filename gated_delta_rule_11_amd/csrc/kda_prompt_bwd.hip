@@ -34,10 +34,15 @@ namespace {
 constexpr int BM = 128;  // owned rows or keys
 constexpr int BN = 64;   // walked keys
 constexpr int BR = 64;   // walked rows
-// Rows closer than this to their sequence's start have D formed anew, as sum_j P_ij dP_ij, where o
-// is rounded: behind it D's error, 2^-8 |do| |o| with |o| falling as 1 / sqrt(keys), is lost in dS'
-// own rounding.  The first row needs it most: its dS is zero, and D's error all that is left.
-constexpr int kNear = 256;
+// D = do . o carries the roundings of o (of its element type, or of the probabilities that a forward with
+// bf16 elements formed it from): up to 2^-8 sum |do| |o|, which dP - D does not forgive where few keys hold
+// a row's weight, or where the values have much in common.  A row's dS sum to zero, so what they sum to is
+// that error: the dq kernel corrects D by it, for dk and dv too, and forms those rows' dq again where it is
+// more than this share of sum |dS|, a quarter of what dS may lose to its own rounding.  (Elements in
+// fp32 round no dS: every row, when o is bf16.)  Measured, the gradients of the rows above: 537 us where few rows
+// need it (530 without the correction; 554 at half this share), 690 where all do (a sink key in every
+// sequence).
+template <typename T> constexpr float kLeft = sizeof(T) == 2 ? 0.0009765625f : 0.f;
 
 // Asks for N products with V vector instructions, and the LDS reads of two fragments, after each.
 template <int N, int V>
@@ -276,15 +281,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   const T* kp = static_cast<const T*>(a.k) + int64_t(kvh) * D;
   const T* vp = static_cast<const T*>(a.v) + int64_t(kvh) * D;
 
-  const int lo = span_of(a.cu, a.nseq, a.n, r0).start;
+  int lo = span_of(a.cu, a.nseq, a.n, r0).start;
   const int hi = r0 + BM < used ? r0 + BM : used;
   const int w0 = r0 + 32 * wave, qi = w0 + l32;
   const int wlast = w0 + 31 < used ? w0 + 31 : used - 1;
   const int qr = qi < used ? qi : used - 1;
   const int start = span_of(a.cu, a.nseq, a.n, qr).start;
-  const int smin = __shfl(start, 0), smax = __shfl(start, 31);
+  int smin = __shfl(start, 0);
+  const int smax = __shfl(start, 31);
   const float c = a.scale * kLog2e;
-  const float ls = a.lse[int64_t(qr) * a.Hq + head] * kLog2e;
+  float ls = a.lse[int64_t(qr) * a.Hq + head] * kLog2e;
   float Di = a.D[int64_t(qr) * a.Hq + head];
 
   F qf[NK], of[NK];
@@ -298,20 +304,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
     }
   }
   f32x16 dq[ND];
+  const uint32_t brow = TD::b_row8_32(lane), bcol = TD::b_col44_32(lane);
 #pragma unroll
   for (int i = 0; i < ND; ++i) dq[i] = zero16();
-
-  const uint32_t brow = TD::b_row8_32(lane), bcol = TD::b_col44_32(lane);
-  // Walks the keys from `from` on: the rows' dq, or (EXACT) the sums of P dP.
-  float dsum = 0.f;
-  auto walk = [&](int from, auto exact) {
-    constexpr bool EXACT = decltype(exact)::value;
-    const int nt = (hi - from + BN - 1) / BN;
-    auto fetch = [&](int t) {
-      T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
-      copy_rows<T, BN, D, 4>(kb, kp, kst, from + t * BN, hi, wave, lane);
-      copy_rows<T, BN, D, 4>(kb + BN * D, vp, kst, from + t * BN, hi, wave, lane);
-    };
+  const bool correct = DB || a.o_bf16;  // D is not exact to fp32
+  auto fetch = [&](int t) {
+    T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
+    copy_rows<T, BN, D, 4>(kb, kp, kst, lo + t * BN, hi, wave, lane);
+    copy_rows<T, BN, D, 4>(kb + BN * D, vp, kst, lo + t * BN, hi, wave, lane);
+  };
+  for (bool again = false;; again = true) {
+    const int nt = (hi - lo + BN - 1) / BN;
+    float sum = 0.f, size = 0.f;  // of dS, and of |dS|
     fetch(0);
     for (int t = 0; t < nt; ++t) {
       copies_done();
@@ -319,7 +323,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
       const T* Ks = buf + (DB ? (t & 1) * 2 * BN * D : 0);
       const T* Vs = Ks + BN * D;
       const uint32_t krow = TD::at(Ks) + brow, vrow = TD::at(Vs) + brow, kcol = TD::at(Ks) + bcol;
-      const int k0 = from + t * BN;
+      const int k0 = lo + t * BN;
 #pragma unroll
       for (int j = 0; j < BN / 32; ++j) {
         const int s0 = k0 + 32 * j;
@@ -333,22 +337,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
         auto gradients = [&](auto whole) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p = fast_exp2(s[i] * c - ls);
-            dp[i] = p * (EXACT ? dp[i] : dp[i] - Di);
+            dp[i] = fast_exp2(s[i] * c - ls) * (dp[i] - Di);
             if constexpr (!decltype(whole)::value)  // the row sees keys start .. qi
               dp[i] = unsigned(s0 + crow(i, h2) - start) <= unsigned(qi - start) ? dp[i] : 0.f;
-            if constexpr (EXACT) dsum += dp[i];
+            sum += dp[i];
+            size += fabsf(dp[i]);
           }
         };
         if (s0 + 31 <= w0 && s0 >= smax) gradients(std::true_type{});
         else gradients(std::false_type{});
-        if constexpr (!EXACT) {
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const F df = frag_of<T>(dp, ks);
+        for (int ks = 0; ks < 2; ++ks) {
+          const F df = frag_of<T>(dp, ks);
 #pragma unroll
-            for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44_32(kcol, 32 * j + 16 * ks, i), df, dq[i]);
-          }
+          for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44_32(kcol, 32 * j + 16 * ks, i), df, dq[i]);
         }
       }
       if (!DB) {
@@ -356,19 +358,30 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
         if (t + 1 < nt) fetch(t + 1);
       }
     }
-  };
-  // Near its sequence's start a row has few keys, dP is close to D, and D from the rounded o costs
-  // dS its accuracy (the first row's dS is zero, and would be half a rounding of do . o).  There D is
-  // formed as the sum of P dP, before dk and dv read it.
-  if (a.o_bf16 && span_of(a.cu, a.nseq, a.n, hi - 1).start > r0 - kNear) {
-    walk(lo > r0 - kNear ? lo : r0 - kNear, std::true_type{});
+    if (again || !correct) break;
+    sum = sum_halves(sum);
+    size = sum_halves(size);
+    Di += sum;
+    if (qi < used && h2 == 0) a.D[int64_t(qi) * a.Hq + head] = Di;
+    // The rows to form again (both halves of the wavefront know): the first one's sequence is where the
+    // keys begin, a row that is done takes probabilities of zero.
+    const bool mine = qi < used && fabsf(sum) > kLeft<T> * size;
+    const uint64_t rows = __ballot(mine);
+    smin = rows ? __shfl(start, __builtin_ctzll(rows)) : hi;
     lds_barrier();
-    if (qi < used && qi - start < kNear) {
-      Di = sum_halves(dsum);
-      if (h2 == 0) a.D[int64_t(qi) * a.Hq + head] = Di;
-    }
+    int* const first = reinterpret_cast<int*>(smem);
+    if (lane == 0) first[wave] = smin;
+    lds_barrier();
+    const int f0 = first[0] < first[1] ? first[0] : first[1], f1 = first[2] < first[3] ? first[2] : first[3];
+    lo = f0 < f1 ? f0 : f1;
+    if (lo >= hi) break;
+    if (!mine) ls = INFINITY;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dq[i][r] = mine ? 0.f : dq[i][r];
+    lds_barrier();
   }
-  walk(lo, std::false_type{});
   if (qi < used) {
     TG* p = static_cast<TG*>(a.dq) + int64_t(qi) * qst + int64_t(head) * D;
 #pragma unroll
@@ -429,7 +442,7 @@ hipError_t launch(const PromptBwdArgs& a, hipStream_t st) {
   if (e == hipSuccess) e = a.o_bf16 ? launch_dot_o<bf16_t>(a, st) : launch_dot_o<float>(a, st);
   if (e != hipSuccess) return e;
   const int ntile = (a.n + BM - 1) / BM;
-  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, lds, st>>>(a, ntile);  // may refine D
+  kq<<<dim3(uint32_t(int64_t(ntile) * a.Hq)), 256, lds, st>>>(a, ntile);  // corrects D, before dk and dv read it
   e = hipGetLastError();
   if (e == hipSuccess) e = a.parts == 1 ? launch_dkv<T, TG, D>(a, ntile, st) : launch_dkv<T, float, D>(a, ntile, st);
   if (e == hipSuccess && a.parts > 1) {

@@ -434,6 +434,9 @@ kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_
  *   d_o [n,Hq,d] in_dtype;  dq [n,Hq,d], dk, dv [n,Hkv,d] in grad_dtype
  *   (written; dk and dv summed over the query heads of a group)
  *   workspace  kda_attn_prompt_bwd_workspace_bytes bytes, 16-byte aligned
+ * do_i . o_i, which o's own rounding leaves inexact, is corrected from the sums
+ * of P (dP - do . o), which are zero: with a bf16 o too, rows that look at few
+ * keys have gradients as accurate as others.
  * Every sum has one owner and a fixed order: the same bits every time.  A
  * non-finite value in one sequence may reach gradients of its neighbours in
  * the packed buffer.
