@@ -83,6 +83,45 @@ template <> struct Op<float> {
   }
 };
 
+// Non-finite elements of fragments: 16 (32) bit lanes that reach zero where an exponent is all
+// ones, over any number of fragments, and a fragment with those elements set to zero.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <typename T> struct Finite;
+template <> struct Finite<bf16_t> {
+  u16x2 low = {0xffff, 0xffff};
+  __device__ __forceinline__ void see(bf16x8 a) {
+    const u32x4 w = __builtin_bit_cast(u32x4, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) low = __builtin_elementwise_min(low, __builtin_bit_cast(u16x2, ~w[i] & 0x7f807f80u));
+  }
+  __device__ __forceinline__ bool all() const { return low[0] != 0 && low[1] != 0; }
+  __device__ __forceinline__ static bf16x8 only(bf16x8 a) {
+    u32x4 w = __builtin_bit_cast(u32x4, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((~w[i] & 0x7f80u) == 0) w[i] &= 0xffff0000u;
+      if ((~w[i] & 0x7f800000u) == 0) w[i] &= 0xffffu;
+    }
+    return __builtin_bit_cast(bf16x8, w);
+  }
+};
+template <> struct Finite<float> {
+  uint32_t low = 0xffffffffu;
+  __device__ __forceinline__ void see(f32x8 a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = ~__float_as_uint(a[i]) & 0x7f800000u;
+      low = x < low ? x : low;
+    }
+  }
+  __device__ __forceinline__ bool all() const { return low != 0; }
+  __device__ __forceinline__ static f32x8 only(f32x8 a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = (~__float_as_uint(a[i]) & 0x7f800000u) == 0 ? 0.f : a[i];
+    return a;
+  }
+};
+
 // Two fp32 values' upper halves as a pair of bf16.
 __device__ __forceinline__ uint32_t upper_halves(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);

@@ -149,6 +149,7 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
 #pragma unroll
   for (int i = 0; i < W::NS - 1; ++i)
     if (i < steps) fetch(i);
+  int bad_lo = steps, bad_hi = -1;  // steps whose masked rows hold non-finite values
   for (int t = 0; t < steps; ++t) {
     if (t + W::NS - 2 < steps) copies_landed<(W::NS - 2) * W::kCopies>();  // tile t is there
     else copies_landed();
@@ -188,15 +189,20 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
         }
       }
     };
-    auto products = [&](int sub) {
+    auto products = [&](int sub, bool finite) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const F pf = frag_of<T>(s[sub], ks), df = frag_of<T>(dp[sub], ks);
         const int rr = 32 * sub + 16 * ks;
 #pragma unroll
         for (int i = 0; i < ND; ++i) {
-          dv[i] = O::mma32(TD::col44_32(ocol, rr, i), pf, dv[i]);
-          dk[i] = O::mma32(TD::col44_32(qcol, rr, i), df, dk[i]);
+          F x = TD::col44_32(ocol, rr, i), y = TD::col44_32(qcol, rr, i);
+          if (!finite) {
+            x = Finite<T>::only(x);
+            y = Finite<T>::only(y);
+          }
+          dv[i] = O::mma32(x, pf, dv[i]);
+          dk[i] = O::mma32(y, df, dk[i]);
         }
       }
     };
@@ -216,11 +222,11 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
       probabilities(0, std::true_type{});
       if constexpr (sizeof(T) == 2) interleave<2 * NK, 9>();
       __builtin_amdgcn_sched_barrier(0);
-      products(0);
+      products(0, true);
       probabilities(1, std::true_type{});
       if constexpr (sizeof(T) == 2) interleave<4 * ND, 9>();
       __builtin_amdgcn_sched_barrier(0);
-      products(1);
+      products(1, true);
     } else {
 #pragma unroll
       for (int sub = 0; sub < BR / 32; ++sub) {
@@ -228,12 +234,44 @@ __global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs 
         // some row at or past the wavefront's first key, before its last key's end
         if (w0 >= used || s0 + 31 < w0 || s0 >= emax || s0 >= hi) continue;
         scores(sub);
-        if (s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi) probabilities(sub, std::true_type{});
-        else probabilities(sub, std::false_type{});
-        products(sub);
+        if (s0 >= w0 + 31 && s0 + 32 <= emin && s0 + 32 <= hi) {
+          probabilities(sub, std::true_type{});
+          products(sub, true);
+          continue;
+        }
+        // Zero times a NaN or infinity is not zero: where a masked row may hold one (its products with the
+        // keys show it), such elements leave the products, and reach the keys that see them after the loop.
+        float probe = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) probe += s[sub][e] * 0.f + dp[sub][e] * 0.f;
+        const bool finite = !__any(probe != 0.f);
+        probabilities(sub, std::false_type{});
+        products(sub, finite);
+        if (!finite) {
+          bad_lo = t < bad_lo ? t : bad_lo;
+          bad_hi = t;
+        }
       }
     }
   }
+  for (int t = bad_lo; t <= bad_hi; ++t)
+    for (int r = 0; r < BR; ++r) {
+      const int row = c0 + (t % nt) * BR + r;
+      if (row >= hi) break;
+      const bool in = unsigned(row - kj) < unsigned(lim - kj);
+      const int64_t at = row * qst + int64_t(h0 + t / nt) * D + 4 * h2;
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = io<T>::load(static_cast<const T*>(a.d_o) + at, 32 * i + 8 * r4 + j),
+                        y = io<T>::load(static_cast<const T*>(a.q) + at, 32 * i + 8 * r4 + j);
+            dv[i][4 * r4 + j] += in && !(fabsf(x) < INFINITY) ? x : 0.f;
+            dk[i][4 * r4 + j] += in && !(fabsf(y) < INFINITY) ? NAN : 0.f;  // the row's scores, and P, are NaN
+          }
+    }
   if (kj < used) {
     const int64_t at = int64_t(kj) * kst + int64_t(kvh) * D;
     TG* kp = (a.parts == 1 ? static_cast<TG*>(a.dk) : reinterpret_cast<TG*>(a.part + (2 * part) * a.n * kst)) + at;
@@ -307,6 +345,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
   const uint32_t brow = TD::b_row8_32(lane), bcol = TD::b_col44_32(lane);
 #pragma unroll
   for (int i = 0; i < ND; ++i) dq[i] = zero16();
+  int bad_lo = hi, bad_hi = 0;  // keys of masked tiles with non-finite values
   const bool correct = DB || a.o_bf16;  // D is not exact to fp32
   auto fetch = [&](int t) {
     T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
@@ -344,13 +383,32 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
             size += fabsf(dp[i]);
           }
         };
-        if (s0 + 31 <= w0 && s0 >= smax) gradients(std::true_type{});
-        else gradients(std::false_type{});
+        auto products = [&](bool finite) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const F df = frag_of<T>(dp, ks);
+          for (int ks = 0; ks < 2; ++ks) {
+            const F df = frag_of<T>(dp, ks);
 #pragma unroll
-          for (int i = 0; i < ND; ++i) dq[i] = O::mma32(TD::col44_32(kcol, 32 * j + 16 * ks, i), df, dq[i]);
+            for (int i = 0; i < ND; ++i) {
+              F x = TD::col44_32(kcol, 32 * j + 16 * ks, i);
+              if (!finite) x = Finite<T>::only(x);
+              dq[i] = O::mma32(x, df, dq[i]);
+            }
+          }
+        };
+        if (s0 + 31 <= w0 && s0 >= smax) {
+          gradients(std::true_type{});
+          products(true);
+        } else {
+          float probe = 0.f;  // a non-finite key shows in its scores, as for dk and dv
+#pragma unroll
+          for (int i = 0; i < 16; ++i) probe += s[i] * 0.f;
+          const bool finite = !__any(probe != 0.f);
+          gradients(std::false_type{});
+          products(finite);
+          if (!finite) {
+            bad_lo = s0 < bad_lo ? s0 : bad_lo;
+            bad_hi = s0 + 32 > bad_hi ? s0 + 32 : bad_hi;
+          }
         }
       }
       if (!DB) {
@@ -381,6 +439,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) dq[i][r] = mine ? 0.f : dq[i][r];
     lds_barrier();
+  }
+  for (int key = bad_lo; key < bad_hi && key < hi; ++key) {
+    const bool seen = key <= qi && key >= start;
+    const T* row = kp + int64_t(key) * kst + 4 * h2;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = io<T>::load(row, 32 * i + 8 * r4 + e);
+          dq[i][4 * r4 + e] += seen && !(fabsf(x) < INFINITY) ? NAN : 0.f;
+        }
   }
   if (qi < used) {
     TG* p = static_cast<TG*>(a.dq) + int64_t(qi) * qst + int64_t(head) * D;

@@ -437,9 +437,8 @@ kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_
  * do_i . o_i, which o's own rounding leaves inexact, is corrected from the sums
  * of P (dP - do . o), which are zero: with a bf16 o too, rows that look at few
  * keys have gradients as accurate as others.
- * Every sum has one owner and a fixed order: the same bits every time.  A
- * non-finite value in one sequence may reach gradients of its neighbours in
- * the packed buffer.
+ * Every sum has one owner and a fixed order: the same bits every time.  A NaN
+ * or infinity in a row reaches the gradients that depend on it and no others.
  */
 size_t kda_attn_prompt_bwd_workspace_bytes(int n, int Hq, int Hkv, int d);
 kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,

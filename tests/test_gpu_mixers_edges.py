@@ -1,5 +1,5 @@
 """Calls of the linear, prompt and cache entry points that their documentation allows at the ends of
-its ranges: a cache without pages, many heads in one call."""
+its ranges: a cache without pages, many heads in one call, NaN and infinities."""
 import ctypes
 import math
 
@@ -53,3 +53,46 @@ def test_linear_many_heads_of_one_call():
         torch.cuda.synchronize()
         assert torch.equal(o[b:b + n], o1) and torch.equal(So[b:b + n], S1)
         assert all(torch.equal(got[y][b:b + n], want[y]) for y in want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,d", [([30, 45, 20], 64), ([190, 260, 1, 69], 128)])
+def test_prompt_gradients_of_non_finite_rows(lens, d, dtype):
+    """A NaN or infinity in a row of one sequence reaches the gradients that depend on it, and no others: those
+    are the same bits as without it.  What depends on row r of its sequence: through q, dq of r, dk and dv of
+    keys up to r; through do, dq of r, dk up to r, one channel of dv up to r; through k, dq from r on, and all
+    of the sequence's dk and dv; through v, dq from r on, and dk."""
+    Hq, Hkv, ch = 4, 2, 3
+    gen = torch.Generator().manual_seed(len(lens))
+    n, cu = sum(lens), [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    clean = {x: torch.randn(n, h, d, generator=gen).to(dtype) for x, h in (("q", Hq), ("k", Hkv), ("v", Hkv), ("do", Hq))}
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+    def grads(x):
+        g = {y: z.to(DEV) for y, z in x.items()}
+        o, lse = kda.attn_prompt_fwd(g["q"], g["k"], g["v"], c, o_dtype=dtype)
+        r = kda.attn_prompt_bwd(g["q"], g["k"], g["v"], c, o, lse, g["do"], grad_dtype=dtype)
+        torch.cuda.synchronize()
+        return {y: z.cpu() for y, z in r.items()}
+
+    want = grads(clean)
+    a, b = cu[1], cu[2]
+    for r in (a, a + lens[1] // 2, b - 1):
+        for name, val in (("q", math.nan), ("do", math.nan), ("do", math.inf), ("k", math.nan), ("v", math.nan), ("v", -math.inf)):
+            x = dict(clean, **{name: clean[name].clone()})
+            x[name][r, :, ch] = val
+            got = grads(x)
+            hit = {"dq": range(r, r + 1) if name in ("q", "do") else range(r, b),
+                   "dk": range(a, r + 1) if name in ("q", "do") else range(a, b),
+                   "dv": range(a, r + 1) if name in ("q", "do") else range(a, b) if name == "k" else range(0)}
+            for y, rows in hit.items():
+                same = [i for i in range(n) if i not in rows]
+                assert torch.equal(got[y][same], want[y][same]), (name, val, r, y)
+                if name == "do" and y == "dv":
+                    rest = [i for i in range(d) if i != ch]
+                    assert torch.equal(got[y][..., rest], want[y][..., rest]), (val, r)
+                    assert not torch.isfinite(got[y][list(rows), :, ch]).any(), (val, r)
+                elif len(rows):
+                    assert not torch.isfinite(got[y][list(rows)]).any(), (name, val, r, y)
