@@ -361,6 +361,7 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
       }
 
       const float ec = ga[4 * C];
+      const bool clean = fabsf(S[0][0]) < INFINITY;
 #pragma unroll
       for (int i = 0; i < NKT; ++i) S[i] *= ec;
 #pragma unroll
@@ -378,6 +379,12 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
       }
 
       if constexpr (OUT > 0) {
+        // Scores of tokens that do not see a value are zero, and zero times a NaN or infinity is not: such
+        // values, which the updated state of their column shows, leave the product.
+        const bool spoiled = __any(clean && !(fabsf(S[0][0]) < INFINITY));
+        if (spoiled)
+#pragma unroll
+          for (int u = 0; u < U; ++u) vf[u] = Finite<T>::only(vf[u]);
         lds_barrier();  // the scores are there
         const uint32_t pb = TP::at(P) + prow;
 #pragma unroll
@@ -389,6 +396,21 @@ __global__ __launch_bounds__((WalkShape<T, DK, DV, OUT>::NT)) void linear_walk_k
               if (REV ? u < tt / 2 : u > tt / 2) continue;
               acc[tt] = O::mma16(vf[u], TP::row8_16(pb + i * W::kP1, tt, u), acc[tt]);
             }
+        if (spoiled) {  // and are added for the tokens that see them
+          const int live = a.T - c * C < C ? a.T - c * C : C;
+#pragma unroll 1
+          for (int s = 0; s < live; ++s) {
+            const f32x4 x = TV::get4(Vs(n), s, 16 * wave + 4 * g4);
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+              const int t = 16 * tt + l16;
+              const float p = io<T>::load(P, TP::off(t, s));
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[tt][r] += (REV ? s >= t : s <= t) && !(fabsf(x[r]) < INFINITY) ? p * x[r] : 0.f;
+            }
+          }
+        }
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
           const int64_t t = t0 + 16 * tt + l16;

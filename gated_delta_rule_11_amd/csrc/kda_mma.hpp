@@ -99,8 +99,8 @@ template <> struct Finite<bf16_t> {
     u32x4 w = __builtin_bit_cast(u32x4, a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if ((~w[i] & 0x7f80u) == 0) w[i] &= 0xffff0000u;
-      if ((~w[i] & 0x7f800000u) == 0) w[i] &= 0xffffu;
+      const u16x2 e = __builtin_elementwise_min(__builtin_bit_cast(u16x2, ~w[i] & 0x7f807f80u), u16x2{1, 1});
+      w[i] &= __builtin_bit_cast(uint32_t, u16x2{0, 0} - e);
     }
     return __builtin_bit_cast(bf16x8, w);
   }

@@ -358,8 +358,9 @@ kda_status kda_decode_replay(const void* q, const void* k, const void* v,
  *        -10000 (a decay of zero); -inf clears the state.  A positive g is not
  *        an error, but sums beyond 80 in a chunk overflow fp32.
  *
- * A non-finite q, k or v reaches outputs of its own and later tokens, and may
- * reach any output of its 64-token chunk.
+ * A NaN or infinity reaches what depends on it and nothing else (outputs of its
+ * own and later tokens; in the backward, gradients likewise), but for dg, where
+ * it may reach all tokens of its block of 256 (fp32 inputs: 128).
  */
 
 /*

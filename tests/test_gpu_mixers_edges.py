@@ -96,3 +96,46 @@ def test_prompt_gradients_of_non_finite_rows(lens, d, dtype):
                     assert not torch.isfinite(got[y][list(rows), :, ch]).any(), (val, r)
                 elif len(rows):
                     assert not torch.isfinite(got[y][list(rows)]).any(), (name, val, r, y)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H,dk,dv", [(150, 2, 128, 128), (90, 2, 16, 64), (70, 1, 64, 16), (900, 1, 32, 32)])
+def test_linear_non_finite_values(T, H, dk, dv, dtype):
+    """A NaN or infinity in token s reaches what depends on it, and nothing else changes by a bit: through q
+    its own output, dk (one channel) and dv up to s; through k outputs and dq (one channel) from s on, and
+    its own dv; through v one channel of the outputs from s on, dq from s on, and its own dk; through do its own
+    dq, dk and dv (one channel) up to s; through g outputs from s on."""
+    B, ch = 2, 3
+    gen = torch.Generator().manual_seed(T)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    clean = {"q": unit(rn(B, T, H, dk)).to(dtype), "k": unit(rn(B, T, H, dk)).to(dtype), "v": rn(B, T, H, dv).to(dtype),
+             "g": -0.1 * torch.rand(B, T, H, generator=gen), "do": rn(B, T, H, dv).to(dtype)}
+
+    def run(x):
+        g = [x[n].to(DEV) for n in ("q", "k", "v", "g")]
+        o, S = kda.linear_chunk_fwd(*g, o_dtype=dtype)
+        r = kda.linear_chunk_bwd(*g, x["do"].to(DEV), grad_dtype=dtype)
+        torch.cuda.synchronize()
+        return {"o": o.cpu(), **{n: r[n].cpu() for n in ("dq", "dk", "dv")}}
+
+    want = run(clean)
+    none, one = range(0), slice(ch, ch + 1)
+    for s in (0, 20, 63, T - 5, T - 1):
+        own, back, on = range(s, s + 1), range(0, s + 1), range(s, T)
+        hits = {"q": {"o": (own, None), "dq": (none, None), "dk": (back, one), "dv": (back, None)},
+                "k": {"o": (on, None), "dq": (on, one), "dk": (none, None), "dv": (own, None)},
+                "v": {"o": (on, one), "dq": (on, None), "dk": (own, None), "dv": (none, None)},
+                "do": {"o": (none, None), "dq": (own, None), "dk": (back, None), "dv": (back, one)},
+                "g": {"o": (on, None)}}
+        for name, hit in hits.items():
+            for val in (math.nan, math.inf) if name in ("v", "do") else (math.nan,):
+                x = dict(clean, **{name: clean[name].clone()})
+                x[name][(1, s, 0) if name == "g" else (1, s, 0, ch)] = val
+                got = run(x)
+                for y, (rows, chan) in hit.items():
+                    mark = torch.zeros(got[y].shape, dtype=torch.bool)
+                    if len(rows):
+                        mark[1, rows[0]:rows[-1] + 1, 0, chan if chan else slice(None)] = True
+                    assert torch.equal(got[y][~mark], want[y][~mark]), (name, val, s, y)
+                    assert not torch.isfinite(got[y][mark]).any(), (name, val, s, y)
