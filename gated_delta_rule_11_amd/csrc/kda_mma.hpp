@@ -42,7 +42,6 @@ template <typename T> struct Op;
 
 template <> struct Op<bf16_t> {
   typedef bf16x8 frag;
-  __device__ __forceinline__ static frag zero() { return __builtin_bit_cast(frag, u32x4{0, 0, 0, 0}); }
   __device__ __forceinline__ static frag load(const bf16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
   __device__ __forceinline__ static frag join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -61,7 +60,6 @@ template <> struct Op<bf16_t> {
 
 template <> struct Op<float> {
   typedef f32x8 frag;
-  __device__ __forceinline__ static frag zero() { return frag{0, 0, 0, 0, 0, 0, 0, 0}; }
   __device__ __forceinline__ static frag load(const float* p) {
     return join(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
   }
@@ -324,32 +322,6 @@ __device__ __forceinline__ float sum_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-
-// Rows of a global matrix staged through registers: `NT` threads hold a tile of ROWS rows of
-// PCOLS elements, of which the first COLS come from memory (the rest, and rows at or past
-// `valid`, are zero).  load() issues the reads, store() puts them into a Tile.
-template <typename T, int ROWS, int COLS, int PCOLS, int NT>
-struct Stage {
-  typedef Tile<T, PCOLS> L;
-  static constexpr int N = (ROWS * L::CH + NT - 1) / NT;
-  u32x4 r[N];
-  __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t valid, int tid) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = tid + i * NT, row = e / L::CH, ch = e % L::CH;
-      r[i] = u32x4{0, 0, 0, 0};
-      if (row < valid && row < ROWS && ch * L::EPC < COLS)
-        r[i] = *reinterpret_cast<const u32x4*>(base + row * stride + ch * L::EPC);
-    }
-  }
-  __device__ __forceinline__ void store(T* t, int tid) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = tid + i * NT, row = e / L::CH, ch = e % L::CH;
-      if (row < ROWS) *reinterpret_cast<u32x4*>(t + L::off(row, ch * L::EPC)) = r[i];
-    }
-  }
-};
 
 // Dispatch of workgroups to consecutive work items per XCD: the hardware deals workgroups to
 // the eight XCDs in turn; the returned index gives each XCD one contiguous run of items, so that

@@ -87,7 +87,7 @@ struct KvShape {
 };
 
 template <typename T, typename TG, int D>
-__global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs a, int ntile) {
+__global__ __launch_bounds__(256, 1) void prompt_dkv_kernel(const PromptBwdArgs a) {
   using O = Op<T>;
   using F = typename O::frag;
   using TD = Tile<T, D>;
@@ -499,7 +499,7 @@ hipError_t launch_dkv(const PromptBwdArgs& a, int ntile, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), int(lds), done);
   if (e != hipSuccess) return e;
-  kern<<<dim3(uint32_t(int64_t(ntile) * a.Hkv * a.parts)), 256, lds, st>>>(a, ntile);
+  kern<<<dim3(uint32_t(int64_t(ntile) * a.Hkv * a.parts)), 256, lds, st>>>(a);
   return hipGetLastError();
 }
 
