@@ -486,12 +486,17 @@ def _dims(what: str, *specs):
             raise KDAError(f"{what}: {name} must be a tensor of {n} dimensions")
 
 
+_MAY_BE_NONE = ("S_in", "S_out", "dS_out", "lse")  # (where one of them is required, the C ABI says so)
+
+
 def _match(what: str, *specs):
-    """One pass over (name, tensor or None, shape, allowed dtypes): what ``_shapes`` and ``_dev`` check."""
+    """One pass over (name, tensor, shape, allowed dtypes): what ``_shapes`` and ``_dev`` check."""
     dev = None
     for name, t, shape, dtypes in specs:
-        if t is None:
-            continue
+        if not isinstance(t, torch.Tensor):
+            if t is None and name in _MAY_BE_NONE:
+                continue
+            raise KDAError(f"{what}: {name} must be a tensor")
         if t.shape != shape:
             raise KDAError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t.dtype not in dtypes:

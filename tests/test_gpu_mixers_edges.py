@@ -139,3 +139,24 @@ def test_linear_non_finite_values(T, H, dk, dv, dtype):
                         mark[1, rows[0]:rows[-1] + 1, 0, chan if chan else slice(None)] = True
                     assert torch.equal(got[y][~mark], want[y][~mark]), (name, val, s, y)
                     assert not torch.isfinite(got[y][mark]).any(), (name, val, s, y)
+
+
+def test_what_is_no_tensor_is_refused():
+    """A missing or foreign argument is the binding's own error, whichever it is."""
+    q = torch.zeros(1, 4, 2, 64, device=DEV)
+    g, cu, S = q[..., 0].contiguous(), torch.tensor([0, 4], dtype=torch.int32, device=DEV), torch.zeros(4, 2, 64, 64, device=DEV)
+    c = torch.zeros(1, 2, 16, 64, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    ct, s, s2, one = c.clone().view(1, 2, 64, 16), torch.ones(1, 2, device=DEV), torch.ones(1, 2, device=DEV), cu[:1]
+    table = one.view(1, 1)
+    calls = [(kda.linear_chunk_fwd, [q, q, q, g]), (kda.linear_chunk_bwd, [q, q, q, g, q]),
+             (kda.linear_decode_step, [q[0], q[0], q[0], g[0], S]), (kda.attn_prompt_fwd, [q[0], q[0], q[0], cu]),
+             (kda.attn_prompt_bwd, [q[0], q[0], q[0], cu, q[0], g[0], q[0]]),
+             (kda.kv_cache_append, [q[0], q[0], cu, one, table, c, ct, s, s2]),
+             (kda.attn_decode_step, [q[0, :1], c, ct, s, s2, table, one])]
+    for call, args in calls:
+        call(*args)
+        for i in range(1, len(args)):
+            for bad in (None, [0.0], 3):
+                with pytest.raises(kda.KDAError):
+                    call(*args[:i], bad, *args[i + 1:])
+    torch.cuda.synchronize()
