@@ -574,7 +574,8 @@ def linear_chunk_fwd(q, k, v, g, S_in=None, o=None, S_out=None, o_dtype=None, sc
                      want_state: bool = True, workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Linear attention with a decay per head: S_t = e^g S_{t-1} + k v^T, o_t = scale S_t^T q.
     q, k [B,T,H,dk], v [B,T,H,dv]; g fp32 log-decays (at most 0), [B,T,H] or [H].
-    Returns (o [B,T,H,dv], S_out [B,H,dk,dv] or None).  ``stream``: as everywhere."""
+    Returns (o [B,T,H,dv], S_out [B,H,dk,dv] or None).  bf16 inputs are multiplied in bf16, with an fp32 o
+    (the default) too; the state is fp32-accurate.  ``stream``: as everywhere."""
     what = "kda_linear_chunk_fwd"
     _dims(what, ("q", q, 4), ("v", v, 4))
     o, S_out = _outs(q, v, o, S_out, _out_dtype(o_dtype, what, "o_dtype"), want_state)
@@ -666,6 +667,7 @@ def attn_prompt_fwd(q, k, v, cu_seqlens, scale: Optional[float] = None, o=None, 
                     want_lse: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Causal attention over packed prompts: q [n,Hq,d], k, v [n,Hkv,d], sequence s in rows
     cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32, on the device).  ``scale`` defaults to 1 / sqrt(d).
+    With bf16 inputs probabilities are rounded to bf16, with an fp32 o (the default) too.
     Returns (o [n,Hq,d], lse [n,Hq] fp32 or None).  Rows behind the last sequence are not written:
     given ``o`` and ``lse`` keep what they hold there, new ones are zero there."""
     what = "kda_attn_prompt_fwd"
@@ -747,7 +749,7 @@ def attn_decode_step(q, k_cache, v_cache, k_scale, v_scale, block_table, context
                      o=None, lse=None, o_dtype=None, want_lse: bool = False,
                      workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Attention of one token per sequence over a paged cache in 8 bits (``kv_cache_append``):
-    q [N,Hq,d].  ``scale`` defaults to 1 / sqrt(d).  Returns (o [N,Hq,d], lse [N,Hq] fp32 or
+    q [N,Hq,d].  ``scale`` defaults to 1 / sqrt(d).  bf16 queries' probabilities are rounded to bf16.  Returns (o [N,Hq,d], lse [N,Hq] fp32 or
     None); a sequence with no tokens gets o = 0, lse = -inf."""
     what = "kda_attn_decode_step"
     _dims(what, ("q", q, 3), ("k_cache", k_cache, 4))

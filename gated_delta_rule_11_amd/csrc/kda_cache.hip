@@ -211,7 +211,7 @@ __device__ __forceinline__ float sum_groups(float x) {
 // 16 g .. + 15 of its column's head: row r of product t is token 16 (r / 4) + 4 t + r % 4.  The
 // probabilities are then in place as the operand of O^T = V^T P^T, and V's 16 tokens of a lane are one load.
 // Codes are exact in bf16; the scales (powers of two) multiply scores and probabilities in fp32
-// and cost nothing; with bf16 queries P is rounded to bf16, 2^-8 of each term, as the output is.
+// and cost nothing; with bf16 queries P is rounded to bf16, 2^-8 of each term, as a bf16 output is.
 // fp32 queries and their probabilities go in as three bf16 parts that sum to them: every product
 // is exact, and three bf16 instructions take a fifth of the time of the eight fp32 ones.
 template <typename T, typename TO, int D>
@@ -481,7 +481,10 @@ hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t st) {
 }
 
 // Parts of a context: enough workgroups to fill the GPU with a few each, none with less than one
-// tile for each of its wavefronts.  Measured, 512 : 1024 : 2048 workgroups, us, 8 key heads, d = 128:
+// tile for each of its wavefronts.  The rule goes by max_pages and the batch, not by each context's length:
+// from 1024 sequence and key head pairs on no context is cut, and one that is far longer than the others ends
+// late (8 key heads: one of 131072 tokens among 31, 127 or 255 of 1024 takes 317, 1236, 1243 us; alone 58).
+// Measured, 512 : 1024 : 2048 workgroups, us, 8 key heads, d = 128:
 // contexts alike, 1 of 131072 tokens 54 : 57 : 65, 8 of 16384 53 : 54 : 58; contexts of any length up
 // to 16384, 8 of them 37 : 32 : 39, 32 of them 142 : 125 : 123.
 int cache_step_splits(int N, int Hq, int Hkv, int page, int max_pages) {

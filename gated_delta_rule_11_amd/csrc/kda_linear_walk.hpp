@@ -31,15 +31,17 @@
 // layout is an operand's), the values' transposing reads serve both P V and the update.
 //
 // With bf16 elements P, and the copy of S that the outputs read, are rounded to bf16, 2^-8 of each
-// term, half a unit of the last place that the outputs have anyway.  The state takes its rows
+// term, half a unit of the last place that the outputs have anyway where they are bf16 (fp32 outputs of
+// bf16 elements carry it too).  The state takes its rows
 // e^{G_C - G_s} v_s as three bf16 parts (24 bits), so it is fp32-accurate however long the
 // sequence; with DOT, P and S too.
 //
-// Measured (bf16, B = 4, T = 32768, H = 32, 128 x 128): 1160 us for 4.33 GB, 3.7 TB/s (857 us at a
-// copy's rate; the memory accesses alone take 933 us in this shape, all but them 870).  Left out
+// Measured (bf16, B = 4, T = 32768, H = 32, 128 x 128): 1145 us for 4.33 GB, 3.8 TB/s (857 us at a
+// copy's rate, 720 at the best of the library's kernels; the memory accesses alone take 933 us in this
+// shape, all but them 870).  Matrix pipe 27 %, vector issue 39 % of the cycles, 4.74 GB moved.  Left out
 // one at a time, the exact parts save 135 us, the scores 115, the stores 118, the copies 207: the
 // sum of issue and bytes in one workgroup per compute unit bounds it, the LDS being full with three
-// chunks in rotation.  The walk without outputs (segments' end states) takes 170 us for 0.54 GB.
+// chunks in rotation.  The walk without outputs (segments' end states) takes 142 to 172 us for 0.54 GB.
 //
 // Few, long sequences are cut into segments (the ABI layer's rule).  The decay being a scalar, a
 // segment's transition is one number: a first walk leaves every segment's end state from zero, a

@@ -44,7 +44,9 @@ constexpr int64_t kMinSegChunks = 4;
 // Nor is a sequence of fewer chunks than this cut: two more launches cost what they save.  Measured,
 // cut : whole, us, 8 heads: 8 chunks, bf16, 24 : 19 (d = 128) and 23 : 16 (64), fp32 33 : 34 and 22 : 15
 // (32), with gradients 107 : 102, 86 : 84, 137 : 146 and 69 : 61; 12 chunks 24 : 27, 23 : 21, 34 : 49,
-// with gradients 110 : 144, 87 : 118, 140 : 210.
+// with gradients 110 : 144, 87 : 118, 140 : 210.  Fewer heads are alike (one of 12 chunks, d = 128: 23 : 25
+// and, gradients alone, 82 : 117); at 64, with two segments each, cutting gains little or costs up to a
+// third: 12 chunks, d = 128, bf16 36 : 27 and 131 : 125, fp32 50 : 50 and 160 : 170, d = 64 23 : 22 and 82 : 102.
 constexpr int64_t kMinCutChunks = 12;
 LinearForm linear_form(int64_t B, int64_t T, int64_t H, int dv, bool bf16) {
   const int C = linear_chunk(bf16);

@@ -16,11 +16,13 @@
 // order the registers have, which the transposing reads of V follow).  The running maximum is
 // raised only when a tile exceeds it by 2^8 (any reference serves while nothing overflows), so
 // most tiles do not touch the accumulators.  Maximum, sum and accumulators are fp32; with bf16
-// elements P is rounded to bf16 for the second product, 2^-8 relative each, as the outputs are.
+// elements P is rounded to bf16 for the second product, 2^-8 relative each, as bf16 outputs are (and fp32
+// outputs of bf16 elements then carry).
 //
 // Measured (bf16, 16270 rows in sequences of 8192, 5000, 1, 2300 and 777, 32 heads on 8, d = 128):
-// 928 us, 866 TFLOP/s of the masked half, where a large matrix product reaches 1230.  What bounds
-// it is the issue of the matrix instructions and of the exponentials between them; the LDS is read
+// 919 us, 875 TFLOP/s of the masked half, where a large matrix product reaches 1230.  What bounds
+// it is the issue of the matrix instructions (38 % of the cycles) and of the vector instructions between
+// them (50 %, not counting that an exponential holds its unit four times as long); the LDS is read
 // without conflicts (they were 34 % of its cycles before the rows were permuted, and the time did
 // not change).  The order of the tiles, longest rows first, lets the short ones fill the end.
 #include "kda_prompt.hpp"

@@ -352,6 +352,11 @@ kda_status kda_decode_replay(const void* q, const void* k, const void* v,
  * and sizes less).  The backward also needs B*H*ceil(T/256), with fp32 inputs
  * B*H*ceil(T/128), below 2^23.  Beyond any of these: KDA_ERR_SHAPE.
  *
+ * With bf16 inputs the decayed scores q.k, and the copies of the state (of its
+ * gradient) that o (dv) reads, are rounded to bf16 for their products, 2^-8 of a term, whatever the
+ * type of o and dv.  States, dS_in, dg, dq and dk have fp32 accuracy (before dq
+ * and dk are rounded to grad_dtype).
+ *
  *   q, k [B,T,H,dk] in_dtype    v [B,T,H,dv] in_dtype
  *   g    fp32 log-decays, at most 0: [B,T,H] (g_per_head == 0), or [H], the
  *        same for every token (g_per_head == 1).  Values below -10000 act as
@@ -425,6 +430,9 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, k
  *       (Entries outside [0, n] or out of order give meaningless results, but
  *       no access outside the arrays.)
  *   o   [n,Hq,d] o_dtype (written)       lse [n,Hq] fp32 (written) or NULL
+ * Sums and statistics are fp32.  With bf16 inputs the probabilities (and dS in
+ * the backward) are rounded to bf16 for the products that follow, 2^-8 of a
+ * term, whatever the outputs' type.
  */
 kda_status kda_attn_prompt_fwd(const void* q, const void* k, const void* v, kda_dtype in_dtype, const int* cu_seqlens,
                                void* o, kda_dtype o_dtype, float* lse, int n, int n_seqs, int Hq, int Hkv, int d,
@@ -457,7 +465,8 @@ kda_status kda_attn_prompt_bwd(const void* q, const void* k, const void* v, kda_
  *   k_scale, v_scale [n_pages,Hkv] fp32: a value is code * scale.  A scale is a
  *       power of two, the smallest with max |x| <= 448 scale (at least 2^-100).
  *   block_table [N,max_pages] int32: the page of tokens p page .. of sequence n
- *       is block_table[n,p].  Each page belongs to one sequence.
+ *       is block_table[n,p].  A page that an append writes to must appear once
+ *       only, in one sequence; pages that are only attended may be shared.
  *   context_len [N] int32: the tokens a sequence holds.
  * All of them in device memory.
  *
@@ -478,6 +487,8 @@ kda_status kda_kv_cache_append(const void* k, const void* v, kda_dtype in_dtype,
  * kda_attn_decode_step -- attention of one query token per sequence over all
  * tokens it holds (append the token's own key and value first):
  *   q [N,Hq,d] in_dtype -> o [N,Hq,d] o_dtype, lse [N,Hq] fp32 or NULL.
+ * With bf16 queries the probabilities are rounded to bf16 for the product with
+ * the values, 2^-8 of a term, whatever the type of o.
  * A sequence with no tokens gets o = 0, lse = -inf.  Tokens past max_pages
  * pages, or in a page whose id is outside [0, n_pages), are left out.  What
  * lies in a page behind the last token is not used, whatever it holds.  With
