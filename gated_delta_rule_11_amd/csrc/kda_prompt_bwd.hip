@@ -18,11 +18,11 @@
 // gradients may be.
 //
 // Measured (bf16, 8192 rows in sequences of 4096, 1023, 2500, 64 and 509, 16 heads on 4, d = 128):
-// dk and dv 338 us, dq 194, D 12, the join of the parts 22 (least of 20 calls; on average 360, 208).  What bounds the first is its K, V, dK
-// and dV in registers (one wavefront per SIMD): its products take 75 us less when left out, its
-// exponentials 38, its copies 39, so none of them is hidden completely.  Four tiles of rows are in
-// rotation there, read a step before their products; masks are formed without branches, and only in
-// the tiles that need them (577 to 382 us).
+// dk and dv 338 us, dq 194, D 12, the join of the parts 22 (least of 20 calls; on average 360 and 208).
+// What bounds the first is its K, V, dK and dV in registers (one wavefront per SIMD): left out, its
+// products save 75 us, its exponentials 38, its copies 39, so none of them is hidden completely.  Four
+// tiles of rows are in rotation there, read a step before their products; masks are formed without
+// branches, and only in the tiles that need them (577 to 382 us).
 #include <type_traits>
 
 #include "kda_prompt.hpp"

@@ -353,14 +353,14 @@ kda_status kda_decode_replay(const void* q, const void* k, const void* v,
  * B*H*ceil(T/128), below 2^23.  Beyond any of these: KDA_ERR_SHAPE.
  *
  * With bf16 inputs the decayed scores q.k, and the copies of the state (of its
- * gradient) that o (dv) reads, are rounded to bf16 for their products, 2^-8 of a term, whatever the
- * type of o and dv.  States, dS_in, dg, dq and dk have fp32 accuracy (before dq
- * and dk are rounded to grad_dtype).
+ * gradient) that o (dv) reads, are rounded to bf16 for their products, 2^-8 of a
+ * term, whatever the type of o and dv.  States, dS_in, dg, dq and dk have fp32
+ * accuracy (before dq and dk are rounded to grad_dtype).
  *
  *   q, k [B,T,H,dk] in_dtype    v [B,T,H,dv] in_dtype
  *   g    fp32 log-decays, at most 0: [B,T,H] (g_per_head == 0), or [H], the
  *        same for every token (g_per_head == 1).  Values below -10000 act as
- *        -10000 (a decay of zero); -inf clears the state.  A positive g is not
+ *        -10000 (a decay of zero); -inf clears a finite state.  A positive g is not
  *        an error, but sums beyond 80 in a chunk overflow fp32.
  *
  * A NaN or infinity reaches what depends on it and nothing else (outputs of its
