@@ -346,7 +346,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void prompt_dq_kernel(
 #pragma unroll
   for (int i = 0; i < ND; ++i) dq[i] = zero16();
   int bad_lo = hi, bad_hi = 0;  // keys of masked tiles with non-finite values
-  const bool correct = DB || a.o_bf16;  // D is not exact to fp32
+  const bool correct = sizeof(T) == 2 || a.o_bf16;  // D is not exact to fp32
   auto fetch = [&](int t) {
     T* kb = buf + (DB ? (t & 1) * 2 * BN * D : 0);
     copy_rows<T, BN, D, 4>(kb, kp, kst, lo + t * BN, hi, wave, lane);
