@@ -19,7 +19,9 @@ Beside the delta rule, on the same layouts:
   linear_decode_step(q, k, v, g, S)               -> (o, S)      (S updated in place unless S_out is given)
   attn_prompt_fwd(q, k, v, cu_seqlens)            -> (o, lse)    causal attention over packed prompts
   attn_prompt_bwd(q, k, v, cu_seqlens, o, lse, d_o) -> gradients
+  rope(x, positions, inv_freq)                    -> y           rotary positions, or (inverse) their gradient
   kv_cache_append(k, v, cu_seqlens, ...)          -> None        paged cache in 8 bits, written in place
+  kv_cache_append_rope(k, v, cu_seqlens, ...)     -> q turned    the same with rotary positions on the way
   attn_decode_step(q, k_cache, v_cache, ...)      -> (o, lse)    attention of one token over it
 """
 from __future__ import annotations
@@ -34,7 +36,7 @@ import torch
 __all__ = ["gate", "chunk_fwd", "chunk_fwd_z", "chunk_fwd_workspace_bytes", "decode_step", "chunk_uses_mfma", "lib",
            "linear_chunk_fwd", "linear_chunk_fwd_workspace_bytes", "linear_chunk_bwd",
            "linear_chunk_bwd_workspace_bytes", "linear_decode_step", "attn_prompt_fwd", "attn_prompt_bwd",
-           "attn_prompt_bwd_workspace_bytes", "kv_cache_append", "attn_decode_step",
+           "attn_prompt_bwd_workspace_bytes", "rope", "kv_cache_append", "kv_cache_append_rope", "attn_decode_step",
            "attn_decode_step_workspace_bytes", "KDAError", "LIB_PATH", "G_MIN"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
@@ -110,6 +112,12 @@ def lib() -> ctypes.CDLL:
     L.kda_attn_prompt_bwd.restype = I
     L.kda_kv_cache_append.argtypes = [P, P, I, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
     L.kda_kv_cache_append.restype = I
+    W = ctypes.c_int64
+    L.kda_rope.argtypes = [P, I, W, P, I, P, P, I, I, I, P, I, W, I, I, I, P]
+    L.kda_rope.restype = I
+    L.kda_kv_cache_append_rope.argtypes = [P, W, P, W, I, P, W, P, I, W, P, I, P, P, I, I, P, P, P, P, P, P, P, I, I, I, I, I, I,
+                                           I, I, I, P]
+    L.kda_kv_cache_append_rope.restype = I
     L.kda_attn_decode_step_workspace_bytes.argtypes = [I] * 6
     L.kda_attn_decode_step_workspace_bytes.restype = Z
     L.kda_attn_decode_step.argtypes = [P, I, P, P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, F, P, Z, P]
@@ -709,6 +717,66 @@ def attn_prompt_bwd(q, k, v, cu_seqlens, o, lse, d_o, scale: Optional[float] = N
     return out
 
 
+def _rows(what: str, name: str, t, shape, dtypes, like) -> int:
+    """Checks a tensor [n, H, d] whose rows may lie apart (a view of a projection's output), each
+    row's heads together, on ``like``'s device; its row stride in elements."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        raise KDAError(f"{what}: {name} must be a tensor of shape {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise KDAError(f"{what}: {name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if not t.is_cuda:
+        raise KDAError("libkda runs on the GPU only: tensor is on the CPU")
+    if t.get_device() != like.get_device():
+        raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on {like.device}")
+    n, H, d = shape
+    row, head, one = t.stride()
+    if t.numel() and ((d > 1 and one != 1) or (H > 1 and head != d) or (n > 1 and row < H * d)):
+        raise KDAError(f"{what}: {name} has strides {t.stride()}: a row's {H} heads of {d} must lie together")
+    return row if n > 1 and t.numel() else H * d
+
+
+def _turn(what: str, n: int, positions, inv_freq, axes, interleaved, like):
+    """Arguments of a rotation after their checks: positions, axes' number, inv_freq, axes, rot, interleaved."""
+    _dims(what, ("inv_freq", inv_freq, 1))
+    half, A = inv_freq.shape[0], 1
+    specs = [("inv_freq", inv_freq, (half,), _F32)]
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+            raise KDAError(f"{what}: positions must be a tensor [n] or [n, axes]")
+        A = positions.shape[1] if positions.dim() == 2 else 1
+        specs.append(("positions", positions, (n,) if positions.dim() == 1 else (n, A), _I32))
+    if axes is not None:
+        specs.append(("axes", axes, (half,), _I32))
+    _match(what, *specs)
+    for name, t, _, _ in specs:
+        if t.get_device() != like.get_device():
+            raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on {like.device}")
+    return _a(positions), A, _a(inv_freq), _a(axes), 2 * half, int(bool(interleaved))
+
+
+@_run_on_stream
+def rope(x, positions, inv_freq, axes=None, interleaved: bool = False, inverse: bool = False, out=None,
+         out_dtype=None) -> torch.Tensor:
+    """Rotary positions: pair j of every head's channels of x [n,H,d] turns by
+    positions[row, axes[j]] * inv_freq[j].  positions [n] or [n,axes] int32, inv_freq [rot/2] fp32 (channels from
+    rot on are copied), axes [rot/2] int32 or None (all of axis 0); pairs are (j, j + rot/2), or (2j, 2j + 1) where
+    ``interleaved``.  ``inverse`` turns backwards: the gradient, dx from dy.  x may be a view whose rows lie apart; so may
+    ``out``, which may be x itself.  Returns y [n,H,d] (``out_dtype``, default x's)."""
+    what = "kda_rope"
+    _dims(what, ("x", x, 3))
+    n, H, d = x.shape
+    xs = _rows(what, "x", x, (n, H, d), _IO, x)
+    if out is None:
+        out = torch.empty((n, H, d), dtype=_out_dtype(out_dtype or x.dtype, what, "out_dtype"), device=x.device)
+    ys = _rows(what, "out", out, (n, H, d), _IO, x)
+    if not isinstance(positions, torch.Tensor):
+        raise KDAError(f"{what}: positions must be a tensor [n] or [n, axes]")
+    pos, A, inv, ax, rot, inter = _turn(what, n, positions, inv_freq, axes, interleaved, x)
+    _check(lib().kda_rope(_a(x), _dtype_code(x), xs, pos, A, inv, ax, rot, inter, int(bool(inverse)), _a(out),
+                          _dtype_code(out), ys, n, H, d, _here(x)), what)
+    return out
+
+
 _F8 = (torch.float8_e4m3fn,)
 
 
@@ -737,6 +805,41 @@ def kv_cache_append(k, v, cu_seqlens, context_len, block_table, k_cache, v_cache
     _check(lib().kda_kv_cache_append(_a(k), _a(v), _dtype_code(k), _a(cu_seqlens), _a(context_len), _a(block_table),
                                      _a(k_cache), _a(v_cache), _a(k_scale), _a(v_scale), n, N, Hkv, d, page, pages, mp,
                                      _here(k)), what)
+
+
+@_run_on_stream
+def kv_cache_append_rope(k, v, cu_seqlens, context_len, block_table, k_cache, v_cache, k_scale, v_scale, inv_freq,
+                         positions=None, axes=None, interleaved: bool = False, q=None, q_out=None,
+                         q_out_dtype=None) -> Optional[torch.Tensor]:
+    """``kv_cache_append`` with rotary positions (``rope``) applied to k on the way, and to the same tokens'
+    queries q [n,Hq,d] if given, in one launch.  ``positions`` [n] or [n,axes] int32; None: each token's place in its
+    sequence.  k, v and q may be views whose rows lie apart (of one projection's output); ``q_out`` too, and it may be q.
+    Returns the turned queries (``q_out_dtype``, default q's), or None without q.  Rows behind the last
+    sequence: a given ``q_out`` keeps what it holds there, a new one is zero there."""
+    what = "kda_kv_cache_append_rope"
+    _dims(what, ("k", k, 3), ("cu_seqlens", cu_seqlens, 1), ("context_len", context_len, 1))
+    n, Hkv, d = k.shape
+    k_row, v_row = _rows(what, "k", k, (n, Hkv, d), _IO, k), _rows(what, "v", v, (n, Hkv, d), _io_of(k), k)
+    given, Hq, q_row, o_row, o_code = q_out is not None, Hkv, Hkv * d, Hkv * d, _dtype_code(k)
+    if q is not None:
+        _dims(what, ("q", q, 3))
+        Hq = q.shape[1]
+        q_row = _rows(what, "q", q, (n, Hq, d), _io_of(k), k)
+        if not given:
+            q_out = torch.empty((n, Hq, d), dtype=_out_dtype(q_out_dtype or q.dtype, what, "q_out_dtype"), device=q.device)
+        o_row, o_code = _rows(what, "q_out", q_out, (n, Hq, d), _IO, k), _dtype_code(q_out)
+    elif given:
+        raise KDAError(f"{what}: q_out without q")
+    pos, A, inv, ax, rot, inter = _turn(what, n, positions, inv_freq, axes, interleaved, k)
+    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
+                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32))
+    if cu_seqlens.get_device() != k.get_device():
+        raise KDAError(f"{what}: cu_seqlens is on {cu_seqlens.device}, the other tensors on {k.device}")
+    _check(lib().kda_kv_cache_append_rope(_a(k), k_row, _a(v), v_row, _dtype_code(k), _a(q), q_row, _a(q_out), o_code, o_row,
+                                          pos, A, inv, ax, rot, inter, _a(cu_seqlens), _a(context_len), _a(block_table),
+                                          _a(k_cache), _a(v_cache), _a(k_scale), _a(v_scale), n, N, Hq, Hkv, d, page, pages,
+                                          mp, int(not given), _here(k)), what)
+    return q_out
 
 
 def attn_decode_step_workspace_bytes(N: int, Hq: int, Hkv: int, d: int, page: int, max_pages: int) -> int:

@@ -54,4 +54,21 @@ inline bool all_aligned(std::initializer_list<const void*> vec16, const void* be
   return aligned(beta, beta_size);
 }
 
+// A launch holds fewer than 2^32 threads.  In workgroups of 256, which all kernels of the mixers have but
+// the linear walks (linear_threads; see walk_grid_ok):
+constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
+
+// ---- prompts and cache ------------------------------------------------------------------
+
+inline bool attn_dim_ok(int d) { return d == 64 || d == 128; }
+inline bool page_ok(int p) { return p == 16 || p == 32 || p == 64; }
+
+// n rows (or N sequences) of Hq heads in groups over Hkv, d wide.
+inline kda_status heads_ok(int64_t n, int64_t Hq, int64_t Hkv, int64_t d) {
+  // the last tile of rows ends within 32 bits
+  if (!sizes_ok(n, 1, Hq, d, d) || Hkv < 1 || n > 0x7fffffffLL - 256) return KDA_ERR_SHAPE;
+  if (!attn_dim_ok(int(d)) || Hq % Hkv != 0) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
 }  // namespace kda

@@ -14,10 +14,6 @@ using namespace kda;
 
 namespace {
 
-// A launch holds fewer than 2^32 threads.  In workgroups of 256, which all kernels here have but the
-// linear walks (linear_threads; see walk_grid_ok):
-constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
-
 // ---- linear attention -------------------------------------------------------------------
 
 struct LinearForm {
@@ -125,17 +121,6 @@ BwdLayout bwd_layout(int64_t B, int64_t T, int64_t H, int dk, int dv, bool bf16,
 }
 
 // ---- prompts and cache ------------------------------------------------------------------
-
-bool attn_dim_ok(int d) { return d == 64 || d == 128; }
-bool page_ok(int p) { return p == 16 || p == 32 || p == 64; }
-
-// n rows (or N sequences) of Hq heads in groups over Hkv, d wide.
-kda_status heads_ok(int64_t n, int64_t Hq, int64_t Hkv, int64_t d) {
-  // the last tile of rows ends within 32 bits
-  if (!sizes_ok(n, 1, Hq, d, d) || Hkv < 1 || n > 0x7fffffffLL - 256) return KDA_ERR_SHAPE;
-  if (!attn_dim_ok(int(d)) || Hq % Hkv != 0) return KDA_ERR_UNSUPPORTED;
-  return KDA_OK;
-}
 
 // Workspace of the prompts' backward: D, and the parts of dk and dv.
 int64_t prompt_bwd_floats(int n, int Hq, int Hkv, int d) {

@@ -112,6 +112,27 @@ struct PromptBwdArgs {
 int prompt_bwd_parts(int n, int Hq, int Hkv);
 hipError_t launch_prompt_bwd(const PromptBwdArgs& a, hipStream_t st);
 
+// ---- rotary positions -------------------------------------------------------------------
+
+struct Rotation {
+  const int* pos;    // [n, axes]; nullptr: a token's place in its sequence
+  const float* inv;  // [half]
+  const int* axis;   // [half], or nullptr: all of axis 0
+  int axes, half;
+  bool interleaved;
+};
+
+struct RopeArgs {
+  const void* x;  // [n, H, d], rows x_stride elements apart
+  void* y;        // may be x
+  int64_t x_stride, y_stride;
+  Rotation turn;
+  int n, H, d;
+  int heads;  // of a wavefront
+  bool inverse, in_bf16, out_bf16;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
+
 // ---- attention over a paged cache in 8 bits -------------------------------------------
 
 struct CacheAppendArgs {
@@ -123,6 +144,17 @@ struct CacheAppendArgs {
   bool in_bf16;
 };
 hipError_t launch_cache_append(const CacheAppendArgs& a, hipStream_t st);
+
+// Appending with the rotation of k on the way, and the rotation of the same tokens' queries (q.x
+// may be nullptr).
+struct CacheRopeArgs {
+  CacheAppendArgs c;
+  int64_t k_stride, v_stride;
+  RopeArgs q;       // q.turn is k's too
+  int N;            // sequences (c.N is 0 where there is no cache to append to)
+  bool zero_tail;   // rotated queries of rows behind the last sequence: set to zero, or left
+};
+hipError_t launch_cache_append_rope(const CacheRopeArgs& a, hipStream_t st);
 
 struct CacheStepArgs {
   const void* q;  // [N, Hq, d]

@@ -313,6 +313,16 @@ __device__ __forceinline__ void store4(T* p, f32x4 x) {
     *reinterpret_cast<f32x4*>(p) = x;
 }
 
+template <typename T>
+__device__ __forceinline__ void store8(T* p, f32x8 x) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<bf16x8*>(p) = __builtin_convertvector(x, bf16x8);
+  } else {
+    store4(p, f32x4{x[0], x[1], x[2], x[3]});
+    store4(p + 4, f32x4{x[4], x[5], x[6], x[7]});
+  }
+}
+
 // The sum and maximum of a value and the other half-wavefront's (lane ^ 32).
 __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

@@ -1,0 +1,147 @@
+// kda_serve_api.cpp -- the C ABI of what a serving step over the paged cache needs beside it
+// (declared in include/kda.h): rotary positions, appending with the rotation on the way.
+// As everywhere in the library, arguments are validated on the host first, on any
+// error nothing is launched, and launches are asynchronous on the caller's stream.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "../../include/kda.h"
+#include "kda_checks.hpp"
+#include "kda_mix_launch.hpp"
+
+using namespace kda;
+
+namespace {
+
+// n rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const void* p;
+  int64_t n, stride, width;
+};
+Range span(const Rows& r) { return {r.p, r.n > 0 ? (r.n - 1) * r.stride + r.width : 0}; }
+bool overlap(const Rows& a, const Range& b) { return kda::overlap(span(a), b); }
+// Views of one buffer whose rows alternate share a range of memory but no byte.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!kda::overlap(span(a), span(b))) return false;
+  if (a.stride != b.stride || a.n < 2 || b.n < 2) return true;
+  const int64_t off = int64_t(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  const int64_t at = ((off % a.stride) + a.stride) % a.stride;  // b's rows within a's
+  return at < a.width || at + b.width > a.stride;
+}
+
+// Rows of H heads of d: apart by at least their width, each on 16 bytes.
+kda_status stride_ok(int64_t stride, int64_t H, int64_t d, size_t e) {
+  if (stride < H * d || stride > (int64_t(1) << 28)) return KDA_ERR_SHAPE;  // (below: products of 64 bits)
+  return (stride * int64_t(e)) % 16 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+
+bool flag_ok(int x) { return x == 0 || x == 1; }
+constexpr int kMaxAxes = 8, kMaxRopeDim = 256;
+bool turn_ok(int rot, int d, int n_axes, int interleaved) {
+  return rot >= 16 && rot % 16 == 0 && rot <= d && n_axes >= 1 && n_axes <= kMaxAxes && flag_ok(interleaved);
+}
+
+// Heads that one wavefront turns: all of a row's, or fewer where that leaves the GPU short of wavefronts.
+int heads_of_wave(int64_t n, int H, int d) {
+  const int side = 64 / (d / 16), all = (H + side - 1) / side;
+  const int64_t want = n < 1 ? 1 : (8192 + n - 1) / n;
+  const int parts = int(want < all ? want : all);
+  return (all + parts - 1) / parts * side;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_rope(const void* x, kda_dtype in_dtype, int64_t x_stride, const int* positions, int n_axes,
+                    const float* inv_freq, const int* axes, int rot, int interleaved, int inverse, void* y,
+                    kda_dtype y_dtype, int64_t y_stride, int n, int H, int d, void* stream) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(y_dtype)) return KDA_ERR_DTYPE;
+  if (!sizes_ok(n, 1, H, d, d)) return KDA_ERR_SHAPE;
+  if (d % 16 != 0 || d > kMaxRopeDim || !turn_ok(rot, d, n_axes, interleaved) || !flag_ok(inverse))
+    return KDA_ERR_UNSUPPORTED;
+  const size_t ex = esize(in_dtype), ey = esize(y_dtype);
+  kda_status s = stride_ok(x_stride, H, d, ex), t = stride_ok(y_stride, H, d, ey);
+  if (s == KDA_ERR_SHAPE || t == KDA_ERR_SHAPE) return KDA_ERR_SHAPE;
+  if (n == 0) return KDA_OK;
+  const int heads = heads_of_wave(n, H, d);
+  if ((int64_t(n) * ((H + heads - 1) / heads) + 3) / 4 > kMaxGrid) return KDA_ERR_SHAPE;
+  if (!x || !positions || !inv_freq || !y) return KDA_ERR_NULL;
+  if (s != KDA_OK || t != KDA_OK || !all_aligned({x, y}, positions, 4) || !aligned(inv_freq, 4) || !aligned(axes, 4))
+    return KDA_ERR_ALIGN;
+  const Rows rx{x, n, x_stride * int64_t(ex), int64_t(H) * d * int64_t(ex)};
+  const Rows ry{y, n, y_stride * int64_t(ey), int64_t(H) * d * int64_t(ey)};
+  const bool same = x == y && in_dtype == y_dtype && x_stride == y_stride;
+  if (!same && overlap(ry, rx)) return KDA_ERR_ALIAS;
+  const Range ins[] = {{positions, int64_t(n) * n_axes * 4}, {inv_freq, int64_t(rot) * 2}, {axes, int64_t(rot) * 2}};
+  for (const Range& in : ins)
+    if (overlap(ry, in)) return KDA_ERR_ALIAS;
+  return from_hip(launch_rope(RopeArgs{x, y, x_stride, y_stride,
+                                       Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, H, d, heads,
+                                       inverse != 0, in_dtype == KDA_BF16, y_dtype == KDA_BF16},
+                              static_cast<hipStream_t>(stream)));
+}
+
+kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_stride, kda_dtype in_dtype,
+                                    const void* q, int64_t q_stride, void* q_out, kda_dtype q_out_dtype,
+                                    int64_t q_out_stride, const int* positions, int n_axes, const float* inv_freq,
+                                    const int* axes, int rot, int interleaved, const int* cu_seqlens,
+                                    const int* context_len, const int* block_table, void* k_cache, void* v_cache,
+                                    float* k_scale, float* v_scale, int n, int N, int Hq, int Hkv, int d, int page,
+                                    int n_pages, int max_pages, int zero_tail, void* stream) {
+  if (!dtype_ok(in_dtype) || (q && !dtype_ok(q_out_dtype))) return KDA_ERR_DTYPE;
+  kda_status s = heads_ok(n, q ? Hq : Hkv, Hkv, d);
+  if (s == KDA_ERR_SHAPE || N < 0 || n_pages < 0 || max_pages < 0 || page < 1) return KDA_ERR_SHAPE;
+  if (s != KDA_OK || !page_ok(page) || !turn_ok(rot, d, n_axes, interleaved) || !flag_ok(zero_tail))
+    return KDA_ERR_UNSUPPORTED;
+  const size_t e = esize(in_dtype), eo = q ? esize(q_out_dtype) : e;
+  const kda_status strides[] = {stride_ok(k_stride, Hkv, d, e), stride_ok(v_stride, Hkv, d, e),
+                                q ? stride_ok(q_stride, Hq, d, e) : KDA_OK, q ? stride_ok(q_out_stride, Hq, d, eo) : KDA_OK};
+  for (const kda_status t : strides)
+    if (t == KDA_ERR_SHAPE) return t;
+  const bool cache = N > 0 && n_pages > 0 && max_pages > 0, turns = q && (N > 0 || zero_tail);
+  if (n == 0 || (!cache && !turns)) return KDA_OK;
+  const int heads = q ? heads_of_wave(n, Hq, d) : 1;
+  const int64_t items = q ? (int64_t(n) * ((Hq + heads - 1) / heads) + 3) / 4 : 0;
+  if ((int64_t(n) / page + 2 * int64_t(N)) * Hkv + items > kMaxGrid) return KDA_ERR_SHAPE;
+  if (!inv_freq || !cu_seqlens || (N > 0 && !context_len) || (!positions && n_axes != 1) || (q && !q_out)) return KDA_ERR_NULL;
+  if (cache && (!k || !v || !block_table || !k_cache || !v_cache || !k_scale || !v_scale)) return KDA_ERR_NULL;
+  for (const kda_status t : strides)
+    if (t != KDA_OK) return t;
+  if (!all_aligned({k, v, q, q ? q_out : nullptr, k_cache, v_cache}, cu_seqlens, 4) || !aligned(context_len, 4) ||
+      !aligned(block_table, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(positions, 4) ||
+      !aligned(inv_freq, 4) || !aligned(axes, 4))
+    return KDA_ERR_ALIGN;
+  const int64_t ph = int64_t(n_pages) * Hkv, es = int64_t(e);
+  const Rows rk{k, n, k_stride * es, Hkv * int64_t(d) * es}, rv{v, n, v_stride * es, Hkv * int64_t(d) * es};
+  const Rows rq{q, n, q_stride * es, Hq * int64_t(d) * es};
+  const Rows ro{q ? q_out : nullptr, n, q_out_stride * int64_t(eo), Hq * int64_t(d) * int64_t(eo)};
+  const Range ins[] = {{cu_seqlens, (int64_t(N) + 1) * 4}, {context_len, int64_t(N) * 4},
+                       {block_table, int64_t(N) * max_pages * 4}, {positions, int64_t(n) * n_axes * 4},
+                       {inv_freq, int64_t(rot) * 2}, {axes, int64_t(rot) * 2}};
+  const Range outs[] = {{k_cache, ph * page * d}, {v_cache, ph * page * d}, {k_scale, ph * 4}, {v_scale, ph * 4}};
+  for (const Range& x : outs) {
+    for (const Range& in : ins)
+      if (kda::overlap(x, in)) return KDA_ERR_ALIAS;
+    for (const Range& y : outs)
+      if (&y != &x && kda::overlap(x, y)) return KDA_ERR_ALIAS;
+    for (const Rows& r : {rk, rv, rq, ro})
+      if (overlap(r, x)) return KDA_ERR_ALIAS;
+  }
+  for (const Range& in : ins)
+    if (overlap(ro, in)) return KDA_ERR_ALIAS;
+  const bool same = q && q == q_out && in_dtype == q_out_dtype && q_stride == q_out_stride;
+  if (overlap(ro, rk) || overlap(ro, rv) || (!same && overlap(ro, rq))) return KDA_ERR_ALIAS;
+  return from_hip(launch_cache_append_rope(
+      CacheRopeArgs{CacheAppendArgs{k, v, cu_seqlens, context_len, block_table, static_cast<uint8_t*>(k_cache),
+                                    static_cast<uint8_t*>(v_cache), k_scale, v_scale, n, cache ? N : 0, Hkv, d, page, n_pages,
+                                    max_pages, in_dtype == KDA_BF16},
+                    k_stride, v_stride,
+                    RopeArgs{turns ? q : nullptr, q_out, q_stride, q_out_stride,
+                             Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, Hq, d, heads, false,
+                             in_dtype == KDA_BF16, q_out_dtype == KDA_BF16},
+                    N, zero_tail != 0},
+      static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

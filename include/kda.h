@@ -46,6 +46,7 @@
 #define KDA_H
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -415,6 +416,28 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, k
 
 /*
  * ---------------------------------------------------------------------------
+ * Rotary positions
+ *
+ *   y_a = x_a cos t - x_b sin t,  y_b = x_b cos t + x_a sin t,  t = positions[row, axes[j]] * inv_freq[j]
+ *
+ * for the pairs j < rot / 2 of every head's channels: (a, b) = (j, j + rot/2), or (2 j, 2 j + 1) where
+ * interleaved == 1.  Channels from rot on are copied.  inverse == 1 turns backwards, which is the gradient: dx from dy.
+ *
+ *   x   [n,H,d] in_dtype, rows x_stride elements apart (a row's heads lie together); y [n,H,d] y_dtype,
+ *       rows y_stride apart (written).  y may be x itself (same type and stride), else they do not overlap.
+ *       d is a multiple of 16, at most 256; rot a multiple of 16, at most d; rows start on 16 bytes.
+ *   positions [n,n_axes] int32, n_axes 1 to 8 (time, height, width, ...); negative ones turn backwards.
+ *   inv_freq  [rot/2] fp32          axes [rot/2] int32, the axis of each pair (clamped to
+ *       0 .. n_axes - 1), or NULL: all of axis 0
+ * Angles are formed and reduced in 64 bits (exact to 2^-50 while below 2^45); sines and cosines are rounded to fp32, the
+ * rest is one fp32 multiply and one multiply-add a channel.
+ */
+kda_status kda_rope(const void* x, kda_dtype in_dtype, int64_t x_stride, const int* positions, int n_axes,
+                    const float* inv_freq, const int* axes, int rot, int interleaved, int inverse, void* y,
+                    kda_dtype y_dtype, int64_t y_stride, int n, int H, int d, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Causal softmax attention over packed prompts, grouped heads
  *
  *   o_i = sum_j P_ij v_j,  P_ij = exp(scale q_i . k_j - lse_i),
@@ -482,6 +505,29 @@ kda_status kda_kv_cache_append(const void* k, const void* v, kda_dtype in_dtype,
                                const int* context_len, const int* block_table, void* k_cache, void* v_cache,
                                float* k_scale, float* v_scale, int n, int N, int Hkv, int d, int page, int n_pages,
                                int max_pages, void* stream);
+
+/*
+ * kda_kv_cache_append_rope -- the same with rotary positions (kda_rope) applied to k on the way, and
+ * to the same tokens' queries, in one launch.
+ *
+ *   k, v [n,Hkv,d], q [n,Hq,d] in_dtype, rows k_stride, v_stride, q_stride elements apart (views of
+ *       one projection's output, say).  q may be NULL: no queries.
+ *   q_out [n,Hq,d] q_out_dtype, rows q_out_stride apart (written); may be q itself.  Rows at or past
+ *       cu_seqlens[N] are left as they were (zero_tail == 0) or set to zero (zero_tail == 1).
+ *   positions [n,n_axes] int32, or NULL (n_axes is 1 then): each token's place in its sequence,
+ *       context_len[i] plus its number among the new ones.
+ *   inv_freq, axes, rot, interleaved: as in kda_rope.
+ * Keys are turned in 64 bits and never rounded to in_dtype: the codes are those of the exactly turned
+ * keys.  v is appended as it is.  Everything else as kda_kv_cache_append; queries are turned
+ * also where a token is dropped.
+ */
+kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_stride, kda_dtype in_dtype,
+                                    const void* q, int64_t q_stride, void* q_out, kda_dtype q_out_dtype,
+                                    int64_t q_out_stride, const int* positions, int n_axes, const float* inv_freq,
+                                    const int* axes, int rot, int interleaved, const int* cu_seqlens,
+                                    const int* context_len, const int* block_table, void* k_cache, void* v_cache,
+                                    float* k_scale, float* v_scale, int n, int N, int Hq, int Hkv, int d, int page,
+                                    int n_pages, int max_pages, int zero_tail, void* stream);
 
 /*
  * kda_attn_decode_step -- attention of one query token per sequence over all
