@@ -23,6 +23,7 @@ Beside the delta rule, on the same layouts:
   kv_cache_append(k, v, cu_seqlens, ...)          -> None        paged cache in 8 bits, written in place
   kv_cache_append_rope(k, v, cu_seqlens, ...)     -> q turned    the same with rotary positions on the way
   attn_decode_step(q, k_cache, v_cache, ...)      -> (o, lse)    attention of one token over it
+  attn_chunk_fwd(q, cu_seqlens, k_cache, ...)     -> (o, lse)    attention of several new tokens a sequence over it
 """
 from __future__ import annotations
 
@@ -37,7 +38,7 @@ __all__ = ["gate", "chunk_fwd", "chunk_fwd_z", "chunk_fwd_workspace_bytes", "dec
            "linear_chunk_fwd", "linear_chunk_fwd_workspace_bytes", "linear_chunk_bwd",
            "linear_chunk_bwd_workspace_bytes", "linear_decode_step", "attn_prompt_fwd", "attn_prompt_bwd",
            "attn_prompt_bwd_workspace_bytes", "rope", "kv_cache_append", "kv_cache_append_rope", "attn_decode_step",
-           "attn_decode_step_workspace_bytes", "KDAError", "LIB_PATH", "G_MIN"]
+           "attn_decode_step_workspace_bytes", "attn_chunk_fwd", "attn_chunk_fwd_workspace_bytes", "KDAError", "LIB_PATH", "G_MIN"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 G_MIN = -5.0
@@ -118,6 +119,10 @@ def lib() -> ctypes.CDLL:
     L.kda_kv_cache_append_rope.argtypes = [P, W, P, W, I, P, W, P, I, W, P, I, P, P, I, I, P, P, P, P, P, P, P, I, I, I, I, I, I,
                                            I, I, I, P]
     L.kda_kv_cache_append_rope.restype = I
+    L.kda_attn_chunk_fwd_workspace_bytes.argtypes = [I] * 8
+    L.kda_attn_chunk_fwd_workspace_bytes.restype = Z
+    L.kda_attn_chunk_fwd.argtypes = [P, W, I, P, P, P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, I, F, I, P, Z, P]
+    L.kda_attn_chunk_fwd.restype = I
     L.kda_attn_decode_step_workspace_bytes.argtypes = [I] * 6
     L.kda_attn_decode_step_workspace_bytes.restype = Z
     L.kda_attn_decode_step.argtypes = [P, I, P, P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, F, P, Z, P]
@@ -871,4 +876,45 @@ def attn_decode_step(q, k_cache, v_cache, k_scale, v_scale, block_table, context
     _check(lib().kda_attn_decode_step(_a(q), _dtype_code(q), _a(k_cache), _a(v_cache), _a(k_scale), _a(v_scale),
                                       _a(block_table), _a(context_len), _a(o), _dtype_code(o), _a(lse), N, Hq, Hkv, d,
                                       page, pages, mp, _softmax_scale(scale, d), wp, wb, _here(q)), what)
+    return o, lse
+
+
+def attn_chunk_fwd_workspace_bytes(n: int, N: int, Hq: int, Hkv: int, d: int, page: int, max_pages: int,
+                                   dtype: torch.dtype) -> int:
+    """Device bytes ``attn_chunk_fwd`` needs as workspace (0: none) for queries of ``dtype``."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_attn_chunk_fwd_workspace_bytes(int(n), int(N), int(Hq), int(Hkv), int(d), int(page), int(max_pages),
+                                                        code))
+
+
+@_run_on_stream
+def attn_chunk_fwd(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
+                   scale: Optional[float] = None, o=None, lse=None, o_dtype=None, want_lse: bool = False,
+                   workspace=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of each sequence's new tokens over a paged cache in 8 bits that holds them already
+    (``kv_cache_append``): rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 of q [n,Hq,d] are the last of sequence i's
+    context_len[i] tokens, each sees itself and what lies before it.  q may be a view whose rows lie apart.  ``scale``
+    defaults to 1 / sqrt(d).  bf16 queries' probabilities are rounded to bf16.  Returns (o [n,Hq,d], lse [n,Hq]
+    fp32 or None); a row that sees no token gets o = 0, lse = -inf.  Rows behind the last sequence: given
+    ``o`` and ``lse`` keep what they hold there, new ones are zero there."""
+    what = "kda_attn_chunk_fwd"
+    _dims(what, ("q", q, 3), ("cu_seqlens", cu_seqlens, 1), ("context_len", context_len, 1), ("k_cache", k_cache, 4))
+    n, Hq, d = q.shape
+    Hkv = k_cache.shape[1]
+    q_row = _rows(what, "q", q, (n, Hq, d), _IO, q)
+    given = o is not None or lse is not None
+    if o is None:
+        o = (torch.zeros if given else torch.empty)((n, Hq, d), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
+    if lse is None and want_lse:
+        lse = (torch.zeros if given else torch.empty)((n, Hq), dtype=torch.float32, device=q.device)
+    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
+                                       ("o", o, (n, Hq, d), _IO), ("lse", lse, (n, Hq), _F32),
+                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32))
+    if o.get_device() != q.get_device():
+        raise KDAError(f"{what}: o is on {o.device}, q on {q.device}")
+    need = attn_chunk_fwd_workspace_bytes(n, N, Hq, Hkv, d, page, mp, q.dtype) if pages and Hkv else 0
+    wp, wb, _keep = _need(workspace, need, q.device)
+    _check(lib().kda_attn_chunk_fwd(_a(q), q_row, _dtype_code(q), _a(cu_seqlens), _a(k_cache), _a(v_cache), _a(k_scale),
+                                    _a(v_scale), _a(block_table), _a(context_len), _a(o), _dtype_code(o), _a(lse), n, N, Hq, Hkv,
+                                    d, page, pages, mp, _softmax_scale(scale, d), int(not given), wp, wb, _here(q)), what)
     return o, lse

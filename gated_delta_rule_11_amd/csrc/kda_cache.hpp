@@ -70,12 +70,12 @@ __device__ __forceinline__ int rows_in_use(const int* cu, int N, int n) {
   return e < 0 ? 0 : (e > n ? n : e);
 }
 
-// Eight codes (two words) as a fragment.  Every e4m3 value is a bf16 value.
-__device__ __forceinline__ bf16x8 codes(uint32_t a, uint32_t b) {
-  const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false),
-               q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true),
-               r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false),
-               s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+// Eight codes (two words) as a fragment, times a power of two.  Every e4m3 value is a bf16 value.
+__device__ __forceinline__ bf16x8 codes(uint32_t a, uint32_t b, float scale = 1.0f) {
+  const bf16x2 p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false),
+               q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true),
+               r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false),
+               s = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true);
   return __builtin_shufflevector(__builtin_shufflevector(p, q, 0, 1, 2, 3), __builtin_shufflevector(r, s, 0, 1, 2, 3), 0, 1,
                                  2, 3, 4, 5, 6, 7);
 }

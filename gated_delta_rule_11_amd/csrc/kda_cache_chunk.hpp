@@ -1,0 +1,820 @@
+// kda_cache_chunk.hpp -- attention of a chunk of new tokens over the paged 8-bit cache.
+//
+//   o_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = e^{scale q_r . k_j},  j <= ctx - new + (r's token)
+//
+// The new tokens of sequence i are the last of its ctx tokens, all of them in the cache.  The query heads
+// of a group read the same keys, so the rows of a tile are (token, head of the group) pairs, 128 of them.
+//
+// Tiles of more than 32 rows ("wide"): four wavefronts of 32 rows walk the keys in steps of 64.  A
+// step's codes are loaded 16 to a lane as they lie, turned into bf16 values (scale and all, exact)
+// once for all four wavefronts, and put into LDS while the step before is multiplied.  Tiles of up to 32
+// rows ("narrow": single tokens, drafted tokens) are bound by the cache's bytes: each wavefront takes
+// every fourth step for all rows, codes go straight to registers, and the four are joined at the end.
+//
+// Scores are formed transposed, S^T = K Q^T, with the rows of K dealt so that a lane ends up with runs of eight
+// consecutive tokens of one query row; P is then in place as the operand of O^T = V^T P^T, and V's pages,
+// [d][token], are that product's other operand as they lie.
+//
+// Sums and statistics are fp32.  bf16 queries: P is rounded to bf16, 2^-8 of a term, as a bf16 output is.  fp32
+// queries and their P go in as three bf16 parts that sum to them: against the codes' exact values
+// every product is exact.  The reference that exponents are taken to stays up to 2^8 above the
+// largest score seen, so that p <= 1 and most steps leave the accumulators alone.
+#pragma once
+
+#include <type_traits>
+
+#include "kda_cache.hpp"
+
+namespace kda {
+
+typedef const __attribute__((address_space(4))) int* const_ints;
+typedef const __attribute__((address_space(4))) float* const_floats;
+// A load by the scalar unit: the same address in every lane, memory that no kernel here writes.
+__device__ __forceinline__ int scalar_load(const int* p) { return *(const_ints)(uintptr_t)p; }
+__device__ __forceinline__ float scalar_load(const float* p) { return *(const_floats)(uintptr_t)p; }
+
+constexpr int kNarrowRows = 32;
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(x)), hi = __builtin_amdgcn_readfirstlane(uint32_t(uint64_t(x) >> 32));
+  return int64_t(uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Sixteen codes without those whose value (code times a power of two) is no finite fp32 number: NaN, and
+// from a scale of 2^120 on the largest; whether there were any.  By bytes: a magnitude plus 128 less the least
+// such magnitude carries into the sign's place.
+__device__ __forceinline__ bool finite_codes(u32x4& w, float scale) {
+  const int k = int(__float_as_uint(scale) >> 23) - 127;
+  int least = (135 - k) * 8;  // the magnitude of 2^(128 - k)
+  least = least > 0x7f ? 0x7f : (least < 1 ? 1 : least);
+  const uint32_t add = 0x01010101u * uint32_t(0x80 - least);
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = ((w[i] & 0x7f7f7f7fu) + add) & 0x80808080u;
+    any |= m;
+    w[i] &= ~((m << 1) - (m >> 7));
+  }
+  return any != 0;
+}
+
+// ---- the division of the work -------------------------------------------------------------
+//
+// Cost of a tile, in units of (64 keys, one head of a group): its steps, weighted, and a start.  Linear
+// in the tile's number, so that a sequence's sum is a closed form.
+constexpr int64_t kWideCost = 3, kStartCost = 8;
+
+struct ChunkSeq {
+  int first, len;  // rows of q, new tokens
+  int64_t ctx;     // tokens held
+};
+__device__ __forceinline__ ChunkSeq chunk_seq(const CacheChunkArgs& a, int i) {
+  int first = a.cu[i], last = a.cu[i + 1];
+  first = first < 0 ? 0 : first;
+  last = last > a.n ? a.n : last;
+  const int c = a.ctx[i];
+  return {first, last > first ? last - first : 0, c < 0 ? 0 : c};
+}
+__device__ __forceinline__ ChunkSeq uniform(const ChunkSeq& s) { return {uniform(s.first), uniform(s.len), uniform(s.ctx)}; }
+
+struct ChunkCost {
+  int64_t tiles, wide, last;  // wide tile t costs wide + 2 kWideCost t; the last one `last`
+  __device__ __forceinline__ ChunkCost(const CacheChunkArgs& a, const ChunkSeq& s) {
+    const int64_t G = a.Hq / a.Hkv, room = int64_t(a.max_pages) * a.page;
+    const int64_t R = int64_t(s.len) * G, ctx = s.ctx < room ? s.ctx : room;
+    const int64_t base = ctx > s.len ? ctx - s.len : 0;
+    tiles = (R + kChunkRows - 1) / kChunkRows;
+    wide = kWideCost * ((base >> 6) * G + 2) + kStartCost * G;
+    const bool narrow = R - (tiles - 1) * kChunkRows <= kNarrowRows;
+    last = tiles == 0 ? 0 : (narrow ? 1 : kWideCost) * (((ctx + 63) >> 6) * G) + kStartCost * G;
+  }
+  __device__ __forceinline__ int64_t before(int64_t t) const { return wide * t + kWideCost * t * (t - 1); }  // t < tiles
+  __device__ __forceinline__ int64_t of(int64_t t) const { return t + 1 == tiles ? last : wide + 2 * kWideCost * t; }
+  __device__ __forceinline__ int64_t all() const { return tiles == 0 ? 0 : before(tiles - 1) + last; }
+};
+
+struct ChunkItem {
+  ChunkSeq s;
+  int kvh;
+  int r0, rows;         // of the sequence's (token, head) rows
+  int64_t t0, t1, nt;   // steps of 64 keys: this workgroup's, and all
+  int64_t end;          // keys that the tile's last row sees
+  int64_t base;         // position of the sequence's first new token
+  int slot;             // part to write, or -1: the tile is whole
+};
+
+__device__ __forceinline__ ChunkItem chunk_item(const CacheChunkArgs& a, const ChunkSeq& s, int kvh, int64_t tile) {
+  ChunkItem x;
+  const int G = a.Hq / a.Hkv;
+  const int64_t R = int64_t(s.len) * G, room = int64_t(a.max_pages) * a.page, r0 = tile * kChunkRows;
+  x.s = s;
+  x.kvh = kvh;
+  x.r0 = int(r0);
+  x.rows = int(R - r0 < kChunkRows ? R - r0 : kChunkRows);
+  x.base = s.ctx - s.len;
+  const int64_t e = x.base + uniform(int((r0 + x.rows - 1) / G)) + 1;
+  x.end = e < 0 ? 0 : (e < room ? e : room);
+  x.nt = (x.end + 63) >> 6;
+  x.t0 = 0;
+  x.t1 = x.nt;
+  x.slot = -1;
+  return x;
+}
+
+// Eight fp32 values of a query row, its sign turned with the scale's.
+template <typename T>
+__device__ __forceinline__ f32x8 load_q(const T* p, bool neg) {
+  typename Op<T>::frag f = Op<T>::load(p);
+  if (neg) f = Op<T>::neg(f);
+  return Op<T>::unpack(f);
+}
+
+template <typename T, int D>
+struct ChunkShape {
+  static constexpr int NP = sizeof(T) == 2 ? 1 : 3;
+  static constexpr int kStage = 2 * 64 * D * 2;  // one step's K and V in bf16
+  static constexpr int kJoin = (4 * kNarrowRows * (D + 4) + 2 * 4 * kNarrowRows) * 4;
+  static constexpr int kQ = (D / 64) * 2 * 2 * NP * 64 * 16;  // the narrow form's parts of queries
+  static constexpr int most(int x, int y) { return x > y ? x : y; }
+  static constexpr size_t lds = most(most(2 * kStage, kJoin), kQ) + 64;
+};
+
+// One wavefront's share of a tile of rows, with what reads and writes it.
+template <typename T, typename TO, int D>
+struct ChunkWork {
+  using O = Op<bf16_t>;
+  using W = ChunkShape<T, D>;
+  static constexpr int NP = W::NP;
+  using Parts8 = Parts<bf16_t, NP, 8>;
+
+  const CacheChunkArgs& a;
+  unsigned char* smem;
+  int* bad;  // set where values that are not finite have been left out
+  int tid, lane, wave, G, P, ps;
+  float c;
+  bool neg;
+
+  __device__ __forceinline__ ChunkWork(const CacheChunkArgs& args, unsigned char* lds) : a(args), smem(lds) {
+    bad = reinterpret_cast<int*>(lds + W::lds - 64);
+    tid = threadIdx.x;
+    lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    G = a.Hq / a.Hkv;
+    P = a.page;
+    ps = page_shift(P);
+    // a negative scale is the positive one with the queries' signs turned; a scale of zero is the
+    // least normal number (a masked score, -inf, times zero would be NaN)
+    c = fmaxf(fabsf(a.scale) * kLog2e, 1.1754944e-38f);
+    neg = a.scale < 0.f;
+  }
+
+  // The page of tokens `tok` .. + 15 of a sequence, -1 where there is none below `end`.
+  __device__ __forceinline__ int page_of(const int* table, int64_t tok, int64_t end) const {
+    int p = -1;
+    if (tok < end) p = scalar_load(table + (tok >> ps));
+    return p >= 0 && p < a.pages ? p : -1;
+  }
+
+  __device__ __forceinline__ float* part(int slot) const { return a.part + int64_t(slot) * chunk_part_floats(D); }
+
+  __device__ __forceinline__ void wide(const ChunkItem& x, const int* table) {
+    using TK = Tile<bf16_t, D>;
+    using TV = Tile<bf16_t, 64>;
+    constexpr int NPC = D / 64, NK = D / 16, ND = D / 32;  // pieces of 1 KB of a wavefront; k steps; blocks of channels
+    bf16_t* const buf = reinterpret_cast<bf16_t*>(smem);
+    const int h2 = lane >> 5, l32 = lane & 31;
+    const bool alive = 32 * wave < x.rows;
+    const int mine = 32 * wave + l32 < x.rows ? 32 * wave + l32 : 0;  // (rows past the end repeat the first one)
+    const uint32_t r = uint32_t(x.r0 + mine), tok = r / uint32_t(G), hd = r % uint32_t(G);
+    const int64_t qp64 = x.base + tok;
+    const int qpos = int(qp64 < -1 ? -1 : qp64);
+    const int64_t row = int64_t(x.s.first) + tok;
+    const int head = x.kvh * G + int(hd);
+    // first positions of the wavefront's and of the tile's rows
+    const int64_t wmin = x.base + uint32_t(x.r0 + (alive ? 32 * wave : 0)) / uint32_t(G), tmin = x.base + uint32_t(x.r0) / uint32_t(G);
+
+    bf16x8 qf[NK][NP];
+#pragma unroll
+    for (int kk = 0; kk < NK; ++kk) {
+      const Parts8 p(load_q(static_cast<const T*>(a.q) + row * a.q_stride + int64_t(head) * D + 16 * kk + 8 * h2, neg));
+#pragma unroll
+      for (int i = 0; i < NP; ++i) qf[kk][i] = part_of(p, i);
+    }
+    f32x16 acc[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i) acc[i] = zero16();
+    float ref = -INFINITY, l = 0.f;
+
+    struct Ids { int p[4]; };
+    auto ids_of = [&](int64_t t) {
+      Ids z;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) z.p[g] = page_of(table, t * 64 + 16 * g, t < x.t1 ? x.end : 0);
+      return z;
+    };
+    u32x4 kr[NPC], vr[NPC];
+    float ksc[NPC], vsc[NPC];
+    auto fetch = [&](const Ids& z) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) {
+        const int at = (wave * NPC + i) * 1024, g = (at / (P * D)) << (ps - 4);  // the page's first 16 tokens
+        const int p = g == 0 ? z.p[0] : (g == 1 ? z.p[1] : (g == 2 ? z.p[2] : z.p[3]));
+        kr[i] = vr[i] = u32x4{0, 0, 0, 0};
+        ksc[i] = vsc[i] = 1.f;
+        if (p >= 0) {
+          const int64_t ph = int64_t(p) * a.Hkv + x.kvh;
+          const int64_t o = ph * P * D + (at & (P * D - 1)) + lane * 16;
+          kr[i] = *reinterpret_cast<const u32x4*>(a.kc + o);
+          vr[i] = *reinterpret_cast<const u32x4*>(a.vc + o);
+          ksc[i] = scalar_load(a.ks + ph);
+          vsc[i] = scalar_load(a.vs + ph);
+        }
+      }
+    };
+    auto put = [&](int64_t t) {
+      bf16_t* const K = buf + (t & 1) * 2 * 64 * D;
+      bf16_t* const V = K + 64 * D;
+      const int64_t k0 = t * 64;
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) {
+        const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
+        const int key = (at + lane * 16) / D, ch = (lane * 16) % D;
+        // row of the tile for a key: bits 2 and 3 change places, so that a result's registers hold runs of eight keys
+        const int kr_ = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
+        *reinterpret_cast<bf16x8*>(K + TK::off(kr_, ch)) = codes(kr[i][0], kr[i][1], ksc[i]);
+        *reinterpret_cast<bf16x8*>(K + TK::off(kr_, ch + 8)) = codes(kr[i][2], kr[i][3], ksc[i]);
+        const int d = o >> ps, vt = ((at / (P * D)) << ps) + (o & (P - 1));
+        if (k0 + 64 > x.end) {  // what lies behind the last token may be anything, NaN too
+          const int64_t left = x.end - k0 - vt;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int nb = int(left < 0 ? 0 : (left > 16 ? 16 : left)) - 4 * w;
+            vr[i][w] &= nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
+          }
+        }
+        // A masked probability is zero, but zero times a NaN is not: where a step is masked for some rows such
+        // values leave the product, and the rows that see them are set at the end.
+        if (k0 + 63 > tmin && finite_codes(vr[i], vsc[i])) *bad = 1;
+        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt)) = codes(vr[i][0], vr[i][1], vsc[i]);
+        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt + 8)) = codes(vr[i][2], vr[i][3], vsc[i]);
+      }
+    };
+
+    Ids now = ids_of(x.t0);
+    fetch(now);
+    Ids next = ids_of(x.t0 + 1);
+    if (x.t0 < x.t1) put(x.t0);
+    lds_barrier();
+    const uint32_t krow = TK::b_row8_32(lane), vrow = TV::b_row8_32(lane);
+    for (int64_t t = x.t0; t < x.t1; ++t) {
+      const Ids here = now;
+      now = next;
+      if (t + 1 < x.t1) {
+        fetch(now);
+        next = ids_of(t + 2);
+      }
+      const bf16_t* K = buf + (t & 1) * 2 * 64 * D;
+      const uint32_t kb = TK::at(K) + krow, vb = TV::at(K + 64 * D) + vrow;
+      if (alive) {
+        f32x16 s[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[j] = zero16();
+#pragma unroll
+          for (int kk = 0; kk < NK; ++kk) {
+            const bf16x8 kf = TK::row8_32(kb, j, kk);
+#pragma unroll
+            for (int i = NP - 1; i >= 0; --i) s[j] = O::mma32(kf, qf[kk][i], s[j]);
+          }
+        }
+        const bool gone = (here.p[0] | here.p[1] | here.p[2] | here.p[3]) < 0;  // a page that is none of the cache's
+        if (t * 64 + 63 > wmin || gone) {
+          const int left = qpos - int(t * 64) - 8 * h2;  // tokens of this half that the row sees: up to `left`
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              s[j][i] = 32 * j + 16 * (i >> 3) + (i & 7) <= left && here.p[2 * j + (i >> 3)] >= 0 ? s[j][i] : -INFINITY;
+        }
+        float mt = s[0][0];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[j][i]);
+        mt = c * max_halves(mt);
+        if (__any(mt > ref)) {
+          const float up = mt > ref ? mt + 8.f : ref;
+          const float al = up == ref ? 1.f : fast_exp2(ref - up);
+          l *= al;
+#pragma unroll
+          for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][e] *= al;
+          ref = up;
+        }
+        const float from = ref == -INFINITY ? 0.f : ref;  // a row that has met no key yet
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[j][i] = fast_exp2(s[j][i] * c - from);
+            l += s[j][i];
+          }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f32x8 p8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p8[e] = s[u >> 1][8 * (u & 1) + e];
+          const Parts8 pf(p8);
+#pragma unroll
+          for (int i = 0; i < ND; ++i) {
+            const bf16x8 vf = TV::row8_32(vb, i, u);
+#pragma unroll
+            for (int k = NP - 1; k >= 0; --k) acc[i] = O::mma32(vf, part_of(pf, k), acc[i]);
+          }
+        }
+      }
+      if (t + 1 < x.t1) put(t + 1);
+      lds_barrier();
+    }
+    l = sum_halves(l);
+    if (!alive || 32 * wave + l32 >= x.rows) return;
+    if (x.slot < 0) {
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      TO* op = static_cast<TO*>(a.o) + (row * a.Hq + head) * D;
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+          store4(op + 32 * i + 8 * r4 + 4 * h2,
+                 f32x4{acc[i][4 * r4] * inv, acc[i][4 * r4 + 1] * inv, acc[i][4 * r4 + 2] * inv, acc[i][4 * r4 + 3] * inv});
+      if (a.lse && h2 == 0) a.lse[row * a.Hq + head] = (ref + log2f(l)) * 0.6931471805599453f;
+    } else {
+      float* pp = part(x.slot);
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4)
+          store4(pp + mine * D + 32 * i + 8 * r4 + 4 * h2,
+                 f32x4{acc[i][4 * r4], acc[i][4 * r4 + 1], acc[i][4 * r4 + 2], acc[i][4 * r4 + 3]});
+      if (h2 == 0) {
+        pp[kChunkRows * D + 2 * mine] = ref;
+        pp[kChunkRows * D + 2 * mine + 1] = l;
+      }
+    }
+  }
+
+  // NC groups of 16 rows.
+  template <int NC>
+  __device__ __forceinline__ void narrow(const ChunkItem& x, const int* table) {
+    constexpr int NM = D / 64, ND = D / 16;
+    const int r16 = lane & 15, g4 = lane >> 4;
+    // queries of 32 rows, and the parts of fp32 ones, in LDS: in registers they would push out the next step
+    constexpr bool QL = NP == 3 || NC == 2;
+    bf16x8(*const qs)[64] = reinterpret_cast<bf16x8(*)[64]>(smem);  // [NC][NM][2][NP]
+    int qpos[NC];
+    bf16x8 qf[NC][NM][2];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const bool live = 16 * n + r16 < x.rows;
+      const uint32_t r = uint32_t(x.r0 + (live ? 16 * n + r16 : 0)), tok = r / uint32_t(G), hd = r % uint32_t(G);
+      const int64_t qp = x.base + tok;
+      qpos[n] = int(qp < -1 ? -1 : qp);
+      const T* q = static_cast<const T*>(a.q) + (int64_t(x.s.first) + tok) * a.q_stride + int64_t(x.kvh * G + int(hd)) * D;
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Parts8 p(load_q(q + 16 * (g4 + 4 * m) + 8 * e, neg));
+          if constexpr (!QL) qf[n][m][e] = part_of(p, 0);
+          else if (wave == 0)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) qs[((n * NM + m) * 2 + e) * NP + i][lane] = part_of(p, i);
+        }
+    }
+    if constexpr (QL) lds_barrier();
+    const int64_t tmin = x.base + uint32_t(x.r0) / uint32_t(G);
+
+    u32x4 kr[4][NM], vr[ND];
+    float ksc = 1.f, vsc = 1.f;
+    // the page of this lane's tokens of a step, as the rows of K (groups by r16) and as the values (by g4)
+    auto page_id = [&](int64_t tok) {
+      int p = -1;
+      if (tok < x.end) p = table[tok >> ps];
+      return p >= 0 && p < a.pages ? p : -1;
+    };
+    auto k_page = [&](int64_t t) { return page_id(t < x.t1 ? t * 64 + 16 * (r16 >> 2) : x.end); };
+    auto v_page = [&](int64_t t) { return page_id(t < x.t1 ? t * 64 + 16 * g4 : x.end); };
+    auto load_k = [&](int p) {
+      const int64_t ph = int64_t(p < 0 ? 0 : p) * a.Hkv + x.kvh;
+      const uint8_t* kp = a.kc + (ph * P + ((16 * (r16 >> 2)) & (P - 1)) + (r16 & 3)) * D + 16 * g4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          kr[q][m] = p >= 0 ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(kp + 4 * q * D + 64 * m)) : u32x4{0, 0, 0, 0};
+      ksc = p >= 0 ? a.ks[ph] : 1.f;
+    };
+    auto load_v = [&](int p) {
+      const int64_t ph = int64_t(p < 0 ? 0 : p) * a.Hkv + x.kvh;
+      const uint8_t* vp = a.vc + (ph * D + r16) * P + ((16 * g4) & (P - 1));
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        vr[d] = p >= 0 ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(vp + 16 * d * P)) : u32x4{0, 0, 0, 0};
+      vsc = p >= 0 ? a.vs[ph] : 1.f;
+    };
+
+    f32x4 acc[NC][ND];
+    float ref[NC], l[NC];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      ref[n] = -INFINITY;
+      l[n] = 0.f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0, 0, 0, 0};
+    }
+    int64_t t = x.t0 + wave;
+    int pv = v_page(t), pk1 = k_page(t + 4), pv1 = v_page(t + 4);
+    if (t < x.t1) {
+      load_k(k_page(t));
+      load_v(pv);
+    }
+    for (; t < x.t1; t += 4) {
+      f32x4 s[NC][4];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[n][q] = f32x4{0, 0, 0, 0};
+      int ql = lane;
+      if constexpr (QL) asm volatile("" : "+v"(ql));  // read again for each step
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          bf16x8 kf[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) kf[q] = codes(kr[q][m][2 * e], kr[q][m][2 * e + 1], ksc);
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int i = NP - 1; i >= 0; --i) {
+              bf16x8 qp;
+              if constexpr (!QL) qp = qf[n][m][e];
+              else qp = qs[((n * NM + m) * 2 + e) * NP + i][ql];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s[n][q] = O::mma16(kf[q], qp, s[n][q]);
+            }
+        }
+      const int64_t k0 = t * 64 + 16 * g4;  // this lane's tokens
+      const bool here = pv >= 0;
+      load_k(pk1);
+      pk1 = k_page(t + 8);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        const int64_t seen = qpos[n] + 1 - k0;
+        const int left = here ? int(seen < 0 ? 0 : (seen > 16 ? 16 : seen)) : 0;
+        float mt = -INFINITY;
+        if (__any(left < 16)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][q][i] = 4 * q + i < left ? s[n][q][i] : -INFINITY;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mt = fmaxf(mt, s[n][q][i]);
+        mt = c * max_groups(mt);
+        if (__any(mt > ref[n])) {
+          const float up = mt > ref[n] ? mt + 8.f : ref[n];
+          const float al = up == ref[n] ? 1.f : fast_exp2(ref[n] - up);
+          l[n] *= al;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) acc[n][d] *= al;
+          ref[n] = up;
+        }
+        const float from = ref[n] == -INFINITY ? 0.f : ref[n];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[n][q][i] = fast_exp2(s[n][q][i] * c - from);
+            l[n] += s[n][q][i];
+          }
+      }
+      if (t * 64 + 64 > x.end) {  // what lies behind the last token may be anything, NaN too
+        const int64_t left = x.end - k0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int nb = int(left < 0 ? 0 : (left > 16 ? 16 : left)) - 4 * w;
+          const uint32_t mask = nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) vr[d][w] &= mask;
+        }
+      }
+      if (t * 64 + 63 > tmin) {  // (as in the wide form)
+        bool any = false;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) any |= finite_codes(vr[d], vsc);
+        if (any) *bad = 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int d0 = 0; d0 < ND; d0 += 4) {
+          bf16x8 vf[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) vf[d] = codes(vr[d0 + d][2 * u], vr[d0 + d][2 * u + 1], vsc);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            const Parts8 pf(__builtin_shufflevector(s[n][2 * u], s[n][2 * u + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int i = NP - 1; i >= 0; --i)
+#pragma unroll
+              for (int d = 0; d < 4; ++d) acc[n][d0 + d] = O::mma16(vf[d], part_of(pf, i), acc[n][d0 + d]);
+          }
+        }
+      }
+      pv = pv1;
+      load_v(pv1);
+      pv1 = v_page(t + 8);
+    }
+    float* const jo = reinterpret_cast<float*>(smem);  // [4][16 NC][D + 4]
+    float* const jm = jo + 4 * 16 * NC * (D + 4);      // [4][16 NC] references, then sums
+    if constexpr (QL) lds_barrier();                   // the queries have been read
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const float ls = sum_groups(l[n]);
+      if (g4 == 0) {
+        jm[wave * 16 * NC + 16 * n + r16] = ref[n];
+        jm[(4 + wave) * 16 * NC + 16 * n + r16] = ls;
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(jo + (wave * 16 * NC + 16 * n + r16) * (D + 4) + 16 * d + 4 * g4) = acc[n][d];
+    }
+    lds_barrier();
+    for (int e = tid; e < x.rows * (D / 4); e += 256) {
+      const int rr = e / (D / 4), c0 = 4 * (e % (D / 4));
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, jm[w * 16 * NC + rr]);
+      const float from = m == -INFINITY ? 0.f : m;
+      float ls = 0.f;
+      f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = fast_exp2(jm[w * 16 * NC + rr] - from);
+        ls += f * jm[(4 + w) * 16 * NC + rr];
+        y += *reinterpret_cast<const f32x4*>(jo + (w * 16 * NC + rr) * (D + 4) + c0) * f;
+      }
+      if (x.slot < 0) {
+        const uint32_t r = uint32_t(x.r0 + rr);
+        const int64_t row = (int64_t(x.s.first) + r / uint32_t(G)) * a.Hq + x.kvh * G + int(r % uint32_t(G));
+        store4(static_cast<TO*>(a.o) + row * D + c0, y * (ls == 0.f ? 0.f : 1.0f / ls));
+        if (a.lse && c0 == 0) a.lse[row] = (m + log2f(ls)) * 0.6931471805599453f;
+      } else {
+        float* pp = part(x.slot);
+        store4(pp + rr * D + c0, y);
+        if (c0 == 0) {
+          pp[kChunkRows * D + 2 * rr] = m;
+          pp[kChunkRows * D + 2 * rr + 1] = ls;
+        }
+      }
+    }
+  }
+
+  // Writes the values that are not finite into the outputs (parts) of the rows that see them: no finite
+  // sum, nor a factor, changes them.
+  __device__ __forceinline__ void set_bad(const ChunkItem& x, const int* table) {
+    const int64_t tmin = x.base + uint32_t(x.r0) / uint32_t(G);
+    int64_t k0 = tmin < 0 ? 0 : (tmin + 1) & ~int64_t(63);
+    k0 = k0 > x.t0 * 64 ? k0 : x.t0 * 64;
+    const int64_t k1 = x.end < x.t1 * 64 ? x.end : x.t1 * 64;
+    for (int e = tid; e < x.rows * D; e += 256) {
+      const int rr = e / D, d = e % D;
+      const uint32_t r = uint32_t(x.r0 + rr), tok = r / uint32_t(G);
+      float y = 0.f;
+#pragma unroll 1
+      for (int64_t key = k0; key < k1 && key <= x.base + tok; ++key) {
+        const int p = table[key >> ps];
+        if (p < 0 || p >= a.pages) continue;
+        const int64_t ph = int64_t(p) * a.Hkv + x.kvh;
+        const float v = float(codes(a.vc[(ph * D + d) * P + (key & (P - 1))], 0, a.vs[ph])[0]);
+        if (!(fabsf(v) < INFINITY)) y += v;
+      }
+      if (y == 0.f) continue;
+      if (x.slot < 0)
+        io<TO>::store(static_cast<TO*>(a.o), ((int64_t(x.s.first) + tok) * a.Hq + x.kvh * G + int(r % uint32_t(G))) * D + d, y);
+      else
+        part(x.slot)[e] = y;
+    }
+  }
+
+  __device__ __forceinline__ void run(const ChunkItem& x, int seq) {
+    const int* table = a.table + int64_t(seq) * a.max_pages;
+    // what follows from the lane's number is formed again for each item: held over the loop, all three forms'
+    // would be in registers at once
+    asm volatile("" : "+v"(tid), "+v"(lane));
+    lds_barrier();  // the item before is out of the LDS
+    if (tid == 0) *bad = 0;
+    lds_barrier();
+    if (x.rows > kNarrowRows) wide(x, table);
+    else if (x.rows > 16) narrow<2>(x, table);
+    else narrow<1>(x, table);
+    lds_barrier();
+    if (*bad) {
+      __threadfence();  // behind the stores of the sums
+      __syncthreads();
+      set_bad(x, table);
+    }
+  }
+};
+
+// What a part is, for the kernel that joins them.
+struct ChunkPart {
+  int kind;  // 0: none; 1: the tile goes on in the next workgroup; 2: its end
+  int first, kvh, r0, rows, pad[3];
+};
+
+template <typename T, typename TO, int D>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kernel(const CacheChunkArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (a.zero_tail) {
+    const int64_t used = a.N > 0 ? rows_in_use(a.cu, a.N, a.n) : 0;
+    for (int64_t row = used + blockIdx.x; row < a.n; row += gridDim.x) {
+      for (int e = tid; e < a.Hq * (D / 4); e += 256)
+        store4(static_cast<TO*>(a.o) + row * a.Hq * D + 4 * int64_t(e), f32x4{0, 0, 0, 0});
+      if (a.lse)
+        for (int e = tid; e < a.Hq; e += 256) a.lse[row * a.Hq + e] = 0.f;
+    }
+  }
+  if (a.N == 0) return;
+  ChunkWork<T, TO, D> work(a, smem);
+  const int G = a.Hq / a.Hkv;
+
+  const bool shared = a.groups > 0;
+  int seq = 0, kvh = 0, w = 0;
+  int64_t x = 0, x1 = 1, rest = 0, tile = 0;
+  ChunkPart* const parts = reinterpret_cast<ChunkPart*>(a.part + int64_t(a.groups) * 2 * chunk_part_floats(D));
+  if (!shared) {
+    // Sequence i's tiles sit at slots cu[i] G / 128 + i onwards, which leaves each at least as many as it has.
+    const int slots = int(gridDim.x / a.Hkv), slot = slots - 1 - int(blockIdx.x / a.Hkv);  // long rows first
+    kvh = int(blockIdx.x % a.Hkv);
+    int lo = 0, up = a.N;
+    auto start = [&](int64_t i) {
+      const int64_t c = a.cu[i];
+      return (c < 0 ? 0 : c) * G / kChunkRows + i;
+    };
+    while (up - lo > 1) {
+      const int step = (up - lo + 63) / 64;
+      const int64_t mid = lo + int64_t(step) * (lane + 1);
+      lo += step * __popcll(__ballot(mid < up && start(mid) <= slot));
+      up = lo + step < up ? lo + step : up;
+    }
+    seq = uniform(lo);
+    tile = uniform(slot - start(lo));
+  } else {
+    // Every workgroup takes an equal piece of the line of all tiles' costs, key heads outermost.
+    int64_t* const sums = reinterpret_cast<int64_t*>(smem);  // [256] costs of the threads' sequences before each, [4]
+    const int per = (a.N + 255) / 256;
+    int64_t mine = 0;
+    for (int i = tid * per; i < (tid + 1) * per && i < a.N; ++i) mine += ChunkCost(a, chunk_seq(a, i)).all();
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t y = __shfl_up((long long)upto, d);
+      upto += lane >= d ? y : 0;
+    }
+    if (lane == 63) sums[256 + (tid >> 6)] = upto;
+    __syncthreads();
+    int64_t head = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < (tid >> 6)) upto += sums[256 + i];
+      head += sums[256 + i];
+    }
+    head = uniform(head);
+    sums[tid] = upto - mine;
+    __syncthreads();
+    const int64_t all = head * a.Hkv, least = 2 * kStartCost * G;
+    int64_t groups = all / least;
+    groups = groups < 1 ? 1 : (groups < a.groups ? groups : a.groups);
+    w = xcd_order(blockIdx.x, a.groups);
+    if (tid == 0) parts[2 * w].kind = parts[2 * w + 1].kind = 0;
+    if (w >= groups || all == 0) return;
+    const int64_t each = all / groups, more = all % groups;
+    x = uniform(each * w + (w < more ? w : more));
+    x1 = uniform(x + each + (w < more ? 1 : 0));
+    kvh = uniform(int(x / head));
+    rest = uniform(x % head);  // to go within this key head's line
+    int lo = 0, up = 256;
+    while (up - lo > 1) {
+      const int mid = (lo + up) / 2;
+      if (sums[mid] <= rest) lo = mid;
+      else up = mid;
+    }
+    rest = uniform(rest - sums[lo]);
+    seq = uniform(lo * per);
+  }
+  while (x < x1) {
+    const ChunkSeq s = uniform(chunk_seq(a, seq));
+    const ChunkCost cost(a, s);
+    int64_t from = 0, to = 1, full = 1;
+    if (shared) {
+      if (rest >= cost.all()) {  // an earlier workgroup's, or empty
+        rest -= cost.all();
+        if (++seq == a.N) {
+          seq = 0;
+          ++kvh;
+        }
+        continue;
+      }
+      int64_t up = cost.tiles;
+      tile = 0;
+      while (up - tile > 1) {
+        const int64_t mid = (tile + up) / 2;
+        if (cost.before(mid) <= rest) tile = mid;
+        else up = mid;
+      }
+      full = cost.of(tile);
+      from = rest - cost.before(tile);
+      to = from + (x1 - x) < full ? from + (x1 - x) : full;
+    } else if (tile < 0 || tile >= cost.tiles) {
+      return;
+    }
+    ChunkItem it = chunk_item(a, s, kvh, tile);
+    if (shared) {
+      it.t0 = uniform(from * it.nt / full);
+      it.t1 = uniform(to * it.nt / full);
+      if (from > 0 || to < full) {
+        it.slot = 2 * w + (from > 0 ? 0 : 1);
+        if (tid == 0) parts[it.slot] = ChunkPart{to < full ? 1 : 2, s.first, kvh, it.r0, it.rows, {0, 0, 0}};
+      }
+    }
+    work.run(it, seq);
+    x = uniform(x + (to - from));
+    rest = uniform(rest + (to - from));
+  }
+}
+
+// Joins the parts of the tile that begins in workgroup blockIdx.x and ends in a later one, 16 rows of it.
+template <typename TO, int D>
+__global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkArgs a) {
+  const ChunkPart* const parts = reinterpret_cast<const ChunkPart*>(a.part + int64_t(a.groups) * 2 * chunk_part_floats(D));
+  const int w = blockIdx.x, G = a.Hq / a.Hkv;
+  const ChunkPart p = parts[2 * w + 1];
+  const int r = 16 * blockIdx.y + threadIdx.x / 16, c0 = (D / 16) * (threadIdx.x % 16);
+  if (p.kind != 1 || r >= p.rows) return;
+  int last = w + 1;
+  while (last + 1 < a.groups && parts[2 * last].kind == 1) ++last;
+  float m = -INFINITY;
+  auto of = [&](int i) { return a.part + int64_t(i == w ? 2 * w + 1 : 2 * i) * chunk_part_floats(D); };
+  for (int i = w; i <= last; ++i) m = fmaxf(m, of(i)[kChunkRows * D + 2 * r]);
+  const float from = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  f32x4 y[D / 64];
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) y[j] = f32x4{0, 0, 0, 0};
+  for (int i = w; i <= last; ++i) {
+    const float* pp = of(i);
+    const float f = fast_exp2(pp[kChunkRows * D + 2 * r] - from);
+    l += f * pp[kChunkRows * D + 2 * r + 1];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) y[j] += *reinterpret_cast<const f32x4*>(pp + r * D + c0 + 4 * j) * f;
+  }
+  const uint32_t rr = uint32_t(p.r0 + r);
+  const int64_t row = (int64_t(p.first) + rr / uint32_t(G)) * a.Hq + p.kvh * G + int(rr % uint32_t(G));
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) store4(static_cast<TO*>(a.o) + row * D + c0 + 4 * j, y[j] * inv);
+  if (a.lse && c0 == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <typename T, typename TO, int D>
+hipError_t launch_chunk(const CacheChunkArgs& a, hipStream_t st) {
+  auto kern = cache_chunk_kernel<T, TO, D>;
+  constexpr size_t lds = ChunkShape<T, D>::lds;
+  static_assert(lds <= 80 * 1024, "two workgroups of a compute unit");
+  static std::atomic<uint64_t> done{0};
+  if constexpr (lds > 65536) {
+    const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), int(lds), done);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t grid = a.groups > 0 ? a.groups : cache_chunk_slots(a.n, a.N, a.Hq, a.Hkv) * a.Hkv;
+  kern<<<dim3(uint32_t(grid < 1 ? 1 : grid)), 256, lds, st>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.groups == 0) return e;
+  cache_chunk_join_kernel<TO, D><<<dim3(uint32_t(a.groups), kChunkRows / 16), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_chunk_any(const CacheChunkArgs& a, hipStream_t st) {
+  if (a.d == 64) return a.out_bf16 ? launch_chunk<T, bf16_t, 64>(a, st) : launch_chunk<T, float, 64>(a, st);
+  return a.out_bf16 ? launch_chunk<T, bf16_t, 128>(a, st) : launch_chunk<T, float, 128>(a, st);
+}
+
+}  // namespace kda

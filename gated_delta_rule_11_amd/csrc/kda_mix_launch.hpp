@@ -171,4 +171,30 @@ struct CacheStepArgs {
 int cache_step_splits(int N, int Hq, int Hkv, int page, int max_pages);
 hipError_t launch_cache_step(const CacheStepArgs& a, hipStream_t st);
 
+// Attention of a chunk of new tokens over the cache (kda_cache_chunk.hpp).
+struct CacheChunkArgs {
+  const void* q;  // [n, Hq, d], rows q_stride elements apart
+  int64_t q_stride;
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  const int *cu, *table, *ctx;
+  void* o;      // [n, Hq, d]
+  float* lse;   // [n, Hq] or nullptr
+  float* part;  // chunk_part_floats() when groups > 0
+  int n, N, Hq, Hkv, d, page, pages, max_pages;
+  int groups;  // workgroups that share the work evenly; 0: one for each tile of rows
+  float scale;
+  bool in_bf16, out_bf16, zero_tail;
+};
+// Rows of a tile: (new token, query head of the group) pairs, heads fastest.
+constexpr int kChunkRows = 128;
+int cache_chunk_groups(int n, int N, int Hq, int Hkv, int page, int max_pages, bool bf16);
+int64_t cache_chunk_slots(int n, int N, int Hq, int Hkv);
+// Two parts of tiles for each workgroup, [rows][d] and [rows][2], and what each part is (8 words).
+__host__ __device__ constexpr int64_t chunk_part_floats(int d) { return kChunkRows * (int64_t(d) + 2); }
+inline int64_t cache_chunk_workspace_floats(int groups, int d) { return int64_t(groups) * 2 * (chunk_part_floats(d) + 8); }
+hipError_t launch_cache_chunk(const CacheChunkArgs& a, hipStream_t st);
+hipError_t launch_cache_chunk_bf16(const CacheChunkArgs& a, hipStream_t st);
+hipError_t launch_cache_chunk_f32(const CacheChunkArgs& a, hipStream_t st);
+
 }  // namespace kda

@@ -1,5 +1,6 @@
 // kda_serve_api.cpp -- the C ABI of what a serving step over the paged cache needs beside it
-// (declared in include/kda.h): rotary positions, appending with the rotation on the way.
+// (declared in include/kda.h): rotary positions, appending with the rotation on the way, attention
+// of a chunk of new tokens.
 // As everywhere in the library, arguments are validated on the host first, on any
 // error nothing is launched, and launches are asynchronous on the caller's stream.
 #include <hip/hip_runtime.h>
@@ -48,6 +49,9 @@ int heads_of_wave(int64_t n, int H, int d) {
   const int parts = int(want < all ? want : all);
   return (all + parts - 1) / parts * side;
 }
+
+// Query heads that share a key head: the costs by which workgroups divide the work stay in 64 bits.
+constexpr int kMaxGroup = 1024;
 
 }  // namespace
 
@@ -141,6 +145,56 @@ kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void*
                              Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, Hq, d, heads, false,
                              in_dtype == KDA_BF16, q_out_dtype == KDA_BF16},
                     N, zero_tail != 0},
+      static_cast<hipStream_t>(stream)));
+}
+
+size_t kda_attn_chunk_fwd_workspace_bytes(int n, int N, int Hq, int Hkv, int d, int page, int max_pages,
+                                          kda_dtype in_dtype) {
+  if (!dtype_ok(in_dtype) || heads_ok(n, Hq, Hkv, d) != KDA_OK || Hq / Hkv > kMaxGroup || !page_ok(page) || N < 1 || n < 1 ||
+      max_pages < 1)
+    return 0;
+  return size_t(cache_chunk_workspace_floats(cache_chunk_groups(n, N, Hq, Hkv, page, max_pages, in_dtype == KDA_BF16), d)) * 4;
+}
+
+kda_status kda_attn_chunk_fwd(const void* q, int64_t q_stride, kda_dtype in_dtype, const int* cu_seqlens,
+                              const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int* block_table, const int* context_len, void* o, kda_dtype o_dtype, float* lse, int n,
+                              int N, int Hq, int Hkv, int d, int page, int n_pages, int max_pages, float scale, int zero_tail,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(o_dtype)) return KDA_ERR_DTYPE;
+  const kda_status s = heads_ok(n, Hq, Hkv, d);
+  if (s == KDA_ERR_SHAPE || N < 0 || n_pages < 0 || max_pages < 0 || page < 1) return KDA_ERR_SHAPE;
+  if (s != KDA_OK || !page_ok(page) || Hq / Hkv > kMaxGroup || !isfinite(scale) || !flag_ok(zero_tail))
+    return KDA_ERR_UNSUPPORTED;
+  const kda_status st = stride_ok(q_stride, Hq, d, esize(in_dtype));
+  if (st == KDA_ERR_SHAPE) return st;
+  if (n == 0 || (N == 0 && !zero_tail)) return KDA_OK;
+  if (cache_chunk_slots(n, N, Hq, Hkv) * Hkv > kMaxGrid) return KDA_ERR_SHAPE;
+  const int used = n_pages > 0 ? max_pages : 0;  // a cache of no pages leaves every token out
+  const int groups = N > 0 && used > 0 ? cache_chunk_groups(n, N, Hq, Hkv, page, used, in_dtype == KDA_BF16) : 0;
+  const size_t need = size_t(cache_chunk_workspace_floats(groups, d)) * 4;
+  if (!q || !o || (N > 0 && (!cu_seqlens || !context_len)) || (need > 0 && !workspace)) return KDA_ERR_NULL;
+  if (N > 0 && used > 0 && (!k_cache || !v_cache || !k_scale || !v_scale || !block_table)) return KDA_ERR_NULL;
+  if (st != KDA_OK || !all_aligned({q, o, k_cache, v_cache, need > 0 ? workspace : nullptr}, block_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(context_len, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(lse, 4))
+    return KDA_ERR_ALIGN;
+  if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
+  const int64_t ph = int64_t(n_pages) * Hkv, nq = int64_t(n) * Hq, e = int64_t(esize(in_dtype));
+  const Rows rq{q, n, q_stride * e, int64_t(Hq) * d * e};
+  const Range ins[] = {span(rq), {k_cache, ph * page * d}, {v_cache, ph * page * d}, {k_scale, ph * 4}, {v_scale, ph * 4},
+                       {block_table, int64_t(N) * max_pages * 4}, {context_len, int64_t(N) * 4},
+                       {cu_seqlens, (int64_t(N) + 1) * 4}};
+  const Range outs[] = {{o, nq * d * int64_t(esize(o_dtype))}, {lse, nq * 4}, {need > 0 ? workspace : nullptr, int64_t(need)}};
+  for (const Range& x : outs) {
+    for (const Range& in : ins)
+      if (kda::overlap(x, in)) return KDA_ERR_ALIAS;
+    for (const Range& y : outs)
+      if (&y != &x && kda::overlap(x, y)) return KDA_ERR_ALIAS;
+  }
+  return from_hip(launch_cache_chunk(
+      CacheChunkArgs{q, q_stride, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale, v_scale,
+                     cu_seqlens, block_table, context_len, o, lse, static_cast<float*>(workspace), n, N, Hq, Hkv, d, page,
+                     n_pages, used, groups, scale, in_dtype == KDA_BF16, o_dtype == KDA_BF16, zero_tail != 0},
       static_cast<hipStream_t>(stream)));
 }
 

@@ -549,6 +549,29 @@ kda_status kda_attn_decode_step(const void* q, kda_dtype in_dtype, const void* k
                                 int d, int page, int n_pages, int max_pages, float scale, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/*
+ * kda_attn_chunk_fwd -- attention of a chunk of new tokens over the cache (append them first): pieces of
+ * a prompt, drafted tokens, single tokens, and any mixture of them in one call.
+ *   q [n,Hq,d] in_dtype, rows q_stride elements apart: rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 are sequence
+ *       i's new tokens, the last of its context_len[i] tokens (here the new ones are counted).  With new tokens,
+ *       row r of a sequence sees its tokens 0 .. context_len[i] - new + r; a row that sees none has o = 0, lse = -inf.
+ *   o [n,Hq,d] o_dtype, lse [n,Hq] fp32 or NULL (written).  Rows at or past cu_seqlens[N] are left as they were
+ *       (zero_tail == 0) or set to zero (zero_tail == 1).
+ * At most 1024 query heads share a key head.  Roundings, missing pages and what lies behind the last token: as in
+ * kda_attn_decode_step, whose results single tokens get (the sums in another order).  fp32 queries: every product is exact.
+ * A NaN or infinity among the values reaches only the rows that see it.
+ * The work, the keys of all rows, is divided evenly over the GPU on the device, whatever the lengths: no list of
+ * them is needed on the host.  Every sum has a fixed order: the same bits every time.
+ *   workspace  kda_attn_chunk_fwd_workspace_bytes bytes, 16-byte aligned (NULL when that is 0); contents do not matter
+ */
+size_t kda_attn_chunk_fwd_workspace_bytes(int n, int N, int Hq, int Hkv, int d, int page, int max_pages,
+                                          kda_dtype in_dtype);
+kda_status kda_attn_chunk_fwd(const void* q, int64_t q_stride, kda_dtype in_dtype, const int* cu_seqlens,
+                              const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int* block_table, const int* context_len, void* o, kda_dtype o_dtype, float* lse, int n,
+                              int N, int Hq, int Hkv, int d, int page, int n_pages, int max_pages, float scale, int zero_tail,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,22 +42,21 @@ def chunk(cache, q, cu, ctx, table, scale):
     o = torch.full((n, Hq, d), math.nan, dtype=torch.float64)
     lse, mag = torch.full((n, Hq), math.nan, dtype=torch.float64), torch.zeros(n, Hq, d, dtype=torch.float64)
     for i in range(len(ctx)):
-        new = cu[i + 1] - cu[i]
+        rows, new = slice(cu[i], cu[i + 1]), cu[i + 1] - cu[i]
         room = min(max(ctx[i], 0), len(table[i]) * P)
         tok = np.array([p for p in range(room) if 0 <= table[i][p // P] < pages], dtype=np.int64)
         pg = np.array([table[i][p // P] for p in tok], dtype=np.int64)
+        seen = torch.from_numpy(tok)[None] <= torch.arange(max(ctx[i], 0) - new, max(ctx[i], 0))[:, None]
+        some = seen.any(1)
         for h in range(Hq):
             hk = h // (Hq // Hkv)
             k = torch.from_numpy(cache.side["k"][pg, hk, tok % P] * cache.scale["k"][pg, hk][:, None]).reshape(-1, d)
             v = torch.from_numpy(cache.side["v"][pg, hk, tok % P] * cache.scale["v"][pg, hk][:, None]).reshape(-1, d)
-            for r in range(new):
-                seen = int(np.searchsorted(tok, ctx[i] - new + r, side="right"))
-                row = cu[i] + r
-                if seen == 0:
-                    o[row, h], lse[row, h] = 0.0, -math.inf
-                    continue
-                s = k[:seen] @ q[row, h] * scale
-                lse[row, h] = torch.logsumexp(s, 0)
-                p = torch.softmax(s, 0)
-                o[row, h], mag[row, h] = p @ v[:seen], p @ v[:seen].abs()
+            w = torch.where(seen, q[rows, h] @ k.T * scale, -math.inf)
+            lse[rows, h] = torch.logsumexp(w, -1) if tok.size else -math.inf
+            p = torch.where(some[:, None], torch.softmax(w, -1), 0.0)
+            p = torch.where(seen, p, 0.0)
+            # a term that a row does not see is no term, whatever the value
+            o[rows, h] = p @ v if bool(v.isfinite().all()) else torch.where(seen[..., None], p[..., None] * v, 0.0).sum(1)
+            mag[rows, h] = p @ v.nan_to_num(0, 0, 0).abs()
     return o, lse, mag
