@@ -64,11 +64,10 @@ __device__ __forceinline__ bool finite_codes(u32x4& w, float scale) {
 //
 // Cost of a tile, in units of (64 keys, one head of a group): its steps, weighted, and a start.  Linear
 // in the tile's number, so that a sequence's sum is a closed form.
-constexpr int64_t kWideCost = 3, kStartCost = 8;
+constexpr int64_t kNarrowCost = 2, kWideCost = 4, kStartCost = 20, kLeastCost = 16;
 
 struct ChunkSeq {
-  int first, len;  // rows of q, new tokens
-  int64_t ctx;     // tokens held
+  int first, len, ctx;  // rows of q, new tokens, tokens held
 };
 __device__ __forceinline__ ChunkSeq chunk_seq(const CacheChunkArgs& a, int i) {
   int first = a.cu[i], last = a.cu[i + 1];
@@ -83,40 +82,57 @@ struct ChunkCost {
   int64_t tiles, wide, last;  // wide tile t costs wide + 2 kWideCost t; the last one `last`
   __device__ __forceinline__ ChunkCost(const CacheChunkArgs& a, const ChunkSeq& s) {
     const int64_t G = a.Hq / a.Hkv, room = int64_t(a.max_pages) * a.page;
-    const int64_t R = int64_t(s.len) * G, ctx = s.ctx < room ? s.ctx : room;
+    const int64_t R = int64_t(s.len) * G, ctx = s.ctx < room ? int64_t(s.ctx) : room;
     const int64_t base = ctx > s.len ? ctx - s.len : 0;
     tiles = (R + kChunkRows - 1) / kChunkRows;
     wide = kWideCost * ((base >> 6) * G + 2) + kStartCost * G;
     const bool narrow = R - (tiles - 1) * kChunkRows <= kNarrowRows;
-    last = tiles == 0 ? 0 : (narrow ? 1 : kWideCost) * (((ctx + 63) >> 6) * G) + kStartCost * G;
+    last = tiles == 0 ? 0 : (narrow ? kNarrowCost : kWideCost) * (((ctx + 63) >> 6) * G) + kStartCost * G;
   }
   __device__ __forceinline__ int64_t before(int64_t t) const { return wide * t + kWideCost * t * (t - 1); }  // t < tiles
   __device__ __forceinline__ int64_t of(int64_t t) const { return t + 1 == tiles ? last : wide + 2 * kWideCost * t; }
   __device__ __forceinline__ int64_t all() const { return tiles == 0 ? 0 : before(tiles - 1) + last; }
+  // the tile at x of the sequence's line: the root of before(t) = x, and the tiles beside it
+  __device__ __forceinline__ int64_t at(int64_t x) const {
+    const double b = double(wide - kWideCost);
+    int64_t t = int64_t((__builtin_sqrt(b * b + 4.0 * kWideCost * double(x)) - b) / (2.0 * kWideCost));
+    t = t < tiles ? t : tiles - 1;
+    while (t > 0 && before(t) > x) --t;
+    while (t + 1 < tiles && before(t + 1) <= x) ++t;
+    return t;
+  }
 };
+
+// x / y, y > 0: from 64-bit floating point, put right by at most a few steps.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  int64_t q = int64_t(double(x) / double(y));
+  while (q * y > x) --q;
+  while ((q + 1) * y <= x) ++q;
+  return q;
+}
 
 struct ChunkItem {
   ChunkSeq s;
   int kvh;
-  int r0, rows;         // of the sequence's (token, head) rows
-  int64_t t0, t1, nt;   // steps of 64 keys: this workgroup's, and all
-  int64_t end;          // keys that the tile's last row sees
-  int64_t base;         // position of the sequence's first new token
-  int slot;             // part to write, or -1: the tile is whole
+  int r0, rows;    // of the sequence's (token, head) rows
+  int t0, t1, nt;  // steps of 64 keys: this workgroup's, and all
+  int end;         // keys that the tile's last row sees
+  int base;        // position of the sequence's first new token
+  int slot;        // part to write, or -1: the tile is whole
 };
 
-__device__ __forceinline__ ChunkItem chunk_item(const CacheChunkArgs& a, const ChunkSeq& s, int kvh, int64_t tile) {
+__device__ __forceinline__ ChunkItem chunk_item(const CacheChunkArgs& a, const ChunkSeq& s, int kvh, int tile) {
   ChunkItem x;
   const int G = a.Hq / a.Hkv;
-  const int64_t R = int64_t(s.len) * G, room = int64_t(a.max_pages) * a.page, r0 = tile * kChunkRows;
+  const int64_t R = int64_t(s.len) * G, room = int64_t(a.max_pages) * a.page, r0 = int64_t(tile) * kChunkRows;
   x.s = s;
   x.kvh = kvh;
   x.r0 = int(r0);
   x.rows = int(R - r0 < kChunkRows ? R - r0 : kChunkRows);
   x.base = s.ctx - s.len;
-  const int64_t e = x.base + uniform(int((r0 + x.rows - 1) / G)) + 1;
-  x.end = e < 0 ? 0 : (e < room ? e : room);
-  x.nt = (x.end + 63) >> 6;
+  const int64_t e = int64_t(x.base) + uniform(int(uint32_t(x.r0 + x.rows - 1) / uint32_t(G))) + 1;
+  x.end = int(e < 0 ? 0 : (e < room ? e : room));
+  x.nt = int((int64_t(x.end) + 63) >> 6);
   x.t0 = 0;
   x.t1 = x.nt;
   x.slot = -1;
@@ -138,7 +154,7 @@ struct ChunkShape {
   static constexpr int kJoin = (4 * kNarrowRows * (D + 4) + 2 * 4 * kNarrowRows) * 4;
   static constexpr int kQ = (D / 64) * 2 * 2 * NP * 64 * 16;  // the narrow form's parts of queries
   static constexpr int most(int x, int y) { return x > y ? x : y; }
-  static constexpr size_t lds = most(most(2 * kStage, kJoin), kQ) + 64;
+  static constexpr size_t lds = most(most(2 * kStage, kJoin), kQ) + 128;  // and a flag, and where the division of the work stands
 };
 
 // One wavefront's share of a tile of rows, with what reads and writes it.
@@ -157,7 +173,7 @@ struct ChunkWork {
   bool neg;
 
   __device__ __forceinline__ ChunkWork(const CacheChunkArgs& args, unsigned char* lds) : a(args), smem(lds) {
-    bad = reinterpret_cast<int*>(lds + W::lds - 64);
+    bad = reinterpret_cast<int*>(lds + W::lds - 128);
     tid = threadIdx.x;
     lane = tid & 63;
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -188,12 +204,10 @@ struct ChunkWork {
     const bool alive = 32 * wave < x.rows;
     const int mine = 32 * wave + l32 < x.rows ? 32 * wave + l32 : 0;  // (rows past the end repeat the first one)
     const uint32_t r = uint32_t(x.r0 + mine), tok = r / uint32_t(G), hd = r % uint32_t(G);
-    const int64_t qp64 = x.base + tok;
-    const int qpos = int(qp64 < -1 ? -1 : qp64);
+    const int qp = x.base + int(tok), qpos = qp < -1 ? -1 : qp;
     const int64_t row = int64_t(x.s.first) + tok;
     const int head = x.kvh * G + int(hd);
-    // first positions of the wavefront's and of the tile's rows
-    const int64_t wmin = x.base + uint32_t(x.r0 + (alive ? 32 * wave : 0)) / uint32_t(G), tmin = x.base + uint32_t(x.r0) / uint32_t(G);
+    const int tmin = uniform(x.base + int(uint32_t(x.r0) / uint32_t(G)));  // position of the tile's first row
 
     bf16x8 qf[NK][NP];
 #pragma unroll
@@ -207,140 +221,174 @@ struct ChunkWork {
     for (int i = 0; i < ND; ++i) acc[i] = zero16();
     float ref = -INFINITY, l = 0.f;
 
-    struct Ids { int p[4]; };
-    auto ids_of = [&](int64_t t) {
-      Ids z;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) z.p[g] = page_of(table, t * 64 + 16 * g, t < x.t1 ? x.end : 0);
-      return z;
+    // A step's pages, and which of its four groups of 16 tokens lie in no page (or behind the last token).  They
+    // come by vector loads, a step ahead: a scalar load on its way makes every wait for the LDS a wait for it too.
+    struct Ids { int page, gone; };  // group g's page in lanes g, g + 4, ...
+    auto ask = [&](int t) {
+      const uint32_t tok = uint32_t(t) * 64 + 16 * (lane & 3);
+      return t < x.t1 && tok < uint32_t(x.end) ? table[tok >> ps] : -1;
     };
-    u32x4 kr[NPC], vr[NPC];
-    float ksc[NPC], vsc[NPC];
-    auto fetch = [&](const Ids& z) {
+    auto ids_of = [&](int asked) {
+      const bool none = asked < 0 || asked >= a.pages;
+      return Ids{none ? 0 : asked, int(__ballot(none)) & 15};  // (what is read for no page is not used)
+    };
+    struct Codes { u32x4 w[NPC]; float scale[NPC]; };
+    auto fetch = [&](Codes& to, const uint8_t* cache, const float* scales, const Ids& z) {
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
         const int at = (wave * NPC + i) * 1024, g = (at / (P * D)) << (ps - 4);  // the page's first 16 tokens
-        const int p = g == 0 ? z.p[0] : (g == 1 ? z.p[1] : (g == 2 ? z.p[2] : z.p[3]));
-        kr[i] = vr[i] = u32x4{0, 0, 0, 0};
-        ksc[i] = vsc[i] = 1.f;
-        if (p >= 0) {
-          const int64_t ph = int64_t(p) * a.Hkv + x.kvh;
-          const int64_t o = ph * P * D + (at & (P * D - 1)) + lane * 16;
-          kr[i] = *reinterpret_cast<const u32x4*>(a.kc + o);
-          vr[i] = *reinterpret_cast<const u32x4*>(a.vc + o);
-          ksc[i] = scalar_load(a.ks + ph);
-          vsc[i] = scalar_load(a.vs + ph);
-        }
+        const int64_t ph = int64_t(__builtin_amdgcn_readlane(z.page, g)) * a.Hkv + x.kvh;
+        to.w[i] = *reinterpret_cast<const u32x4*>(cache + ph * P * D + (at & (P * D - 1)) + lane * 16);
+        to.scale[i] = scales[ph + (lane >> 6)];
       }
     };
-    auto put = [&](int64_t t) {
-      bf16_t* const K = buf + (t & 1) * 2 * 64 * D;
-      bf16_t* const V = K + 64 * D;
-      const int64_t k0 = t * 64;
+    auto put_k = [&](bf16_t* K, const Codes& k) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) {
+        const int at = (wave * NPC + i) * 1024, key = (at + lane * 16) / D, ch = (lane * 16) % D;
+        // row of the tile for a key: bits 2 and 3 change places, so that a result's registers hold runs of eight keys
+        const int kw = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
+        *reinterpret_cast<bf16x8*>(K + TK::off(kw, ch)) = codes(k.w[i][0], k.w[i][1], k.scale[i]);
+        *reinterpret_cast<bf16x8*>(K + TK::off(kw, ch + 8)) = codes(k.w[i][2], k.w[i][3], k.scale[i]);
+      }
+    };
+    // The values of a step that some row does not see all of.
+    auto clean_v = [&](Codes& v, int t, const Ids& z) {
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
         const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
-        const int key = (at + lane * 16) / D, ch = (lane * 16) % D;
-        // row of the tile for a key: bits 2 and 3 change places, so that a result's registers hold runs of eight keys
-        const int kr_ = (key & ~12) | ((key & 4) << 1) | ((key & 8) >> 1);
-        *reinterpret_cast<bf16x8*>(K + TK::off(kr_, ch)) = codes(kr[i][0], kr[i][1], ksc[i]);
-        *reinterpret_cast<bf16x8*>(K + TK::off(kr_, ch + 8)) = codes(kr[i][2], kr[i][3], ksc[i]);
-        const int d = o >> ps, vt = ((at / (P * D)) << ps) + (o & (P - 1));
-        if (k0 + 64 > x.end) {  // what lies behind the last token may be anything, NaN too
-          const int64_t left = x.end - k0 - vt;
+        const int vt = ((at / (P * D)) << ps) + (o & (P - 1));
+        const int left = z.gone >> (vt >> 4) & 1 ? 0 : x.end - t * 64 - vt;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int nb = int(left < 0 ? 0 : (left > 16 ? 16 : left)) - 4 * w;
-            vr[i][w] &= nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
-          }
+        for (int w = 0; w < 4; ++w) {  // what lies behind the last token may be anything, NaN too
+          const int nb = int(left < 0 ? 0 : (left > 16 ? 16 : left)) - 4 * w;
+          v.w[i][w] &= nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
         }
         // A masked probability is zero, but zero times a NaN is not: where a step is masked for some rows such
         // values leave the product, and the rows that see them are set at the end.
-        if (k0 + 63 > tmin && finite_codes(vr[i], vsc[i])) *bad = 1;
-        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt)) = codes(vr[i][0], vr[i][1], vsc[i]);
-        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt + 8)) = codes(vr[i][2], vr[i][3], vsc[i]);
+        if (finite_codes(v.w[i], v.scale[i])) *bad = 1;
       }
     };
-
-    Ids now = ids_of(x.t0);
-    fetch(now);
-    Ids next = ids_of(x.t0 + 1);
-    if (x.t0 < x.t1) put(x.t0);
-    lds_barrier();
-    const uint32_t krow = TK::b_row8_32(lane), vrow = TV::b_row8_32(lane);
-    for (int64_t t = x.t0; t < x.t1; ++t) {
-      const Ids here = now;
-      now = next;
-      if (t + 1 < x.t1) {
-        fetch(now);
-        next = ids_of(t + 2);
+    auto put_v = [&](bf16_t* V, const Codes& v) {
+#pragma unroll
+      for (int i = 0; i < NPC; ++i) {
+        const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
+        const int d = o >> ps, vt = ((at / (P * D)) << ps) + (o & (P - 1));
+        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt)) = codes(v.w[i][0], v.w[i][1], v.scale[i]);
+        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt + 8)) = codes(v.w[i][2], v.w[i][3], v.scale[i]);
       }
-      const bf16_t* K = buf + (t & 1) * 2 * 64 * D;
-      const uint32_t kb = TK::at(K) + krow, vb = TV::at(K + 64 * D) + vrow;
-      if (alive) {
-        f32x16 s[2];
+    };
+    const uint32_t krow = TK::b_row8_32(lane), vrow = TV::b_row8_32(lane);
+    const int first_edge = (tmin + 1) >> 6;  // the first step that some row does not see all of
+    auto k_of = [&](int t) { return buf + (t & 1) * (2 * 64 * D); };
+    int asked = ask(x.t0), asked2 = ask(x.t0 + 1);
+    Ids one = ids_of(asked), two = ids_of(asked2), three;
+    asked = ask(x.t0 + 2);
+    Codes kc, vc;
+    if (x.t0 < x.t1) {
+      Codes k0, v0;
+      fetch(k0, a.kc, a.ks, one);
+      fetch(v0, a.vc, a.vs, one);
+      fetch(kc, a.kc, a.ks, two);
+      fetch(vc, a.vc, a.vs, two);
+      put_k(k_of(x.t0), k0);
+      if (x.t0 >= first_edge || one.gone != 0) clean_v(v0, x.t0, one);
+      put_v(k_of(x.t0) + 64 * D, v0);
+    }
+    lds_barrier();
+    if (!alive) {  // no rows: this wavefront only brings its share of the steps
+      for (int t = x.t0; t < x.t1; ++t) {
+        three = ids_of(asked);
+        asked = ask(t + 3);
+        put_k(k_of(t + 1), kc);
+        clean_v(vc, t + 1, two);
+        put_v(k_of(t + 1) + 64 * D, vc);
+        fetch(kc, a.kc, a.ks, three);
+        fetch(vc, a.vc, a.vs, three);
+        two = three;
+        lds_barrier();
+      }
+      return;
+    }
+    for (int t = x.t0; t < x.t1; ++t) {
+      three = ids_of(asked);
+      asked = ask(t + 3);
+      const uint32_t kb = TK::at(k_of(t)) + krow, vb = TV::at(k_of(t) + 64 * D) + vrow;
+      __builtin_amdgcn_s_setprio(1);
+      f32x16 s[2];
+      s[0] = s[1] = zero16();
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          s[j] = zero16();
+          const bf16x8 kf = TK::row8_32(kb, j, kk);
 #pragma unroll
-          for (int kk = 0; kk < NK; ++kk) {
-            const bf16x8 kf = TK::row8_32(kb, j, kk);
-#pragma unroll
-            for (int i = NP - 1; i >= 0; --i) s[j] = O::mma32(kf, qf[kk][i], s[j]);
-          }
+          for (int i = NP - 1; i >= 0; --i) s[j] = O::mma32(kf, qf[kk][i], s[j]);
         }
-        const bool gone = (here.p[0] | here.p[1] | here.p[2] | here.p[3]) < 0;  // a page that is none of the cache's
-        if (t * 64 + 63 > wmin || gone) {
-          const int left = qpos - int(t * 64) - 8 * h2;  // tokens of this half that the row sees: up to `left`
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              s[j][i] = 32 * j + 16 * (i >> 3) + (i & 7) <= left && here.p[2 * j + (i >> 3)] >= 0 ? s[j][i] : -INFINITY;
-        }
-        float mt = s[0][0];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[j][i]);
-        mt = c * max_halves(mt);
-        if (__any(mt > ref)) {
-          const float up = mt > ref ? mt + 8.f : ref;
-          const float al = up == ref ? 1.f : fast_exp2(ref - up);
-          l *= al;
-#pragma unroll
-          for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][e] *= al;
-          ref = up;
-        }
-        const float from = ref == -INFINITY ? 0.f : ref;  // a row that has met no key yet
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            s[j][i] = fast_exp2(s[j][i] * c - from);
-            l += s[j][i];
-          }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          f32x8 p8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p8[e] = s[u >> 1][8 * (u & 1) + e];
-          const Parts8 pf(p8);
-#pragma unroll
-          for (int i = 0; i < ND; ++i) {
-            const bf16x8 vf = TV::row8_32(vb, i, u);
-#pragma unroll
-            for (int k = NP - 1; k >= 0; --k) acc[i] = O::mma32(vf, part_of(pf, k), acc[i]);
-          }
-        }
+      if (t + 1 < x.t1) {
+        if (t + 1 >= first_edge || two.gone != 0) clean_v(vc, t + 1, two);
+        put_k(k_of(t + 1), kc);
+        put_v(k_of(t + 1) + 64 * D, vc);
       }
-      if (t + 1 < x.t1) put(t + 1);
+      __builtin_amdgcn_s_setprio(0);
+      bf16x8 vf[2][ND];
+#pragma unroll
+      for (int i = 0; i < ND; ++i) vf[0][i] = TV::row8_32(vb, i, 0);
+      
+      if (t + 2 < x.t1) {
+        fetch(kc, a.kc, a.ks, three);
+        fetch(vc, a.vc, a.vs, three);
+      }
+      if (t >= first_edge || one.gone != 0) {
+        const int left = qpos - t * 64 - 8 * h2;  // tokens of this half that the row sees: up to `left`
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[j][i] = 32 * j + 16 * (i >> 3) + (i & 7) <= left && !(one.gone >> (2 * j + (i >> 3)) & 1) ? s[j][i] : -INFINITY;
+      }
+      float mt = s[0][0];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[j][i]);
+      mt = c * max_halves(mt);
+      if (__any(mt > ref)) {
+        const float up = mt > ref ? mt + 8.f : ref;
+        const float al = up == ref ? 1.f : fast_exp2(ref - up);
+        l *= al;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][e] *= al;
+        ref = up;
+      }
+      __builtin_amdgcn_s_setprio(1);
+      const float from = ref == -INFINITY ? 0.f : ref;  // a row that has met no key yet
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (u < 3)
+#pragma unroll
+          for (int i = 0; i < ND; ++i) vf[(u + 1) & 1][i] = TV::row8_32(vb, i, u + 1);
+        f32x8 p8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p8[e] = fast_exp2(s[u >> 1][8 * (u & 1) + e] * c - from);
+        // (summed in pairs: a long row's sum would lose its terms' last bits one by one)
+        l += ((p8[0] + p8[1]) + (p8[2] + p8[3])) + ((p8[4] + p8[5]) + (p8[6] + p8[7]));
+        const Parts8 pf(p8);
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+          for (int k = NP - 1; k >= 0; --k) acc[i] = O::mma32(vf[u & 1][i], part_of(pf, k), acc[i]);
+      }
+      
+      __builtin_amdgcn_s_setprio(0);
+      one = two;
+      two = three;
       lds_barrier();
     }
     l = sum_halves(l);
-    if (!alive || 32 * wave + l32 >= x.rows) return;
+    if (32 * wave + l32 >= x.rows) return;
     if (x.slot < 0) {
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       TO* op = static_cast<TO*>(a.o) + (row * a.Hq + head) * D;
@@ -380,8 +428,8 @@ struct ChunkWork {
     for (int n = 0; n < NC; ++n) {
       const bool live = 16 * n + r16 < x.rows;
       const uint32_t r = uint32_t(x.r0 + (live ? 16 * n + r16 : 0)), tok = r / uint32_t(G), hd = r % uint32_t(G);
-      const int64_t qp = x.base + tok;
-      qpos[n] = int(qp < -1 ? -1 : qp);
+      const int qp = x.base + int(tok);
+      qpos[n] = qp < -1 ? -1 : qp;
       const T* q = static_cast<const T*>(a.q) + (int64_t(x.s.first) + tok) * a.q_stride + int64_t(x.kvh * G + int(hd)) * D;
 #pragma unroll
       for (int m = 0; m < NM; ++m)
@@ -395,18 +443,18 @@ struct ChunkWork {
         }
     }
     if constexpr (QL) lds_barrier();
-    const int64_t tmin = x.base + uint32_t(x.r0) / uint32_t(G);
+    const int tmin = uniform(x.base + int(uint32_t(x.r0) / uint32_t(G)));
 
     u32x4 kr[4][NM], vr[ND];
     float ksc = 1.f, vsc = 1.f;
     // the page of this lane's tokens of a step, as the rows of K (groups by r16) and as the values (by g4)
-    auto page_id = [&](int64_t tok) {
+    auto page_id = [&](uint32_t tok) {
       int p = -1;
-      if (tok < x.end) p = table[tok >> ps];
+      if (tok < uint32_t(x.end)) p = table[tok >> ps];
       return p >= 0 && p < a.pages ? p : -1;
     };
-    auto k_page = [&](int64_t t) { return page_id(t < x.t1 ? t * 64 + 16 * (r16 >> 2) : x.end); };
-    auto v_page = [&](int64_t t) { return page_id(t < x.t1 ? t * 64 + 16 * g4 : x.end); };
+    auto k_page = [&](int t) { return page_id(t < x.t1 ? uint32_t(t) * 64 + 16 * (r16 >> 2) : uint32_t(x.end)); };
+    auto v_page = [&](int t) { return page_id(t < x.t1 ? uint32_t(t) * 64 + 16 * g4 : uint32_t(x.end)); };
     auto load_k = [&](int p) {
       const int64_t ph = int64_t(p < 0 ? 0 : p) * a.Hkv + x.kvh;
       const uint8_t* kp = a.kc + (ph * P + ((16 * (r16 >> 2)) & (P - 1)) + (r16 & 3)) * D + 16 * g4;
@@ -435,7 +483,7 @@ struct ChunkWork {
 #pragma unroll
       for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0, 0, 0, 0};
     }
-    int64_t t = x.t0 + wave;
+    int t = x.t0 + wave;
     int pv = v_page(t), pk1 = k_page(t + 4), pv1 = v_page(t + 4);
     if (t < x.t1) {
       load_k(k_page(t));
@@ -467,13 +515,13 @@ struct ChunkWork {
               for (int q = 0; q < 4; ++q) s[n][q] = O::mma16(kf[q], qp, s[n][q]);
             }
         }
-      const int64_t k0 = t * 64 + 16 * g4;  // this lane's tokens
+      const int64_t k0 = int64_t(t) * 64 + 16 * g4;  // this lane's tokens
       const bool here = pv >= 0;
       load_k(pk1);
       pk1 = k_page(t + 8);
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
-        const int64_t seen = qpos[n] + 1 - k0;
+        const int64_t seen = int64_t(qpos[n]) + 1 - k0;
         const int left = here ? int(seen < 0 ? 0 : (seen > 16 ? 16 : seen)) : 0;
         float mt = -INFINITY;
         if (__any(left < 16)) {
@@ -496,15 +544,17 @@ struct ChunkWork {
           ref[n] = up;
         }
         const float from = ref[n] == -INFINITY ? 0.f : ref[n];
+        float sum = 0.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             s[n][q][i] = fast_exp2(s[n][q][i] * c - from);
-            l[n] += s[n][q][i];
+            sum += s[n][q][i];
           }
+        l[n] += sum;
       }
-      if (t * 64 + 64 > x.end) {  // what lies behind the last token may be anything, NaN too
+      if (x.end - t * 64 < 64) {  // what lies behind the last token may be anything, NaN too
         const int64_t left = x.end - k0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -514,7 +564,7 @@ struct ChunkWork {
           for (int d = 0; d < ND; ++d) vr[d][w] &= mask;
         }
       }
-      if (t * 64 + 63 > tmin) {  // (as in the wide form)
+      if (tmin - t * 64 < 63) {  // (as in the wide form)
         bool any = false;
 #pragma unroll
         for (int d = 0; d < ND; ++d) any |= finite_codes(vr[d], vsc);
@@ -588,16 +638,16 @@ struct ChunkWork {
   // Writes the values that are not finite into the outputs (parts) of the rows that see them: no finite
   // sum, nor a factor, changes them.
   __device__ __forceinline__ void set_bad(const ChunkItem& x, const int* table) {
-    const int64_t tmin = x.base + uint32_t(x.r0) / uint32_t(G);
-    int64_t k0 = tmin < 0 ? 0 : (tmin + 1) & ~int64_t(63);
-    k0 = k0 > x.t0 * 64 ? k0 : x.t0 * 64;
-    const int64_t k1 = x.end < x.t1 * 64 ? x.end : x.t1 * 64;
+    const int tmin = uniform(x.base + int(uint32_t(x.r0) / uint32_t(G)));
+    int64_t k0 = tmin < 0 ? 0 : (tmin + 1) & ~63;
+    k0 = k0 > int64_t(x.t0) * 64 ? k0 : int64_t(x.t0) * 64;
+    const int64_t k1 = x.end < int64_t(x.t1) * 64 ? x.end : int64_t(x.t1) * 64;
     for (int e = tid; e < x.rows * D; e += 256) {
       const int rr = e / D, d = e % D;
       const uint32_t r = uint32_t(x.r0 + rr), tok = r / uint32_t(G);
       float y = 0.f;
 #pragma unroll 1
-      for (int64_t key = k0; key < k1 && key <= x.base + tok; ++key) {
+      for (int64_t key = k0; key < k1 && key <= int64_t(x.base) + tok; ++key) {
         const int p = table[key >> ps];
         if (p < 0 || p >= a.pages) continue;
         const int64_t ph = int64_t(p) * a.Hkv + x.kvh;
@@ -632,6 +682,13 @@ struct ChunkWork {
   }
 };
 
+// Where a workgroup stands: its share still to do, the tile (-1: to be found, `rest` into the sequence's line).
+struct ChunkState {
+  int64_t todo, rest;
+  int seq, kvh, tile, w;
+  ChunkSeq s;
+};
+
 // What a part is, for the kernel that joins them.
 struct ChunkPart {
   int kind;  // 0: none; 1: the tile goes on in the next workgroup; 2: its end
@@ -656,13 +713,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
   const int G = a.Hq / a.Hkv;
 
   const bool shared = a.groups > 0;
-  int seq = 0, kvh = 0, w = 0;
-  int64_t x = 0, x1 = 1, rest = 0, tile = 0;
+  ChunkState z{};
+  z.todo = 1;
   ChunkPart* const parts = reinterpret_cast<ChunkPart*>(a.part + int64_t(a.groups) * 2 * chunk_part_floats(D));
   if (!shared) {
     // Sequence i's tiles sit at slots cu[i] G / 128 + i onwards, which leaves each at least as many as it has.
     const int slots = int(gridDim.x / a.Hkv), slot = slots - 1 - int(blockIdx.x / a.Hkv);  // long rows first
-    kvh = int(blockIdx.x % a.Hkv);
+    z.kvh = int(blockIdx.x % a.Hkv);
     int lo = 0, up = a.N;
     auto start = [&](int64_t i) {
       const int64_t c = a.cu[i];
@@ -674,8 +731,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
       lo += step * __popcll(__ballot(mid < up && start(mid) <= slot));
       up = lo + step < up ? lo + step : up;
     }
-    seq = uniform(lo);
-    tile = uniform(slot - start(lo));
+    const int64_t tile = slot - start(lo);
+    z.s = chunk_seq(a, lo);
+    if (tile < 0 || tile >= ChunkCost(a, z.s).tiles) return;
+    z.seq = lo;
+    z.tile = int(tile);
   } else {
     // Every workgroup takes an equal piece of the line of all tiles' costs, key heads outermost.
     int64_t* const sums = reinterpret_cast<int64_t*>(smem);  // [256] costs of the threads' sequences before each, [4]
@@ -699,98 +759,166 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
     head = uniform(head);
     sums[tid] = upto - mine;
     __syncthreads();
-    const int64_t all = head * a.Hkv, least = 2 * kStartCost * G;
-    int64_t groups = all / least;
-    groups = groups < 1 ? 1 : (groups < a.groups ? groups : a.groups);
-    w = xcd_order(blockIdx.x, a.groups);
+    const int64_t all = head * a.Hkv, most = all / (kLeastCost * G);
+    const int groups = int(most < 1 ? 1 : (most < a.groups ? most : a.groups));
+    const int w = xcd_order(blockIdx.x, a.groups);
     if (tid == 0) parts[2 * w].kind = parts[2 * w + 1].kind = 0;
     if (w >= groups || all == 0) return;
-    const int64_t each = all / groups, more = all % groups;
-    x = uniform(each * w + (w < more ? w : more));
-    x1 = uniform(x + each + (w < more ? 1 : 0));
-    kvh = uniform(int(x / head));
-    rest = uniform(x % head);  // to go within this key head's line
+    const int64_t each = quotient(all, groups), more = all - each * groups;
+    const int64_t x = uniform(each * w + (w < more ? w : more));
+    z.todo = each + (w < more ? 1 : 0);
+    z.kvh = int(quotient(x, head));
+    const int64_t rest = x - z.kvh * head;  // to go within this key head's line
     int lo = 0, up = 256;
     while (up - lo > 1) {
       const int mid = (lo + up) / 2;
       if (sums[mid] <= rest) lo = mid;
       else up = mid;
     }
-    rest = uniform(rest - sums[lo]);
-    seq = uniform(lo * per);
+    z.rest = rest - sums[lo];
+    z.seq = lo * per;
+    z.tile = -1;  // to be found
+    z.s = chunk_seq(a, z.seq);
+    z.w = w;
   }
-  while (x < x1) {
-    const ChunkSeq s = uniform(chunk_seq(a, seq));
-    const ChunkCost cost(a, s);
-    int64_t from = 0, to = 1, full = 1;
+  // What comes next is kept in the LDS while an item is worked on: in scalar registers it would push others out.
+  ChunkState* const state = reinterpret_cast<ChunkState*>(smem + ChunkShape<T, D>::lds - 112);
+  for (;;) {
+    int64_t from = 0, to = 1, full = 1, rest = uniform(z.rest);
+    ChunkSeq s = uniform(z.s);
+    int tile = uniform(z.tile), seq = uniform(z.seq), kvh = uniform(z.kvh);
+    const int64_t todo = uniform(z.todo);
+    const int w = uniform(z.w);
     if (shared) {
-      if (rest >= cost.all()) {  // an earlier workgroup's, or empty
-        rest -= cost.all();
+      ChunkCost cost(a, s);
+      while (tile >= cost.tiles || (tile < 0 && rest >= cost.all())) {  // behind this sequence's tiles
+        rest = tile < 0 ? rest - cost.all() : 0;
+        tile = rest > 0 ? -1 : 0;
         if (++seq == a.N) {
           seq = 0;
           ++kvh;
         }
-        continue;
+        s = uniform(chunk_seq(a, seq));
+        cost = ChunkCost(a, s);
       }
-      int64_t up = cost.tiles;
-      tile = 0;
-      while (up - tile > 1) {
-        const int64_t mid = (tile + up) / 2;
-        if (cost.before(mid) <= rest) tile = mid;
-        else up = mid;
+      if (tile < 0) {
+        tile = int(cost.at(rest));
+        from = rest - cost.before(tile);
       }
       full = cost.of(tile);
-      from = rest - cost.before(tile);
-      to = from + (x1 - x) < full ? from + (x1 - x) : full;
-    } else if (tile < 0 || tile >= cost.tiles) {
-      return;
+      to = from + todo < full ? from + todo : full;
     }
     ChunkItem it = chunk_item(a, s, kvh, tile);
-    if (shared) {
-      it.t0 = uniform(from * it.nt / full);
-      it.t1 = uniform(to * it.nt / full);
-      if (from > 0 || to < full) {
-        it.slot = 2 * w + (from > 0 ? 0 : 1);
-        if (tid == 0) parts[it.slot] = ChunkPart{to < full ? 1 : 2, s.first, kvh, it.r0, it.rows, {0, 0, 0}};
-      }
+    if (shared && (from > 0 || to < full)) {
+      // (the same step from both sides of a cut: both form it from the same numbers)
+      it.t0 = from > 0 ? uniform(int(double(from) * double(it.nt) / double(full))) : 0;
+      if (to < full) it.t1 = uniform(int(double(to) * double(it.nt) / double(full)));
+      it.slot = 2 * w + (from > 0 ? 0 : 1);
+      if (tid == 0) parts[it.slot] = ChunkPart{to < full ? 1 : 2, s.first, kvh, it.r0, it.rows, {0, 0, 0}};
     }
+    lds_barrier();  // the state has been read
+    if (tid == 0) *state = ChunkState{todo - (to - from), 0, seq, kvh, tile + 1, w, s};
     work.run(it, seq);
-    x = uniform(x + (to - from));
-    rest = uniform(rest + (to - from));
+    lds_barrier();
+    z = *state;
+    if (uniform(z.todo) <= 0) return;
   }
 }
 
-// Joins the parts of the tile that begins in workgroup blockIdx.x and ends in a later one, 16 rows of it.
+// Joins the parts of the tile that begins in workgroup blockIdx.x and ends in a later one: a sixteenth of its
+// rows.  D / 4 threads to a row.  Most tiles have two to four parts, which are read all at once; of more, several
+// groups of threads share a row's.
+constexpr int kJoinBlocks = 16, kJoinFew = 4;
+static_assert(kJoinBlocks * 8 >= kChunkRows, "every row has a group of threads");
 template <typename TO, int D>
 __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkArgs a) {
+  constexpr int L = D / 4, NG = 256 / L;
+  __shared__ f32x4 sy[NG][L];
+  __shared__ float sl[NG];
+  __shared__ int end;
   const ChunkPart* const parts = reinterpret_cast<const ChunkPart*>(a.part + int64_t(a.groups) * 2 * chunk_part_floats(D));
-  const int w = blockIdx.x, G = a.Hq / a.Hkv;
+  const int w = blockIdx.x, tid = threadIdx.x, G = a.Hq / a.Hkv, g = tid / L, e = tid % L;
   const ChunkPart p = parts[2 * w + 1];
-  const int r = 16 * blockIdx.y + threadIdx.x / 16, c0 = (D / 16) * (threadIdx.x % 16);
-  if (p.kind != 1 || r >= p.rows) return;
-  int last = w + 1;
-  while (last + 1 < a.groups && parts[2 * last].kind == 1) ++last;
+  int few[kJoinFew];
+#pragma unroll
+  for (int i = 1; i < kJoinFew; ++i) few[i] = w + i < a.groups ? parts[2 * (w + i)].kind : 0;
+  if (p.kind != 1) return;  // (the rest of p says nothing then)
+  int lg = 0;               // rows of a block: 1 << lg
+#pragma unroll
+  for (int i = 0; i < 3; ++i) lg += (kJoinBlocks << i) < p.rows;
+  const int per = 1 << lg, row0 = int(blockIdx.y) << lg, r = row0 + (g & (per - 1));
+  if (row0 >= p.rows) return;
+  const bool live = r < p.rows;
+  auto part = [&](int i) { return a.part + int64_t(i == 0 ? 2 * w + 1 : 2 * (w + i)) * chunk_part_floats(D); };
+  auto write = [&](f32x4 y, float l, float m) {
+    const uint32_t rr = uint32_t(p.r0 + r);
+    const int64_t row = (int64_t(p.first) + rr / uint32_t(G)) * a.Hq + p.kvh * G + int(rr % uint32_t(G));
+    store4(static_cast<TO*>(a.o) + row * D + 4 * e, y * (l == 0.f ? 0.f : 1.0f / l));
+    if (a.lse && e == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+  };
+  int n = 0;  // parts, where they are few
+#pragma unroll
+  for (int i = kJoinFew - 1; i > 0; --i) n = few[i] == 2 ? i + 1 : n;
+  if (n > 0) {
+    if (!live || g >= per) return;
+    f32x4 y[kJoinFew];
+    f32x2 ml[kJoinFew];
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      const float* pp = part(i < n ? i : 0);
+      y[i] = *reinterpret_cast<const f32x4*>(pp + r * D + 4 * e);
+      ml[i] = *reinterpret_cast<const f32x2*>(pp + kChunkRows * D + 2 * r);
+    }
+    float m = ml[0][0];
+#pragma unroll
+    for (int i = 1; i < kJoinFew; ++i) m = i < n ? fmaxf(m, ml[i][0]) : m;
+    const float from = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i)
+      if (i < n) {
+        const float f = fast_exp2(ml[i][0] - from);
+        l += f * ml[i][1];
+        sum += y[i] * f;
+      }
+    write(sum, l, m);
+    return;
+  }
+  if (tid == 0) end = a.groups - 1;
+  __syncthreads();
+  for (int i = w + 1; i < a.groups; i += 256) {  // its last part: the first one that does not go on
+    if (i + tid < a.groups && parts[2 * (i + tid)].kind != 1) atomicMin(&end, i + tid);
+    __syncthreads();
+    if (end < i + 256) break;
+  }
+  n = end - w + 1;
+  const int share = NG >> lg;  // groups to a row
   float m = -INFINITY;
-  auto of = [&](int i) { return a.part + int64_t(i == w ? 2 * w + 1 : 2 * i) * chunk_part_floats(D); };
-  for (int i = w; i <= last; ++i) m = fmaxf(m, of(i)[kChunkRows * D + 2 * r]);
+  if (live)
+    for (int i = e; i < n; i += L) m = fmaxf(m, part(i)[kChunkRows * D + 2 * r]);
+#pragma unroll
+  for (int d = 1; d < L; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
   const float from = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  f32x4 y[D / 64];
-#pragma unroll
-  for (int j = 0; j < D / 64; ++j) y[j] = f32x4{0, 0, 0, 0};
-  for (int i = w; i <= last; ++i) {
-    const float* pp = of(i);
-    const float f = fast_exp2(pp[kChunkRows * D + 2 * r] - from);
-    l += f * pp[kChunkRows * D + 2 * r + 1];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) y[j] += *reinterpret_cast<const f32x4*>(pp + r * D + c0 + 4 * j) * f;
+  f32x4 y = {0, 0, 0, 0};
+  if (live)
+#pragma unroll 4
+    for (int i = g >> lg; i < n; i += share) {
+      const float* pp = part(i);
+      const float f = fast_exp2(pp[kChunkRows * D + 2 * r] - from);
+      l += f * pp[kChunkRows * D + 2 * r + 1];
+      y += *reinterpret_cast<const f32x4*>(pp + r * D + 4 * e) * f;
+    }
+  sy[g][e] = y;
+  if (e == 0) sl[g] = l;
+  __syncthreads();
+  if (g >= per || !live) return;
+  for (int i = g + per; i < NG; i += per) {
+    y += sy[i][e];
+    l += sl[i];
   }
-  const uint32_t rr = uint32_t(p.r0 + r);
-  const int64_t row = (int64_t(p.first) + rr / uint32_t(G)) * a.Hq + p.kvh * G + int(rr % uint32_t(G));
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-#pragma unroll
-  for (int j = 0; j < D / 64; ++j) store4(static_cast<TO*>(a.o) + row * D + c0 + 4 * j, y[j] * inv);
-  if (a.lse && c0 == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+  write(y, l, m);
 }
 
 template <typename T, typename TO, int D>
@@ -807,7 +935,7 @@ hipError_t launch_chunk(const CacheChunkArgs& a, hipStream_t st) {
   kern<<<dim3(uint32_t(grid < 1 ? 1 : grid)), 256, lds, st>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.groups == 0) return e;
-  cache_chunk_join_kernel<TO, D><<<dim3(uint32_t(a.groups), kChunkRows / 16), 256, 0, st>>>(a);
+  cache_chunk_join_kernel<TO, D><<<dim3(uint32_t(a.groups), kJoinBlocks), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
