@@ -502,14 +502,20 @@ def _dims(what: str, *specs):
 _MAY_BE_NONE = ("S_in", "S_out", "dS_out", "lse")  # (where one of them is required, the C ABI says so)
 
 
-def _match(what: str, *specs):
-    """One pass over (name, tensor, shape, allowed dtypes): what ``_shapes`` and ``_dev`` check."""
-    dev = None
+def _match(what: str, *specs, like=None):
+    """One pass over (name, tensor, shape, allowed dtypes): what ``_shapes`` and ``_dev`` check.  The device is that of
+    ``like``, else of the first tensor."""
+    dev = None if like is None else like.get_device()
     for name, t, shape, dtypes in specs:
         if not isinstance(t, torch.Tensor):
             if t is None and name in _MAY_BE_NONE:
                 continue
             raise KDAError(f"{what}: {name} must be a tensor")
+        at = t.get_device()  # (-1: on the CPU)
+        if dev is None:
+            dev = at
+        if t.shape == shape and t.dtype in dtypes and at == dev and at >= 0 and t.is_contiguous():
+            continue
         if t.shape != shape:
             raise KDAError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t.dtype not in dtypes:
@@ -518,10 +524,7 @@ def _match(what: str, *specs):
             raise KDAError("libkda runs on the GPU only: tensor is on the CPU")
         if not t.is_contiguous():
             raise KDAError(f"{what}: {name} must be contiguous")
-        if dev is None:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on cuda:{dev}")
+        raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on cuda:{dev}")
 
 
 def _a(t: Optional[torch.Tensor]):
@@ -729,34 +732,38 @@ def _rows(what: str, name: str, t, shape, dtypes, like) -> int:
         raise KDAError(f"{what}: {name} must be a tensor of shape {tuple(shape)}")
     if t.dtype not in dtypes:
         raise KDAError(f"{what}: {name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise KDAError("libkda runs on the GPU only: tensor is on the CPU")
-    if t.get_device() != like.get_device():
+    if at != like.get_device():
         raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on {like.device}")
     n, H, d = shape
     row, head, one = t.stride()
-    if t.numel() and ((d > 1 and one != 1) or (H > 1 and head != d) or (n > 1 and row < H * d)):
-        raise KDAError(f"{what}: {name} has strides {t.stride()}: a row's {H} heads of {d} must lie together")
-    return row if n > 1 and t.numel() else H * d
+    if n <= 1 or H * d == 0:
+        row = H * d
+    if (one != 1 and d > 1) or (head != d and H > 1) or row < H * d:
+        if t.numel():
+            raise KDAError(f"{what}: {name} has strides {t.stride()}: a row's {H} heads of {d} must lie together")
+    return row
 
 
-def _turn(what: str, n: int, positions, inv_freq, axes, interleaved, like):
-    """Arguments of a rotation after their checks: positions, axes' number, inv_freq, axes, rot, interleaved."""
-    _dims(what, ("inv_freq", inv_freq, 1))
+def _turn(what: str, n: int, positions, inv_freq, axes):
+    """A rotation's number of axes, its pairs, and the specs of its tensors for ``_match``."""
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise KDAError(f"{what}: inv_freq must be a tensor of 1 dimensions")
     half, A = inv_freq.shape[0], 1
     specs = [("inv_freq", inv_freq, (half,), _F32)]
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
             raise KDAError(f"{what}: positions must be a tensor [n] or [n, axes]")
-        A = positions.shape[1] if positions.dim() == 2 else 1
-        specs.append(("positions", positions, (n,) if positions.dim() == 1 else (n, A), _I32))
+        if positions.dim() == 1:
+            specs.append(("positions", positions, (n,), _I32))
+        else:
+            A = positions.shape[1]
+            specs.append(("positions", positions, (n, A), _I32))
     if axes is not None:
         specs.append(("axes", axes, (half,), _I32))
-    _match(what, *specs)
-    for name, t, _, _ in specs:
-        if t.get_device() != like.get_device():
-            raise KDAError(f"{what}: {name} is on {t.device}, the other tensors on {like.device}")
-    return _a(positions), A, _a(inv_freq), _a(axes), 2 * half, int(bool(interleaved))
+    return A, half, specs
 
 
 @_run_on_stream
@@ -773,25 +780,28 @@ def rope(x, positions, inv_freq, axes=None, interleaved: bool = False, inverse: 
     xs = _rows(what, "x", x, (n, H, d), _IO, x)
     if out is None:
         out = torch.empty((n, H, d), dtype=_out_dtype(out_dtype or x.dtype, what, "out_dtype"), device=x.device)
-    ys = _rows(what, "out", out, (n, H, d), _IO, x)
-    if not isinstance(positions, torch.Tensor):
+        ys = H * d
+    else:
+        ys = _rows(what, "out", out, (n, H, d), _IO, x)
+    if positions is None:
         raise KDAError(f"{what}: positions must be a tensor [n] or [n, axes]")
-    pos, A, inv, ax, rot, inter = _turn(what, n, positions, inv_freq, axes, interleaved, x)
-    _check(lib().kda_rope(_a(x), _dtype_code(x), xs, pos, A, inv, ax, rot, inter, int(bool(inverse)), _a(out),
-                          _dtype_code(out), ys, n, H, d, _here(x)), what)
+    A, half, specs = _turn(what, n, positions, inv_freq, axes)
+    _match(what, *specs, like=x)
+    _check(lib().kda_rope(_a(x), _dtype_code(x), xs, _a(positions), A, _a(inv_freq), _a(axes), 2 * half, int(bool(interleaved)),
+                          int(bool(inverse)), _a(out), _dtype_code(out), ys, n, H, d, _here(x)), what)
     return out
 
 
 _F8 = (torch.float8_e4m3fn,)
 
 
-def _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len, *more):
+def _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len, *more, like=None):
     _dims(what, ("k_cache", k_cache, 4), ("block_table", block_table, 2))
     pages, _, page, _ = k_cache.shape
     N, max_pages = block_table.shape
     _match(what, *more, ("k_cache", k_cache, (pages, Hkv, page, d), _F8), ("v_cache", v_cache, (pages, Hkv, d, page), _F8),
            ("k_scale", k_scale, (pages, Hkv), _F32), ("v_scale", v_scale, (pages, Hkv), _F32),
-           ("block_table", block_table, (N, max_pages), _I32), ("context_len", context_len, (N,), _I32))
+           ("block_table", block_table, (N, max_pages), _I32), ("context_len", context_len, (N,), _I32), like=like)
     return N, page, pages, max_pages
 
 
@@ -822,7 +832,7 @@ def kv_cache_append_rope(k, v, cu_seqlens, context_len, block_table, k_cache, v_
     Returns the turned queries (``q_out_dtype``, default q's), or None without q.  Rows behind the last
     sequence: a given ``q_out`` keeps what it holds there, a new one is zero there."""
     what = "kda_kv_cache_append_rope"
-    _dims(what, ("k", k, 3), ("cu_seqlens", cu_seqlens, 1), ("context_len", context_len, 1))
+    _dims(what, ("k", k, 3), ("context_len", context_len, 1))
     n, Hkv, d = k.shape
     k_row, v_row = _rows(what, "k", k, (n, Hkv, d), _IO, k), _rows(what, "v", v, (n, Hkv, d), _io_of(k), k)
     given, Hq, q_row, o_row, o_code = q_out is not None, Hkv, Hkv * d, Hkv * d, _dtype_code(k)
@@ -830,20 +840,22 @@ def kv_cache_append_rope(k, v, cu_seqlens, context_len, block_table, k_cache, v_
         _dims(what, ("q", q, 3))
         Hq = q.shape[1]
         q_row = _rows(what, "q", q, (n, Hq, d), _io_of(k), k)
-        if not given:
+        if given:
+            o_row = _rows(what, "q_out", q_out, (n, Hq, d), _IO, k)
+        else:
             q_out = torch.empty((n, Hq, d), dtype=_out_dtype(q_out_dtype or q.dtype, what, "q_out_dtype"), device=q.device)
-        o_row, o_code = _rows(what, "q_out", q_out, (n, Hq, d), _IO, k), _dtype_code(q_out)
+            o_row = Hq * d
+        o_code = _dtype_code(q_out)
     elif given:
         raise KDAError(f"{what}: q_out without q")
-    pos, A, inv, ax, rot, inter = _turn(what, n, positions, inv_freq, axes, interleaved, k)
-    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
-                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32))
-    if cu_seqlens.get_device() != k.get_device():
-        raise KDAError(f"{what}: cu_seqlens is on {cu_seqlens.device}, the other tensors on {k.device}")
+    A, half, specs = _turn(what, n, positions, inv_freq, axes)
+    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len, *specs,
+                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32), like=k)
     _check(lib().kda_kv_cache_append_rope(_a(k), k_row, _a(v), v_row, _dtype_code(k), _a(q), q_row, _a(q_out), o_code, o_row,
-                                          pos, A, inv, ax, rot, inter, _a(cu_seqlens), _a(context_len), _a(block_table),
-                                          _a(k_cache), _a(v_cache), _a(k_scale), _a(v_scale), n, N, Hq, Hkv, d, page, pages,
-                                          mp, int(not given), _here(k)), what)
+                                          _a(positions), A, _a(inv_freq), _a(axes), 2 * half, int(bool(interleaved)),
+                                          _a(cu_seqlens), _a(context_len), _a(block_table), _a(k_cache), _a(v_cache),
+                                          _a(k_scale), _a(v_scale), n, N, Hq, Hkv, d, page, pages, mp, int(not given),
+                                          _here(k)), what)
     return q_out
 
 
@@ -898,21 +910,22 @@ def attn_chunk_fwd(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tabl
     fp32 or None); a row that sees no token gets o = 0, lse = -inf.  Rows behind the last sequence: given
     ``o`` and ``lse`` keep what they hold there, new ones are zero there."""
     what = "kda_attn_chunk_fwd"
-    _dims(what, ("q", q, 3), ("cu_seqlens", cu_seqlens, 1), ("context_len", context_len, 1), ("k_cache", k_cache, 4))
+    _dims(what, ("q", q, 3), ("context_len", context_len, 1), ("k_cache", k_cache, 4))
     n, Hq, d = q.shape
     Hkv = k_cache.shape[1]
     q_row = _rows(what, "q", q, (n, Hq, d), _IO, q)
-    given = o is not None or lse is not None
-    if o is None:
+    given, specs = o is not None or lse is not None, []
+    if o is not None:
+        specs.append(("o", o, (n, Hq, d), _IO))
+    else:
         o = (torch.zeros if given else torch.empty)((n, Hq, d), dtype=_out_dtype(o_dtype, what, "o_dtype"), device=q.device)
-    if lse is None and want_lse:
+    if lse is not None:
+        specs.append(("lse", lse, (n, Hq), _F32))
+    elif want_lse:
         lse = (torch.zeros if given else torch.empty)((n, Hq), dtype=torch.float32, device=q.device)
-    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len,
-                                       ("o", o, (n, Hq, d), _IO), ("lse", lse, (n, Hq), _F32),
-                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32))
-    if o.get_device() != q.get_device():
-        raise KDAError(f"{what}: o is on {o.device}, q on {q.device}")
-    need = attn_chunk_fwd_workspace_bytes(n, N, Hq, Hkv, d, page, mp, q.dtype) if pages and Hkv else 0
+    N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len, *specs,
+                                       ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32), like=q)
+    need = lib().kda_attn_chunk_fwd_workspace_bytes(n, N, Hq, Hkv, d, page, mp, _dtype_code(q)) if pages and Hkv else 0
     wp, wb, _keep = _need(workspace, need, q.device)
     _check(lib().kda_attn_chunk_fwd(_a(q), q_row, _dtype_code(q), _a(cu_seqlens), _a(k_cache), _a(v_cache), _a(k_scale),
                                     _a(v_scale), _a(block_table), _a(context_len), _a(o), _dtype_code(o), _a(lse), n, N, Hq, Hkv,

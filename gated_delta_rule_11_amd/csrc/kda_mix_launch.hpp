@@ -128,9 +128,13 @@ struct RopeArgs {
   int64_t x_stride, y_stride;
   Rotation turn;
   int n, H, d;
-  int heads;  // of a wavefront
+  int rows, side, heads;  // of a wavefront: rows, heads at a time, heads in all (rope_waves)
   bool inverse, in_bf16, out_bf16;
 };
+// The items of wavefronts: parts of every `rows` rows.
+inline int64_t rope_items(const RopeArgs& a) {
+  return (int64_t(a.n) + a.rows - 1) / a.rows * ((a.H + a.heads - 1) / a.heads);
+}
 hipError_t launch_rope(const RopeArgs& a, hipStream_t st);
 
 // ---- attention over a paged cache in 8 bits -------------------------------------------

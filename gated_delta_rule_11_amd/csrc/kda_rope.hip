@@ -1,9 +1,8 @@
 // kda_rope.hip -- rotary positions over rows of heads, and their gradient (the turn backwards).
 //
-// Bound by the bytes of x and y.  One wavefront takes one row and some of its heads: its lanes form the
-// row's sines and cosines once, one pair (two where half > 64) each, and hand them round through the
-// LDS; then each lane turns one unit of 16 channels for head after head, so the row's sines cost a
-// few instructions a head and neighbouring lanes read neighbouring memory.
+// Bound by the bytes of x and y.  A wavefront's lanes form the sines and cosines of its rows once, one pair after
+// another, and hand them round through the LDS; then each lane turns one unit of 16 channels for head after head, so
+// the sines cost a few instructions a head and neighbouring lanes read neighbouring memory.
 #include "kda_mix_launch.hpp"
 #include "kda_rotary.hpp"
 
@@ -13,19 +12,18 @@ namespace {
 
 template <typename T, typename TO>
 __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs a) {
-  __shared__ float sc[4][2][128];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ float sc[4][2][kSines];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t item = int64_t(blockIdx.x) * 4 + wave;
   const int parts = (a.H + a.heads - 1) / a.heads;
-  const int64_t row = item / parts;
-  if (row >= a.n) return;  // (no barrier follows: a wavefront only reads what it wrote itself)
-  rotate_row<T, TO>(a, row, 0, int(item % parts) * a.heads, sc[wave], lane);
+  const int64_t row0 = item / parts * a.rows;
+  if (row0 >= a.n) return;  // (no barrier follows: a wavefront only reads what it wrote itself)
+  rotate_rows<T, TO>(a, row0, 0, int(item % parts) * a.heads, sc[wave], lane);
 }
 
 template <typename T, typename TO>
 hipError_t launch(const RopeArgs& a, hipStream_t st) {
-  const int64_t items = int64_t(a.n) * ((a.H + a.heads - 1) / a.heads);
-  rope_kernel<T, TO><<<dim3(uint32_t((items + 3) / 4)), 256, 0, st>>>(a);
+  rope_kernel<T, TO><<<dim3(uint32_t((rope_items(a) + 3) / 4)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

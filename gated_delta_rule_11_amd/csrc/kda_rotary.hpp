@@ -121,33 +121,37 @@ __device__ __forceinline__ int sequence_of(const int* cu, int N, int64_t row, in
   return lo;
 }
 
-// One row's heads h0 .. h0 + heads - 1 turned by one wavefront; `sc` is its own LDS.
+// Heads h0 .. h0 + heads - 1 of rows row0 .. row0 + rows - 1 turned by one wavefront, `side` heads at a time; `sc` is
+// its own LDS.  (`place` is for one row.)
+constexpr int kSines = 512;  // of a wavefront: rows * half, at most 64 / (d / 16) * d / 2
 template <typename T, typename TO>
-__device__ __forceinline__ void rotate_row(const RopeArgs& a, int64_t row, int64_t place, int h0, float (*sc)[128], int lane) {
-  const int half = a.turn.half, units = a.d / 16, side = 64 / units;
+__device__ __forceinline__ void rotate_rows(const RopeArgs& a, int64_t row0, int64_t place, int h0, float (*sc)[kSines], int lane) {
+  const int half = a.turn.half, units = a.d / 16;
   const bool inter = a.turn.interleaved;
-  for (int j = lane; j < half; j += 64) {
-    double s, c;
-    sine_cosine(angle_of(a.turn, row, place, j), s, c);
+  for (int j = lane; j < a.rows * half; j += 64) {
+    const int64_t row = row0 + j / half;
+    double s = 0.0, c = 1.0;
+    if (row < a.n) sine_cosine(angle_of(a.turn, row, place, j % half), s, c);
     sc[0][j] = float(c);
     sc[1][j] = float(a.inverse ? -s : s);
   }
   __builtin_amdgcn_wave_barrier();
-  const int u = lane % units, hl = lane / units;
-  if (hl >= side) return;
+  const int u = lane % units, g = lane / units, r = g / a.side;
+  const int64_t row = row0 + r;
+  if (r >= a.rows || row >= a.n) return;
   const Unit w = unit_of(u, half);
   float c[8], s[8];
   if (w.turns)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      c[e] = sc[0][pair_of(u, e, half, inter)];
-      s[e] = sc[1][pair_of(u, e, half, inter)];
+      c[e] = sc[0][r * half + pair_of(u, e, half, inter)];
+      s[e] = sc[1][r * half + pair_of(u, e, half, inter)];
     }
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   TO* y = static_cast<TO*>(a.y) + row * a.y_stride;
   const int end = h0 + a.heads < a.H ? h0 + a.heads : a.H;
 #pragma unroll 4
-  for (int h = h0 + hl; h < end; h += side) {
+  for (int h = h0 + g % a.side; h < end; h += a.side) {
     f32x8 x0 = Op<T>::unpack(Op<T>::load(x + int64_t(h) * a.d + 8 * w.c0));
     f32x8 x1 = Op<T>::unpack(Op<T>::load(x + int64_t(h) * a.d + 8 * w.c1));
     if (w.turns) turn(x0, x1, c, s, inter);

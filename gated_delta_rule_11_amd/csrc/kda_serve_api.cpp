@@ -42,12 +42,20 @@ bool turn_ok(int rot, int d, int n_axes, int interleaved) {
   return rot >= 16 && rot % 16 == 0 && rot <= d && n_axes >= 1 && n_axes <= kMaxAxes && flag_ok(interleaved);
 }
 
-// Heads that one wavefront turns: all of a row's, or fewer where that leaves the GPU short of wavefronts.
-int heads_of_wave(int64_t n, int H, int d) {
-  const int side = 64 / (d / 16), all = (H + side - 1) / side;
-  const int64_t want = n < 1 ? 1 : (8192 + n - 1) / n;
-  const int parts = int(want < all ? want : all);
-  return (all + parts - 1) / parts * side;
+// What one wavefront turns: with `many`, so many rows that its lanes, a unit of 16 channels each, come out even with
+// the heads (24 heads of 64 channels: two rows of eight heads at a time); all of the rows' heads, or fewer where that
+// leaves the GPU short of wavefronts.
+void rope_waves(RopeArgs& a, bool many) {
+  const int most = 64 / (a.d / 16);
+  a.side = most;
+  a.rows = 1;
+  if (many) {
+    while (a.H % a.side != 0) --a.side;
+    a.rows = most / a.side;
+  }
+  const int64_t all = (a.H + a.side - 1) / a.side, groups = (int64_t(a.n) + a.rows - 1) / a.rows;
+  const int64_t want = groups < 1 ? 1 : (8192 + groups - 1) / groups, parts = want < all ? want : all;
+  a.heads = int((all + parts - 1) / parts * a.side);
 }
 
 // Query heads that share a key head: the costs by which workgroups divide the work stay in 64 bits.
@@ -68,8 +76,10 @@ kda_status kda_rope(const void* x, kda_dtype in_dtype, int64_t x_stride, const i
   kda_status s = stride_ok(x_stride, H, d, ex), t = stride_ok(y_stride, H, d, ey);
   if (s == KDA_ERR_SHAPE || t == KDA_ERR_SHAPE) return KDA_ERR_SHAPE;
   if (n == 0) return KDA_OK;
-  const int heads = heads_of_wave(n, H, d);
-  if ((int64_t(n) * ((H + heads - 1) / heads) + 3) / 4 > kMaxGrid) return KDA_ERR_SHAPE;
+  RopeArgs args{x, y, x_stride, y_stride, Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, H, d, 1, 1, 1,
+                inverse != 0, in_dtype == KDA_BF16, y_dtype == KDA_BF16};
+  rope_waves(args, true);
+  if ((rope_items(args) + 3) / 4 > kMaxGrid) return KDA_ERR_SHAPE;
   if (!x || !positions || !inv_freq || !y) return KDA_ERR_NULL;
   if (s != KDA_OK || t != KDA_OK || !all_aligned({x, y}, positions, 4) || !aligned(inv_freq, 4) || !aligned(axes, 4))
     return KDA_ERR_ALIGN;
@@ -80,10 +90,7 @@ kda_status kda_rope(const void* x, kda_dtype in_dtype, int64_t x_stride, const i
   const Range ins[] = {{positions, int64_t(n) * n_axes * 4}, {inv_freq, int64_t(rot) * 2}, {axes, int64_t(rot) * 2}};
   for (const Range& in : ins)
     if (overlap(ry, in)) return KDA_ERR_ALIAS;
-  return from_hip(launch_rope(RopeArgs{x, y, x_stride, y_stride,
-                                       Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, H, d, heads,
-                                       inverse != 0, in_dtype == KDA_BF16, y_dtype == KDA_BF16},
-                              static_cast<hipStream_t>(stream)));
+  return from_hip(launch_rope(args, static_cast<hipStream_t>(stream)));
 }
 
 kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_stride, kda_dtype in_dtype,
@@ -105,8 +112,11 @@ kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void*
     if (t == KDA_ERR_SHAPE) return t;
   const bool cache = N > 0 && n_pages > 0 && max_pages > 0, turns = q && (N > 0 || zero_tail);
   if (n == 0 || (!cache && !turns)) return KDA_OK;
-  const int heads = q ? heads_of_wave(n, Hq, d) : 1;
-  const int64_t items = q ? (int64_t(n) * ((Hq + heads - 1) / heads) + 3) / 4 : 0;
+  RopeArgs queries{turns ? q : nullptr, q_out, q_stride, q_out_stride,
+                   Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, Hq, d, 1, 1, 1, false,
+                   in_dtype == KDA_BF16, q_out_dtype == KDA_BF16};
+  if (q) rope_waves(queries, false);
+  const int64_t items = q ? (rope_items(queries) + 3) / 4 : 0;
   if ((int64_t(n) / page + 2 * int64_t(N)) * Hkv + items > kMaxGrid) return KDA_ERR_SHAPE;
   if (!inv_freq || !cu_seqlens || (N > 0 && !context_len) || (!positions && n_axes != 1) || (q && !q_out)) return KDA_ERR_NULL;
   if (cache && (!k || !v || !block_table || !k_cache || !v_cache || !k_scale || !v_scale)) return KDA_ERR_NULL;
@@ -140,11 +150,7 @@ kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void*
       CacheRopeArgs{CacheAppendArgs{k, v, cu_seqlens, context_len, block_table, static_cast<uint8_t*>(k_cache),
                                     static_cast<uint8_t*>(v_cache), k_scale, v_scale, n, cache ? N : 0, Hkv, d, page, n_pages,
                                     max_pages, in_dtype == KDA_BF16},
-                    k_stride, v_stride,
-                    RopeArgs{turns ? q : nullptr, q_out, q_stride, q_out_stride,
-                             Rotation{positions, inv_freq, axes, n_axes, rot / 2, interleaved != 0}, n, Hq, d, heads, false,
-                             in_dtype == KDA_BF16, q_out_dtype == KDA_BF16},
-                    N, zero_tail != 0},
+                    k_stride, v_stride, queries, N, zero_tail != 0},
       static_cast<hipStream_t>(stream)));
 }
 
