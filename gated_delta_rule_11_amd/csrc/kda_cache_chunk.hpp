@@ -193,6 +193,12 @@ struct ChunkWork {
     return p >= 0 && p < a.pages ? p : -1;
   }
 
+  // Four channels (c0 a multiple of 4) of row rr within a part of a tile of `rows`: as the wide form holds them, its 64
+  // lanes one behind another; row by row in the narrow form.
+  __device__ __forceinline__ static int part_at(int rows, int rr, int c0) {
+    if (rows <= kNarrowRows) return rr * D + c0;
+    return (((rr >> 5) * (D / 8) + (c0 >> 3)) * 64 + (c0 >> 2 & 1) * 32 + (rr & 31)) * 4;
+  }
   __device__ __forceinline__ float* part(int slot) const { return a.part + int64_t(slot) * chunk_part_floats(D); }
 
   __device__ __forceinline__ void wide(const ChunkItem& x, const int* table) {
@@ -200,19 +206,25 @@ struct ChunkWork {
     using TV = Tile<bf16_t, 64>;
     constexpr int NPC = D / 64, NK = D / 16, ND = D / 32;  // pieces of 1 KB of a wavefront; k steps; blocks of channels
     bf16_t* const buf = reinterpret_cast<bf16_t*>(smem);
-    const int h2 = lane >> 5, l32 = lane & 31;
-    const bool alive = 32 * wave < x.rows;
-    const int mine = 32 * wave + l32 < x.rows ? 32 * wave + l32 : 0;  // (rows past the end repeat the first one)
-    const uint32_t r = uint32_t(x.r0 + mine), tok = r / uint32_t(G), hd = r % uint32_t(G);
-    const int qp = x.base + int(tok), qpos = qp < -1 ? -1 : qp;
-    const int64_t row = int64_t(x.s.first) + tok;
-    const int head = x.kvh * G + int(hd);
+    const int h2 = lane >> 5, l32 = lane & 31, w0 = 32 * wave;
+    const bool alive = w0 < x.rows;
+    // A step's pages, group g's in lanes g, g + 4, ...  They come by vector loads, ahead of what they are for: a
+    // scalar load on its way makes every wait for the LDS a wait for it too.
+    auto ask = [&](int t) {
+      const uint32_t tok = uint32_t(t) * 64 + 16 * (lane & 3);
+      return t < x.t1 && tok < uint32_t(x.end) ? table[tok >> ps] : -1;
+    };
+    const int asked0 = ask(x.t0), asked1 = ask(x.t0 + 1);
+    int asked = ask(x.t0 + 2);
+    const uint32_t r = uint32_t(x.r0 + (w0 + l32 < x.rows ? w0 + l32 : 0)), tok = r / uint32_t(G), hd = r % uint32_t(G);
+    const int qp = x.base + int(tok), qpos = qp < -1 ? -1 : qp;  // (rows past the end repeat the first one)
     const int tmin = uniform(x.base + int(uint32_t(x.r0) / uint32_t(G)));  // position of the tile's first row
 
     bf16x8 qf[NK][NP];
+    const T* q = static_cast<const T*>(a.q) + (int64_t(x.s.first) + tok) * a.q_stride + int64_t(x.kvh * G + int(hd)) * D;
 #pragma unroll
     for (int kk = 0; kk < NK; ++kk) {
-      const Parts8 p(load_q(static_cast<const T*>(a.q) + row * a.q_stride + int64_t(head) * D + 16 * kk + 8 * h2, neg));
+      const Parts8 p(load_q(q + 16 * kk + 8 * h2, neg));
 #pragma unroll
       for (int i = 0; i < NP; ++i) qf[kk][i] = part_of(p, i);
     }
@@ -221,13 +233,8 @@ struct ChunkWork {
     for (int i = 0; i < ND; ++i) acc[i] = zero16();
     float ref = -INFINITY, l = 0.f;
 
-    // A step's pages, and which of its four groups of 16 tokens lie in no page (or behind the last token).  They
-    // come by vector loads, a step ahead: a scalar load on its way makes every wait for the LDS a wait for it too.
-    struct Ids { int page, gone; };  // group g's page in lanes g, g + 4, ...
-    auto ask = [&](int t) {
-      const uint32_t tok = uint32_t(t) * 64 + 16 * (lane & 3);
-      return t < x.t1 && tok < uint32_t(x.end) ? table[tok >> ps] : -1;
-    };
+    // Its pages, and which of its four groups of 16 tokens lie in no page (or behind the last token).
+    struct Ids { int page, gone; };
     auto ids_of = [&](int asked) {
       const bool none = asked < 0 || asked >= a.pages;
       return Ids{none ? 0 : asked, int(__ballot(none)) & 15};  // (what is read for no page is not used)
@@ -281,9 +288,7 @@ struct ChunkWork {
     const uint32_t krow = TK::b_row8_32(lane), vrow = TV::b_row8_32(lane);
     const int first_edge = (tmin + 1) >> 6;  // the first step that some row does not see all of
     auto k_of = [&](int t) { return buf + (t & 1) * (2 * 64 * D); };
-    int asked = ask(x.t0), asked2 = ask(x.t0 + 1);
-    Ids one = ids_of(asked), two = ids_of(asked2), three;
-    asked = ask(x.t0 + 2);
+    Ids one = ids_of(asked0), two = ids_of(asked1), three;
     Codes kc, vc;
     if (x.t0 < x.t1) {
       Codes k0, v0;
@@ -388,28 +393,46 @@ struct ChunkWork {
       lds_barrier();
     }
     l = sum_halves(l);
-    if (32 * wave + l32 >= x.rows) return;
+    const bool mine = w0 + l32 < x.rows;
     if (x.slot < 0) {
+      // through the LDS, so that a row's channels leave side by side (every wavefront has left the last step)
+      constexpr int E = 16 / int(sizeof(TO)), RS = D + E, RPI = 64 * E / D;  // rows of one store of the wavefront
+      TO* const rows = reinterpret_cast<TO*>(smem) + wave * 32 * RS;
       const float inv = l == 0.f ? 0.f : 1.0f / l;
-      TO* op = static_cast<TO*>(a.o) + (row * a.Hq + head) * D;
 #pragma unroll
       for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4)
-          store4(op + 32 * i + 8 * r4 + 4 * h2,
+          store4(rows + l32 * RS + 32 * i + 8 * r4 + 4 * h2,
                  f32x4{acc[i][4 * r4] * inv, acc[i][4 * r4 + 1] * inv, acc[i][4 * r4 + 2] * inv, acc[i][4 * r4 + 3] * inv});
-      if (a.lse && h2 == 0) a.lse[row * a.Hq + head] = (ref + log2f(l)) * 0.6931471805599453f;
+      if (a.lse && h2 == 0 && mine) a.lse[(int64_t(x.s.first) + tok) * a.Hq + x.kvh * G + int(hd)] = (ref + log2f(l)) * 0.6931471805599453f;
+      __builtin_amdgcn_wave_barrier();
+      int rr = lane / (D / E), at = int(uint32_t(x.r0 + w0 + rr) / uint32_t(G)), h = x.r0 + w0 + rr - at * G;
+      const int c0 = lane % (D / E) * E, tokens = RPI / G, heads = RPI % G;
+#pragma unroll
+      for (int i = 0; i < 32 / RPI; ++i) {
+        if (w0 + rr < x.rows)
+          *reinterpret_cast<u32x4*>(static_cast<TO*>(a.o) + ((int64_t(x.s.first) + at) * a.Hq + x.kvh * G + h) * D + c0) =
+              *reinterpret_cast<const u32x4*>(rows + rr * RS + c0);
+        rr += RPI;
+        at += tokens;
+        h += heads;
+        if (h >= G) {
+          h -= G;
+          ++at;
+        }
+      }
     } else {
       float* pp = part(x.slot);
 #pragma unroll
       for (int i = 0; i < ND; ++i)
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4)
-          store4(pp + mine * D + 32 * i + 8 * r4 + 4 * h2,
+          store4(pp + ((wave * (D / 8) + 4 * i + r4) * 64 + lane) * 4,
                  f32x4{acc[i][4 * r4], acc[i][4 * r4 + 1], acc[i][4 * r4 + 2], acc[i][4 * r4 + 3]});
-      if (h2 == 0) {
-        pp[kChunkRows * D + 2 * mine] = ref;
-        pp[kChunkRows * D + 2 * mine + 1] = l;
+      if (h2 == 0 && mine) {
+        pp[kChunkRows * D + 2 * (w0 + l32)] = ref;
+        pp[kChunkRows * D + 2 * (w0 + l32) + 1] = l;
       }
     }
   }
@@ -422,27 +445,6 @@ struct ChunkWork {
     // queries of 32 rows, and the parts of fp32 ones, in LDS: in registers they would push out the next step
     constexpr bool QL = NP == 3 || NC == 2;
     bf16x8(*const qs)[64] = reinterpret_cast<bf16x8(*)[64]>(smem);  // [NC][NM][2][NP]
-    int qpos[NC];
-    bf16x8 qf[NC][NM][2];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      const bool live = 16 * n + r16 < x.rows;
-      const uint32_t r = uint32_t(x.r0 + (live ? 16 * n + r16 : 0)), tok = r / uint32_t(G), hd = r % uint32_t(G);
-      const int qp = x.base + int(tok);
-      qpos[n] = qp < -1 ? -1 : qp;
-      const T* q = static_cast<const T*>(a.q) + (int64_t(x.s.first) + tok) * a.q_stride + int64_t(x.kvh * G + int(hd)) * D;
-#pragma unroll
-      for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const Parts8 p(load_q(q + 16 * (g4 + 4 * m) + 8 * e, neg));
-          if constexpr (!QL) qf[n][m][e] = part_of(p, 0);
-          else if (wave == 0)
-#pragma unroll
-            for (int i = 0; i < NP; ++i) qs[((n * NM + m) * 2 + e) * NP + i][lane] = part_of(p, i);
-        }
-    }
-    if constexpr (QL) lds_barrier();
     const int tmin = uniform(x.base + int(uint32_t(x.r0) / uint32_t(G)));
 
     u32x4 kr[4][NM], vr[ND];
@@ -483,12 +485,35 @@ struct ChunkWork {
 #pragma unroll
       for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0, 0, 0, 0};
     }
+    // (the first step is on its way before the queries are waited for)
     int t = x.t0 + wave;
+    const int pk = k_page(t);
     int pv = v_page(t), pk1 = k_page(t + 4), pv1 = v_page(t + 4);
     if (t < x.t1) {
-      load_k(k_page(t));
+      load_k(pk);
       load_v(pv);
     }
+    int qpos[NC];
+    bf16x8 qf[NC][NM][2];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const bool live = 16 * n + r16 < x.rows;
+      const uint32_t r = uint32_t(x.r0 + (live ? 16 * n + r16 : 0)), tok = r / uint32_t(G), hd = r % uint32_t(G);
+      const int qp = x.base + int(tok);
+      qpos[n] = qp < -1 ? -1 : qp;
+      const T* q = static_cast<const T*>(a.q) + (int64_t(x.s.first) + tok) * a.q_stride + int64_t(x.kvh * G + int(hd)) * D;
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Parts8 p(load_q(q + 16 * (g4 + 4 * m) + 8 * e, neg));
+          if constexpr (!QL) qf[n][m][e] = part_of(p, 0);
+          else if (wave == 0)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) qs[((n * NM + m) * 2 + e) * NP + i][lane] = part_of(p, i);
+        }
+    }
+    if constexpr (QL) lds_barrier();
     for (; t < x.t1; t += 4) {
       f32x4 s[NC][4];
 #pragma unroll
@@ -626,7 +651,7 @@ struct ChunkWork {
         if (a.lse && c0 == 0) a.lse[row] = (m + log2f(ls)) * 0.6931471805599453f;
       } else {
         float* pp = part(x.slot);
-        store4(pp + rr * D + c0, y);
+        store4(pp + part_at(x.rows, rr, c0), y);
         if (c0 == 0) {
           pp[kChunkRows * D + 2 * rr] = m;
           pp[kChunkRows * D + 2 * rr + 1] = ls;
@@ -658,7 +683,7 @@ struct ChunkWork {
       if (x.slot < 0)
         io<TO>::store(static_cast<TO*>(a.o), ((int64_t(x.s.first) + tok) * a.Hq + x.kvh * G + int(r % uint32_t(G))) * D + d, y);
       else
-        part(x.slot)[e] = y;
+        part(x.slot)[part_at(x.rows, rr, d & ~3) + (d & 3)] = y;
     }
   }
 
@@ -849,6 +874,7 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
   const int per = 1 << lg, row0 = int(blockIdx.y) << lg, r = row0 + (g & (per - 1));
   if (row0 >= p.rows) return;
   const bool live = r < p.rows;
+  const int at = ChunkWork<TO, TO, D>::part_at(p.rows, r, 4 * e);
   auto part = [&](int i) { return a.part + int64_t(i == 0 ? 2 * w + 1 : 2 * (w + i)) * chunk_part_floats(D); };
   auto write = [&](f32x4 y, float l, float m) {
     const uint32_t rr = uint32_t(p.r0 + r);
@@ -866,7 +892,7 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
 #pragma unroll
     for (int i = 0; i < kJoinFew; ++i) {
       const float* pp = part(i < n ? i : 0);
-      y[i] = *reinterpret_cast<const f32x4*>(pp + r * D + 4 * e);
+      y[i] = *reinterpret_cast<const f32x4*>(pp + at);
       ml[i] = *reinterpret_cast<const f32x2*>(pp + kChunkRows * D + 2 * r);
     }
     float m = ml[0][0];
@@ -908,7 +934,7 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
       const float* pp = part(i);
       const float f = fast_exp2(pp[kChunkRows * D + 2 * r] - from);
       l += f * pp[kChunkRows * D + 2 * r + 1];
-      y += *reinterpret_cast<const f32x4*>(pp + r * D + 4 * e) * f;
+      y += *reinterpret_cast<const f32x4*>(pp + at) * f;
     }
   sy[g][e] = y;
   if (e == 0) sl[g] = l;
