@@ -259,8 +259,10 @@ struct ChunkWork {
         *reinterpret_cast<bf16x8*>(K + TK::off(kw, ch + 8)) = codes(k.w[i][2], k.w[i][3], k.scale[i]);
       }
     };
-    // The values of a step that some row does not see all of.
+    const int first_edge = (tmin + 1) >> 6;  // the first step that some row does not see all of
+    // The values of a step that some row does not see all of, or with tokens in no page.
     auto clean_v = [&](Codes& v, int t, const Ids& z) {
+      if (t < first_edge && z.gone == 0) return;
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
         const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
@@ -272,8 +274,8 @@ struct ChunkWork {
           v.w[i][w] &= nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
         }
         // A masked probability is zero, but zero times a NaN is not: where a step is masked for some rows such
-        // values leave the product, and the rows that see them are set at the end.
-        if (finite_codes(v.w[i], v.scale[i])) *bad = 1;
+        // values leave the product, and the rows that see them are set at the end (set_bad, from this step on).
+        if (t >= first_edge && finite_codes(v.w[i], v.scale[i])) *bad = 1;
       }
     };
     auto put_v = [&](bf16_t* V, const Codes& v) {
@@ -286,7 +288,6 @@ struct ChunkWork {
       }
     };
     const uint32_t krow = TK::b_row8_32(lane), vrow = TV::b_row8_32(lane);
-    const int first_edge = (tmin + 1) >> 6;  // the first step that some row does not see all of
     auto k_of = [&](int t) { return buf + (t & 1) * (2 * 64 * D); };
     Ids one = ids_of(asked0), two = ids_of(asked1), three;
     Codes kc, vc;
@@ -297,7 +298,7 @@ struct ChunkWork {
       fetch(kc, a.kc, a.ks, two);
       fetch(vc, a.vc, a.vs, two);
       put_k(k_of(x.t0), k0);
-      if (x.t0 >= first_edge || one.gone != 0) clean_v(v0, x.t0, one);
+      clean_v(v0, x.t0, one);
       put_v(k_of(x.t0) + 64 * D, v0);
     }
     lds_barrier();
@@ -331,7 +332,7 @@ struct ChunkWork {
           for (int i = NP - 1; i >= 0; --i) s[j] = O::mma32(kf, qf[kk][i], s[j]);
         }
       if (t + 1 < x.t1) {
-        if (t + 1 >= first_edge || two.gone != 0) clean_v(vc, t + 1, two);
+        clean_v(vc, t + 1, two);
         put_k(k_of(t + 1), kc);
         put_v(k_of(t + 1) + 64 * D, vc);
       }
@@ -339,7 +340,6 @@ struct ChunkWork {
       bf16x8 vf[2][ND];
 #pragma unroll
       for (int i = 0; i < ND; ++i) vf[0][i] = TV::row8_32(vb, i, 0);
-      
       if (t + 2 < x.t1) {
         fetch(kc, a.kc, a.ks, three);
         fetch(vc, a.vc, a.vs, three);
@@ -386,7 +386,6 @@ struct ChunkWork {
 #pragma unroll
           for (int k = NP - 1; k >= 0; --k) acc[i] = O::mma32(vf[u & 1][i], part_of(pf, k), acc[i]);
       }
-      
       __builtin_amdgcn_s_setprio(0);
       one = two;
       two = three;

@@ -167,6 +167,69 @@ def test_nan_and_infinity_reach_the_rows_that_see_them(width, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P,d", [(16, 64), (64, 128)])
+def test_nan_among_values_that_every_row_sees(P, d, dtype):
+    """In the first steps of a long context, for every number of a tile's rows, also beside tokens that lie in no page."""
+    for width in (None, 70 * 64 // P):
+        for new in (1, 9, 20, 40, 70, 128):  # two heads of a group: up to 128 rows to a tile, whole tiles behind it
+            ctx = [new + 200]
+            c, t = filled(ctx, 1, P, d, **({} if width is None else {"width": width}))
+            q = torch.randn(new, 2, d).to(dtype)
+            for gone in (None, 0 if P == 64 else 2):
+                if gone is not None:
+                    t[0][gone] = -1
+                clean = run(c, t, q, [new], ctx)
+                code = c["vc"].view(torch.uint8)
+                at = [1, 70, 130, 199] if gone is None else [65, 70, 199]
+                kept = [code[t[0][x // P], 0, 5 + i, x % P].item() for i, x in enumerate(at)]
+                for i, x in enumerate(at):
+                    code[t[0][x // P], 0, 5 + i, x % P] = 0x7F
+                got = run(c, t, q, [new], ctx)
+                torch.cuda.synchronize()
+                for i, x in enumerate(at):
+                    assert bool(got[0][..., 5 + i].isnan().all()), (width, new, gone, x)
+                    code[t[0][x // P], 0, 5 + i, x % P] = kept[i]
+                got[0][..., 5:5 + len(at)] = clean[0][..., 5:5 + len(at)]
+                assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+                if gone == 2:  # the missing page's neighbours in its step
+                    code[t[0][1], 0, 9, 3] = 0x7F
+                    got = run(c, t, q, [new], ctx)
+                    torch.cuda.synchronize()
+                    assert bool(got[0][..., 9].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_cache_beyond_32_bits_of_offsets(dtype):
+    """The last pages of a cache of more than 4 GiB a side give what the first pages of a small one give."""
+    new, ctx, P, d = [40, 3], [700, 50], 64, 128
+    c, t = filled(ctx, 1, P, d)
+    pages = c["kc"].shape[0]
+    far = 2 ** 32 // (P * d) + 5
+    big = {x: torch.zeros((far + pages, *c[x].shape[1:]), dtype=torch.uint8 if x[1] == "c" else F32, device=DEV) for x in c}
+    for x in c:
+        big[x][far:] = c[x].view(big[x].dtype)
+        big[x] = big[x].view(c[x].dtype)
+    q = torch.randn(43, 4, d).to(dtype)
+    want = run(c, t, q, new, ctx)
+    got = run(big, [[p + far for p in x] for x in t], q, new, ctx)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_workspace_of_any_contents():
+    """Words of one, which would mark every part as one that goes on, and words of a large number."""
+    new, ctx = [5, 150, 1], [3000, 700, 90]
+    c, t = filled(ctx, 2, 16, 64)
+    q = torch.randn(156, 4, 64).to(BF)
+    want = run(c, t, q, new, ctx)
+    for word in (1, 2, 0x7F7F7F7F, -1):
+        ws = torch.full((kda.attn_chunk_fwd_workspace_bytes(156, 3, 4, 2, 64, 16, len(t[0]), BF) // 4,), word, dtype=torch.int32, device=DEV)
+        got = run(c, t, q, new, ctx, workspace=ws.view(torch.uint8))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_largest_values(dtype):
     """Values near the end of fp32 and probabilities summed without overflow on the way."""
     new, ctx = [4, 50], [600, 90]

@@ -163,6 +163,26 @@ def test_many_sequences():
     mx.close("q", got, want, mag, BF, 1.0, 3.0)
 
 
+def test_a_cache_beyond_32_bits_of_offsets():
+    """The last pages of a cache of more than 4 GiB a side, by both forms."""
+    gen = torch.Generator().manual_seed(11)
+    P, d, inv = 64, 128, sv.frequencies(64).to(DEV)
+    far = 2 ** 32 // (P * d) + 5
+    big = {x: torch.zeros(far + 6, 1, *s, dtype=t, device=DEV) for x, s, t in (("kc", (P, d), torch.uint8), ("vc", (d, P), torch.uint8), ("ks", (), F32), ("vs", (), F32))}
+    for new, held in (([3, 1], [70, 0]), ([150, 90], [5, 60])):
+        c = cache(6, 1, P, d)
+        for x in c:
+            big[x][far:] = c[x].view(big[x].dtype)
+        at = {x: y.view(c[x].dtype) for x, y in big.items()}
+        table = [[0, 3, 1], [5, 2, 4]]
+        k, v = (tokens(gen, sum(new), 1, d, BF).to(DEV) for _ in range(2))
+        append(c, k, v, ends(new), held, table, inv)
+        append(at, k, v, ends(new), held, [[p + far for p in x] for x in table], inv)
+        torch.cuda.synchronize()
+        for x in c:
+            assert torch.equal(big[x][far:], c[x].view(big[x].dtype)), x
+
+
 def test_special_values():
     """Infinities and NaN among the turned channels do not enter the scale; the largest values overflow to it."""
     inv, pos = sv.frequencies(32), torch.zeros(4, dtype=torch.int32)
