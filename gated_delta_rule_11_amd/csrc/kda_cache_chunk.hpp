@@ -268,6 +268,7 @@ struct ChunkWork {
         const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
         const int vt = ((at / (P * D)) << ps) + (o & (P - 1));
         const int left = z.gone >> (vt >> 4) & 1 ? 0 : x.end - t * 64 - vt;
+        if (left <= 0) v.scale[i] = 1.f;  // (a zero by the scale of a page that is none could be NaN)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {  // what lies behind the last token may be anything, NaN too
           const int nb = int(left < 0 ? 0 : (left > 16 ? 16 : left)) - 4 * w;

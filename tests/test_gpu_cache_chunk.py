@@ -167,6 +167,33 @@ def test_nan_and_infinity_reach_the_rows_that_see_them(width, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P,d", [(16, 64), (32, 128), (64, 128)])
+def test_scales_of_pages_not_in_use_do_not_matter(P, d, dtype):
+    """Page 0 among them, NaN and infinite: with lengths that end inside a step, and with pages left out."""
+    new, ctx = [3, 40, 90, 20], [70, 90, 150, 700]
+    for width in (None, 70 * 64 // P):
+        c, t = filled(ctx, 1, P, d, **({} if width is None else {"width": width}))
+        held = [t[i][:-(-x // P)] for i, x in enumerate(ctx)]
+        free = min(set(range(c["kc"].shape[0])) - {p for x in held for p in x})
+        swap = {0: free, free: 0}
+        for x in c:
+            both = c[x].view(torch.uint8) if x[1] == "c" else c[x]
+            both[[0, free]] = both[[free, 0]]
+        t = [[swap.get(p, p) for p in held[i]] + [0] * (len(t[i]) - len(held[i])) for i in range(4)]
+        t[1][0] = t[2][1] = t[3][-1] = -1
+        q = torch.randn(sum(new), 2, d).to(dtype)
+        want = run(c, t, q, new, ctx)
+        compare("before", want, c, t, q, new, ctx)
+        unused = sorted(set(range(c["kc"].shape[0])) - {p for i, x in enumerate(ctx) for p in t[i][:-(-x // P)]})
+        assert 0 in unused
+        for word in (math.nan, math.inf, -math.inf):
+            c["ks"][unused], c["vs"][unused] = word, word
+            got = run(c, t, q, new, ctx)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("P,d", [(16, 64), (64, 128)])
 def test_nan_among_values_that_every_row_sees(P, d, dtype):
     """In the first steps of a long context, for every number of a tile's rows, also beside tokens that lie in no page."""
