@@ -34,8 +34,7 @@ __device__ __forceinline__ u32x2v encode8(const f32x8& x, float inv) {
   return w;
 }
 
-// A unit of k turned in 64 bits, its 16 channels in `own`, a column of the thread's own in LDS: with the channels in
-// registers the eight pairs would have to be written out, and their terms held at once (160 registers against 90).
+// A unit of k turned in 64 bits, its 16 channels in `own`, a column of the thread's own in LDS (for append_few).
 constexpr int kColumns = 256;
 __device__ __forceinline__ void turn_unit(const Rotation& t, int64_t row, int64_t place, int u, float* own, float& most) {
 #pragma unroll 2
@@ -117,15 +116,76 @@ __device__ __forceinline__ bool page_work(const CacheAppendArgs& a, int slot, in
   return true;
 }
 
-// One workgroup for a page and key head: all of its rows at once in registers.
-template <typename T, int D>
-__device__ __forceinline__ void append_page(const CacheRopeArgs& ra, int id, uint8_t* lds, float* red) {
+// A turned bf16 key stays in bf16, rounded to odd: eight bits so rounded give the same codes (of four, or fewer) as all.
+__device__ __forceinline__ uint32_t odd_bf16(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u >> 16) | (u & 0xffffu ? 1u : 0u);
+}
+// elements 2 w and 2 w + 1 of a fragment, read and written by whole registers
+__device__ __forceinline__ f32x2 two(const bf16x8& x, int w) {
+  const uint32_t u = __builtin_bit_cast(u32x4, x)[w];
+  return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x2 two(const f32x8& x, int w) { return f32x2{x[2 * w], x[2 * w + 1]}; }
+__device__ __forceinline__ void put_two(bf16x8& x, int w, float a, float b) {
+  u32x4 u = __builtin_bit_cast(u32x4, x);
+  u[w] = odd_bf16(a) | odd_bf16(b) << 16;
+  x = __builtin_bit_cast(bf16x8, u);
+}
+__device__ __forceinline__ void put_two(f32x8& x, int w, float a, float b) {
+  x[2 * w] = a;
+  x[2 * w + 1] = b;
+}
+// A unit of HB heads' k turned in 64 bits in place: the sines are formed once for all heads.
+template <typename T, int HB>
+__device__ __forceinline__ void turn_units(const Rotation& t, int64_t row, int64_t place, int u, typename Op<T>::frag (*k)[2], float* most) {
+  if (t.interleaved)
+#pragma unroll
+    for (int b = 0; b < HB; ++b) {
+      const auto even = __builtin_shufflevector(k[b][0], k[b][1], 0, 2, 4, 6, 8, 10, 12, 14);
+      k[b][1] = __builtin_shufflevector(k[b][0], k[b][1], 1, 3, 5, 7, 9, 11, 13, 15);
+      k[b][0] = even;
+    }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    double s[2], c[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) sine_cosine(angle_of(t, row, place, pair_of(u, 2 * w + e, t.half, t.interleaved)), s[e], c[e]);
+#pragma unroll
+    for (int b = 0; b < HB; ++b) {
+      const f32x2 x = two(k[b][0], w), y = two(k[b][1], w);
+      float f[2], g[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const double p = x[e], q = y[e];
+        f[e] = to_fp32(mul_add(p, c[e], -q * s[e]));
+        g[e] = to_fp32(mul_add(q, c[e], p * s[e]));
+        const float af = fabsf(f[e]), ag = fabsf(g[e]);
+        most[b] = af < INFINITY && af > most[b] ? af : most[b];
+        most[b] = ag < INFINITY && ag > most[b] ? ag : most[b];
+      }
+      put_two(k[b][0], w, f[0], f[1]);
+      put_two(k[b][1], w, g[0], g[1]);
+      __builtin_amdgcn_sched_barrier(0);  // the terms of two pairs at a time: all of them would not fit the registers
+    }
+  }
+  if (t.interleaved)
+#pragma unroll
+    for (int b = 0; b < HB; ++b) {
+      const auto low = __builtin_shufflevector(k[b][0], k[b][1], 0, 8, 1, 9, 2, 10, 3, 11);
+      k[b][1] = __builtin_shufflevector(k[b][0], k[b][1], 4, 12, 5, 13, 6, 14, 7, 15);
+      k[b][0] = low;
+    }
+}
+
+// One workgroup for a page and HB key heads, a thread for each unit of its rows' keys: all at once in registers.
+template <typename T, int D, int HB>
+__device__ __forceinline__ void append_page(const CacheRopeArgs& ra, int id, uint8_t* image, float* red) {
   const CacheAppendArgs& a = ra.c;
   const Rotation& t = ra.q.turn;
-  constexpr int CPR = D / 8, NV = 64 * CPR / 256;  // 8-element chunks of a row; chunks of a thread
-  constexpr int UPR = D / 16, NK = 64 * UPR / 256;  // units of two chunks, of a row and of a thread
-  const int tid = threadIdx.x, P = a.page;
-  const int h = id % a.Hkv, slot = id / a.Hkv;
+  constexpr int CPR = D / 8, UPR = D / 16, NT = 64 * UPR;  // chunks of 8 channels, units of two, of a row; threads
+  const int tid = threadIdx.x, P = a.page, sets = a.Hkv / HB;
+  const int h = id % sets * HB, slot = id / sets;
 
   int page;
   PageWork w;
@@ -133,97 +193,102 @@ __device__ __forceinline__ void append_page(const CacheRopeArgs& ra, int id, uin
   if (page < 0 || page >= a.pages) return;
   const int off = w.off, cnt = w.cnt;
   const int64_t row0 = w.row0, p0 = w.p0, ph = int64_t(page) * a.Hkv + h;
-  const float old_k = a.ks[ph], old_v = a.vs[ph];
+  float old_k[HB], old_v[HB];
+#pragma unroll
+  for (int b = 0; b < HB; ++b) {
+    old_k[b] = a.ks[ph + b];
+    old_v[b] = a.vs[ph + b];
+  }
 
   typedef typename Op<T>::frag F;
-  F kr[NK][2], vr[NV];
+  F kr[HB][2], vr[HB][2];
+  const int row = tid / UPR, u = tid % UPR;
+  const Unit un = unit_of(u, t.half);
+  const T* src = static_cast<const T*>(a.k) + (row0 + row) * ra.k_stride + h * D;
 #pragma unroll
-  for (int i = 0; i < NK; ++i) {
-    const int e = tid + 256 * i, r = e / UPR;
-    const Unit w = unit_of(e % UPR, t.half);
-    const T* src = static_cast<const T*>(a.k) + (row0 + r) * ra.k_stride + h * D;
-    kr[i][0] = kr[i][1] = F{};
-    if (r < cnt) {
-      kr[i][0] = Op<T>::load(src + 8 * w.c0);
-      kr[i][1] = Op<T>::load(src + 8 * w.c1);
+  for (int b = 0; b < HB; ++b) {
+    kr[b][0] = kr[b][1] = F{};
+    if (row < cnt) {
+      kr[b][0] = Op<T>::load(src + b * D + 8 * un.c0);
+      kr[b][1] = Op<T>::load(src + b * D + 8 * un.c1);
     }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = tid + 256 * i, r = e / CPR, c = e % CPR;
-    vr[i] = F{};
-    if (r < cnt) vr[i] = Op<T>::load(static_cast<const T*>(a.v) + (row0 + r) * ra.v_stride + h * D + 8 * c);
-  }
-  // The turned keys wait in LDS for the scale.
-  float* const own = reinterpret_cast<float*>(lds) + tid;
-  float mk = 0.f, mv = 0.f;
+  for (int i = 0; i < 2; ++i) {
+    const int e = tid + NT * i, r = e / CPR, c = e % CPR;
 #pragma unroll
-  for (int i = 0; i < NK; ++i) {
-    const int e = tid + 256 * i, r = e / UPR, u = e % UPR;
-    const f32x8 x0 = Op<T>::unpack(kr[i][0]), x1 = Op<T>::unpack(kr[i][1]);
-    if (r < cnt) {
-      to_column(own + 16 * i * kColumns, x0, x1);
-      if (unit_of(u, t.half).turns) {
-        turn_unit(t, row0 + r, p0 + r, u, own + 16 * i * kColumns, mk);
-      } else {
-        see(mk, x0);
-        see(mk, x1);
-      }
+    for (int b = 0; b < HB; ++b) {
+      vr[b][i] = F{};
+      if (r < cnt) vr[b][i] = Op<T>::load(static_cast<const T*>(a.v) + (row0 + r) * ra.v_stride + (h + b) * D + 8 * c);
     }
   }
+  float mk[HB] = {}, mv[HB] = {};
+  if (row < cnt && un.turns)
+    turn_units<T, HB>(t, row0 + row, p0 + row, u, kr, mk);
+  else
 #pragma unroll
-  for (int i = 0; i < NV; ++i) see(mv, Op<T>::unpack(vr[i]));
+    for (int b = 0; b < HB; ++b) {
+      see(mk[b], Op<T>::unpack(kr[b][0]));
+      see(mk[b], Op<T>::unpack(kr[b][1]));
+    }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    mk = fmaxf(mk, __shfl_xor(mk, d));
-    mv = fmaxf(mv, __shfl_xor(mv, d));
-  }
-  if ((tid & 63) == 0) {
-    red[tid >> 6] = mk;
-    red[4 + (tid >> 6)] = mv;
+  for (int b = 0; b < HB; ++b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) see(mv[b], Op<T>::unpack(vr[b][i]));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      mk[b] = fmaxf(mk[b], __shfl_xor(mk[b], d));
+      mv[b] = fmaxf(mv[b], __shfl_xor(mv[b], d));
+    }
+    if ((tid & 63) == 0) {
+      red[2 * b * UPR + (tid >> 6)] = mk[b];
+      red[(2 * b + 1) * UPR + (tid >> 6)] = mv[b];
+    }
   }
   __syncthreads();  // every thread has read the scales
-  float sk = scale_for(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-  float sv = scale_for(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
-  if (off > 0) {
-    sk = fmaxf(sk, old_k);
-    sv = fmaxf(sv, old_v);
-  }
-  if (tid == 0) {
-    a.ks[ph] = sk;
-    a.vs[ph] = sv;
-  }
-  const float ik = inverse_pow2(sk), iv = inverse_pow2(sv);
-  uint8_t* kc = a.kc + ph * P * D;
 #pragma unroll
-  for (int i = 0; i < NK; ++i) {
-    const int e = tid + 256 * i, r = e / UPR;
-    const Unit w = unit_of(e % UPR, t.half);
-    if (r < cnt) {
-      *reinterpret_cast<u32x2v*>(kc + (off + r) * D + 8 * w.c0) = encode8(from_column(own + 16 * i * kColumns), ik);
-      *reinterpret_cast<u32x2v*>(kc + (off + r) * D + 8 * w.c1) = encode8(from_column(own + (16 * i + 8) * kColumns), ik);
-    }
-  }
-  lds_barrier();  // the keys are out of the LDS
-  uint8_t* const image = lds;  // new V codes, [d][P + 4]
+  for (int b = 0; b < HB; ++b) {
+    const float* m = red + 2 * b * UPR;  // (a wavefront for every unit of a row)
+    float most_k = m[0], most_v = m[UPR];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = tid + 256 * i, r = e / CPR, c = e % CPR;
-    if (r < cnt) {
-      const u32x2v w = encode8(Op<T>::unpack(vr[i]), iv);
+    for (int i = 1; i < UPR; ++i) {
+      most_k = fmaxf(most_k, m[i]);
+      most_v = fmaxf(most_v, m[UPR + i]);
+    }
+    float sk = scale_for(most_k), sv = scale_for(most_v);
+    if (off > 0) {
+      sk = fmaxf(sk, old_k[b]);
+      sv = fmaxf(sv, old_v[b]);
+    }
+    if (tid == 0) {
+      a.ks[ph + b] = sk;
+      a.vs[ph + b] = sv;
+    }
+    const float ik = inverse_pow2(sk), iv = inverse_pow2(sv);
+    uint8_t *kc = a.kc + (ph + b) * P * D, *im = image + b * D * (64 + 4);  // im: new V codes, [d][P + 4]
+    if (row < cnt) {
+      *reinterpret_cast<u32x2v*>(kc + (off + row) * D + 8 * un.c0) = encode8(Op<T>::unpack(kr[b][0]), ik);
+      *reinterpret_cast<u32x2v*>(kc + (off + row) * D + 8 * un.c1) = encode8(Op<T>::unpack(kr[b][1]), ik);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) image[(8 * c + j) * (P + 4) + off + r] = uint8_t(w[j / 4] >> (8 * (j % 4)));
+    for (int i = 0; i < 2; ++i) {
+      const int e = tid + NT * i, r = e / CPR, c = e % CPR;
+      if (r < cnt) {
+        const u32x2v w = encode8(Op<T>::unpack(vr[b][i]), iv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) im[(8 * c + j) * (P + 4) + off + r] = uint8_t(w[j / 4] >> (8 * (j % 4)));
+      }
     }
-  }
-  if (off > 0 && sk > old_k) {
-    const float f = old_k * ik;
-    for (int e = tid; e < off * D / 4; e += 256) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(kc) + e;
-      *p = recode4(*p, f);
+    if (off > 0 && sk > old_k[b]) {
+      const float f = old_k[b] * ik;
+      for (int e = tid; e < off * D / 4; e += NT) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(kc) + e;
+        *p = recode4(*p, f);
+      }
     }
+    lds_barrier();
+    store_v_image<D, NT>(a.vc + (ph + b) * P * D, im, P, off, cnt, off > 0 && sv > old_v[b], old_v[b] * iv, tid);
   }
-  __syncthreads();
-  store_v_image<D>(a.vc + ph * P * D, image, P, off, cnt, off > 0 && sv > old_v, old_v * iv, tid);
 }
 
 // One wavefront for a page and key head, rows in passes of 64 / (D / 16): the form for few tokens to a page, where
@@ -324,23 +389,26 @@ __device__ __forceinline__ void append_few(const CacheRopeArgs& ra, int64_t item
   }
 }
 
-// FEW: append_few, four (page, head) pairs to a workgroup; else one.  The queries' workgroups follow the pages': the two
-// kinds in turn took 100 us where this order takes 85 (14300 tokens, 32 and 8 heads of 128).
-template <typename T, typename TO, int D, bool FEW>
-__global__ __launch_bounds__(256) void cache_append_rope_kernel(const CacheRopeArgs a, int pages) {
-  __shared__ __align__(16) uint8_t lds[FEW ? 16 * kColumns * 4 : 64 * D * 4];  // (also four rows' sines)
-  __shared__ float red[8];
+// FORM 0: append_few, four (page, head) pairs to a workgroup; else append_page with FORM heads.  The queries' workgroups
+// follow the pages': the two kinds in turn took 100 us where this order took 85 (14300 tokens, 32 and 8 heads of 128).
+template <int D, int FORM> constexpr int kThreads = FORM == 0 ? 256 : 4 * D;
+template <typename T, typename TO, int D, int FORM>
+__global__ __launch_bounds__((kThreads<D, FORM>), (FORM == 0 ? 1 : 4)) void cache_append_rope_kernel(const CacheRopeArgs a, int pages) {
+  constexpr int NW = kThreads<D, FORM> / 64, kRows = NW * 2 * kSines * 4, kImages = FORM * D * (64 + 4);  // rows' sines; V's codes
+  static_assert(16 * kColumns * 4 <= kRows, "a wavefront's unit of keys");
+  __shared__ __align__(16) uint8_t lds[kImages > kRows ? kImages : kRows];
+  __shared__ float red[FORM == 0 ? 1 : 2 * FORM * NW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), id = int(blockIdx.x);
   if (id < pages) {
-    if constexpr (FEW) {
+    if constexpr (FORM == 0) {
       const int64_t item = int64_t(id) * 4 + wave;
       if (item < (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv) append_few<T, D>(a, item, lane, reinterpret_cast<float*>(lds) + threadIdx.x);
     } else {
-      append_page<T, D>(a, id, lds, red);
+      append_page<T, D, FORM>(a, id, lds, red);
     }
     return;
   }
-  const int64_t item = (int64_t(id) - pages) * 4 + wave;
+  const int64_t item = (int64_t(id) - pages) * NW + wave;
   const int parts = (a.q.H + a.q.heads - 1) / a.q.heads, h0 = int(item % parts) * a.q.heads;
   const int64_t row = item / parts;
   if (row >= a.q.n) return;
@@ -361,21 +429,30 @@ __global__ __launch_bounds__(256) void cache_append_rope_kernel(const CacheRopeA
   rotate_rows<T, TO>(a.q, row, place, h0, reinterpret_cast<float(*)[kSines]>(lds) + 2 * wave, lane);
 }
 
-template <typename T, typename TO, int D, bool FEW>
+template <typename T, typename TO, int D, int FORM>
 hipError_t launch(const CacheRopeArgs& a, hipStream_t st) {
+  constexpr int NT = kThreads<D, FORM>, NW = NT / 64;
   const int64_t pairs = a.c.N > 0 ? (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv : 0;
-  const int64_t pages = FEW ? (pairs + 3) / 4 : pairs;
+  const int64_t pages = FORM == 0 ? (pairs + 3) / 4 : pairs / (FORM == 0 ? 1 : FORM);
   const int64_t items = a.q.x ? rope_items(a.q) : 0;
-  cache_append_rope_kernel<T, TO, D, FEW><<<dim3(uint32_t(pages + (items + 3) / 4)), 256, 0, st>>>(a, int(pages));
+  cache_append_rope_kernel<T, TO, D, FORM><<<dim3(uint32_t(pages + (items + NW - 1) / NW)), NT, 0, st>>>(a, int(pages));
   return hipGetLastError();
+}
+
+template <typename T, typename TO, int D>
+hipError_t launch_form(const CacheRopeArgs& a, hipStream_t st) {
+  // Few tokens to a sequence, and so to a page: 16 rows are two passes (d = 128) of one wavefront.
+  if (int64_t(a.c.n) <= 16 * int64_t(a.c.N)) return launch<T, TO, D, 0>(a, st);
+  // Two heads that share the sines, where that leaves every compute unit three workgroups: 14300 tokens of 8 heads of 128
+  // with 32 of queries take 78 us so and 80 by single heads, 2400 tokens of 64 sequences 25.3 and 24.5.
+  const int64_t pairs = (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv;
+  if (a.c.Hkv % 2 == 0 && pairs >= 2 * 768) return launch<T, TO, D, 2>(a, st);
+  return launch<T, TO, D, 1>(a, st);
 }
 
 template <typename T, typename TO>
 hipError_t launch_d(const CacheRopeArgs& a, hipStream_t st) {
-  // few tokens to a sequence, and so to a page: 16 rows are two passes (d = 128) of one wavefront
-  const bool few = int64_t(a.c.n) <= 16 * int64_t(a.c.N);
-  if (a.c.d == 64) return few ? launch<T, TO, 64, true>(a, st) : launch<T, TO, 64, false>(a, st);
-  return few ? launch<T, TO, 128, true>(a, st) : launch<T, TO, 128, false>(a, st);
+  return a.c.d == 64 ? launch_form<T, TO, 64>(a, st) : launch_form<T, TO, 128>(a, st);
 }
 
 }  // namespace

@@ -54,6 +54,20 @@ def test_codes_scales_and_queries(d, rot, interleaved, A, P, dtype):
         mx.close("q", got, want, mag, dtype, 1.0, 3.0)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,rot,interleaved,Hkv", [(64, 64, False, 8), (64, 32, True, 4), (128, 128, True, 8), (128, 96, False, 7)])
+def test_so_many_pages_that_heads_share_the_sines(d, rot, interleaved, Hkv, dtype):
+    gen = torch.Generator().manual_seed(d + rot)
+    P, new, held = 16, [3000, 1, 0, 3300], [5, 16, 3, 0]
+    c = cache(500, Hkv, P, d)
+    ref = mx.Cache(c["kc"], c["vc"], c["ks"], c["vs"])
+    table, cu, inv = table_of([a + b for a, b in zip(new, held)], P, 500), ends(new), sv.frequencies(rot // 2)
+    k, v = (tokens(gen, cu[-1], Hkv, d, dtype) for _ in range(2))
+    append(c, k.to(DEV), v.to(DEV), cu, held, table, inv, interleaved=interleaved)
+    ref.append(sv.turned(mx.f64(k), sv.places(cu, held), inv, None, interleaved)[0], mx.f64(v), cu, held, table)
+    same(c, ref, Hkv)
+
+
 def test_every_length_of_a_page():
     gen = torch.Generator().manual_seed(2)
     inv = sv.frequencies(32)
