@@ -291,6 +291,10 @@ __device__ __forceinline__ void append_page(const CacheRopeArgs& ra, int id, uin
   }
 }
 
+__device__ __forceinline__ u32x4 recode16(const u32x4& x, float f) {
+  return u32x4{recode4(x[0], f), recode4(x[1], f), recode4(x[2], f), recode4(x[3], f)};
+}
+
 // One wavefront for a page and key head, rows in passes of 64 / (D / 16): the form for few tokens to a page, where
 // a workgroup's other lanes would have nothing to do.  Of several passes the last stays in registers, the others are
 // turned again once the scale is known.
@@ -348,26 +352,41 @@ __device__ __forceinline__ void append_few(const CacheRopeArgs& ra, int64_t item
   }
   const float ik = inverse_pow2(sk), iv = inverse_pow2(sv);
   uint8_t *kc = a.kc + ph * P * D, *vc = a.vc + ph * P * D;
+  // The earlier codes at a larger scale: every load on its way before the first is waited for.
   if (w.off > 0 && sk > old_k) {
     const float f = old_k * ik;
-#pragma unroll 4
-    for (int e = lane; e < w.off * D / 4; e += 64) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(kc) + e;
-      *p = recode4(*p, f);
-    }
+    u32x4 x[D / 16];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+      if (lane + 64 * j < w.off * (D / 16)) x[j] = reinterpret_cast<const u32x4*>(kc)[lane + 64 * j];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+      if (lane + 64 * j < w.off * (D / 16)) reinterpret_cast<u32x4*>(kc)[lane + 64 * j] = recode16(x[j], f);
   }
   if (w.off > 0 && sv > old_v) {
+    // of a channel's row of tokens three times sixteen, three words and three bytes; what lies behind is not touched
     const float f = old_v * iv;
-    const int words = w.off / 4, rest = w.off % 4;  // of a channel's row of tokens; what lies behind them is not touched
-#pragma unroll 4
-    for (int e = lane; e < D * words; e += 64) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(vc + (e / words) * P) + e % words;
-      *p = recode4(*p, f);
-    }
-    for (int e = lane; e < D * rest; e += 64) {
-      uint8_t* p = vc + (e / rest) * P + 4 * words + e % rest;
-      *p = uint8_t(recode4(*p, f));
-    }
+    const int n16 = w.off / 16, n4 = w.off % 16 / 4, n1 = w.off % 4;
+    u32x4 x[D / 64][3];
+    uint32_t y[D / 64][3], z[D / 64][3];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint8_t* p = vc + (lane + 64 * j) * P;
+        if (i < n16) x[j][i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
+        if (i < n4) y[j][i] = *reinterpret_cast<const uint32_t*>(p + 16 * n16 + 4 * i);
+        if (i < n1) z[j][i] = p[16 * n16 + 4 * n4 + i];
+      }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        uint8_t* p = vc + (lane + 64 * j) * P;
+        if (i < n16) *reinterpret_cast<u32x4*>(p + 16 * i) = recode16(x[j][i], f);
+        if (i < n4) *reinterpret_cast<uint32_t*>(p + 16 * n16 + 4 * i) = recode4(y[j][i], f);
+        if (i < n1) p[16 * n16 + 4 * n4 + i] = uint8_t(recode4(z[j][i], f));
+      }
   }
   for (int pass = passes - 1; pass >= 0; --pass) {
     if (pass + 1 < passes) load(pass);
