@@ -892,7 +892,8 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
 #pragma unroll
     for (int i = 0; i < kJoinFew; ++i) {
       const float* pp = part(i < n ? i : 0);
-      y[i] = *reinterpret_cast<const f32x4*>(pp + at);
+      y[i] = f32x4{0, 0, 0, 0};
+      if (i < n) y[i] = *reinterpret_cast<const f32x4*>(pp + at);
       ml[i] = *reinterpret_cast<const f32x2*>(pp + kChunkRows * D + 2 * r);
     }
     float m = ml[0][0];
