@@ -460,8 +460,9 @@ hipError_t launch(const CacheRopeArgs& a, hipStream_t st) {
 
 template <typename T, typename TO, int D>
 hipError_t launch_form(const CacheRopeArgs& a, hipStream_t st) {
-  // Few tokens to a sequence, and so to a page: 16 rows are two passes (d = 128) of one wavefront.
-  if (int64_t(a.c.n) <= 16 * int64_t(a.c.N)) return launch<T, TO, D, 0>(a, st);
+  // Few tokens to a sequence, and so to a page: 8 rows are one pass (d = 128) of one wavefront.  64 sequences of 8 tokens
+  // take 9.4 us so and 11.9 by workgroups, of 16 tokens 20.2 and 14.5; 256 single tokens 12.7 and 30.6.
+  if (int64_t(a.c.n) <= 8 * int64_t(a.c.N)) return launch<T, TO, D, 0>(a, st);
   // Two heads that share the sines, where that leaves every compute unit three workgroups: 14300 tokens of 8 heads of 128
   // with 32 of queries take 78 us so and 80 by single heads, 2400 tokens of 64 sequences 25.3 and 24.5.
   const int64_t pairs = (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv;

@@ -193,6 +193,7 @@ struct CacheChunkArgs {
 // Rows of a tile: (new token, query head of the group) pairs, heads fastest.
 constexpr int kChunkRows = 128;
 int cache_chunk_groups(int n, int N, int Hq, int Hkv, int page, int max_pages, bool bf16);
+int cache_chunk_most_groups(int n, int N, int Hq, int Hkv, int page, int max_pages, bool bf16);
 int64_t cache_chunk_slots(int n, int N, int Hq, int Hkv);
 // Two parts of tiles for each workgroup, [rows][d] and [rows][2], and what each part is (8 words).
 __host__ __device__ constexpr int64_t chunk_part_floats(int d) { return kChunkRows * (int64_t(d) + 2); }

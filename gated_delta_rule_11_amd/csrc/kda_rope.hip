@@ -2,7 +2,11 @@
 //
 // Bound by the bytes of x and y.  A wavefront's lanes form the sines and cosines of its rows once, one pair after
 // another, and hand them round through the LDS; then each lane turns one unit of 16 channels for head after head, so
-// the sines cost a few instructions a head and neighbouring lanes read neighbouring memory.
+// the sines cost a few instructions a head and neighbouring lanes read neighbouring memory.  A table of sines would be
+// read again for every row; formed in 64 bits they need none, and are right at any position.
+//
+// Measured: 333 MB (bf16, 5100 rows of 128 heads' worth of 128 channels) in 65 us, 5.1 TB/s; 110 MB of fp32 rows of 24 heads
+// of 64, forwards or backwards, in 29; 32 rows of 32 heads in 3.6.
 #include "kda_mix_launch.hpp"
 #include "kda_rotary.hpp"
 

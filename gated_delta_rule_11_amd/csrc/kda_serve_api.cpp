@@ -43,8 +43,9 @@ bool turn_ok(int rot, int d, int n_axes, int interleaved) {
 }
 
 // What one wavefront turns: with `many`, so many rows that its lanes, a unit of 16 channels each, come out even with
-// the heads (24 heads of 64 channels: two rows of eight heads at a time); all of the rows' heads, or fewer where that
-// leaves the GPU short of wavefronts.
+// the heads (24 heads of 64 channels: two rows of eight heads at a time, 55 us for 65 by whole rows); all of the rows'
+// heads, or fewer where that leaves the GPU short of wavefronts (256 rows of 32 heads of 128: 3.6 us in four parts, 4.6
+// whole; 2000 rows 7.0 whole, 8.2 in four parts).
 void rope_waves(RopeArgs& a, bool many) {
   const int most = 64 / (a.d / 16);
   a.side = most;
@@ -54,7 +55,7 @@ void rope_waves(RopeArgs& a, bool many) {
     a.rows = most / a.side;
   }
   const int64_t all = (a.H + a.side - 1) / a.side, groups = (int64_t(a.n) + a.rows - 1) / a.rows;
-  const int64_t want = groups < 1 ? 1 : (8192 + groups - 1) / groups, parts = want < all ? want : all;
+  const int64_t want = groups < 1 ? 1 : (2048 + groups - 1) / groups, parts = want < all ? want : all;
   a.heads = int((all + parts - 1) / parts * a.side);
 }
 
@@ -159,7 +160,7 @@ size_t kda_attn_chunk_fwd_workspace_bytes(int n, int N, int Hq, int Hkv, int d, 
   if (!dtype_ok(in_dtype) || heads_ok(n, Hq, Hkv, d) != KDA_OK || Hq / Hkv > kMaxGroup || !page_ok(page) || N < 1 || n < 1 ||
       max_pages < 1)
     return 0;
-  return size_t(cache_chunk_workspace_floats(cache_chunk_groups(n, N, Hq, Hkv, page, max_pages, in_dtype == KDA_BF16), d)) * 4;
+  return size_t(cache_chunk_workspace_floats(cache_chunk_most_groups(n, N, Hq, Hkv, page, max_pages, in_dtype == KDA_BF16), d)) * 4;
 }
 
 kda_status kda_attn_chunk_fwd(const void* q, int64_t q_stride, kda_dtype in_dtype, const int* cu_seqlens,

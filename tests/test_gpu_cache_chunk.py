@@ -2,8 +2,8 @@
 
 Bounds: with bf16 queries each probability and the output are rounded once (2^-8 each).  In fp32: a sum over the channels and
 one over the tokens (three exact products to a term with fp32 queries), the exponent's own |x| 2^-24 for |x| up to 48, the
-joins.  Two forms divide the work: tables of up to 512 tokens run one workgroup to a tile of rows, longer ones divide all
-rows' keys evenly; ``width`` makes a short context's table long."""
+joins.  Two forms divide the work: one workgroup to a tile of rows, and where the table has room for many tokens all rows'
+keys in even shares.  Every test runs with the table as it is and with one that has room for more (``wider``)."""
 import math
 
 import numpy as np
@@ -21,13 +21,27 @@ BF, F32 = torch.bfloat16, torch.float32
 F8 = torch.float8_e4m3fn
 
 
+MORE = 0
+
+
+@pytest.fixture(params=[0, 4500], autouse=True)
+def more(request):
+    global MORE
+    MORE = request.param
+
+
+def wider(t, P):
+    """The table with room for MORE tokens: columns of no page."""
+    return [list(x) + [-1] * max(0, MORE // P - len(x)) for x in t]
+
+
 def ends(new):
     return [0, *np.cumsum(new).tolist()]
 
 
 def run(c, t, q, new, ctx, **kw):
     kw = {"o_dtype": q.dtype, "want_lse": True, **kw}
-    return kda.attn_chunk_fwd(q.to(DEV), i32(ends(new)), c["kc"], c["vc"], c["ks"], c["vs"], i32(t), i32(ctx), **kw)
+    return kda.attn_chunk_fwd(q.to(DEV), i32(ends(new)), c["kc"], c["vc"], c["ks"], c["vs"], i32(wider(t, c["kc"].shape[2])), i32(ctx), **kw)
 
 
 def compare(label, got, c, t, q, new, ctx, scale=None):
@@ -57,7 +71,7 @@ CTX = [1, 300, 70, 15, 64, 129, 33, 65, 250, 64, 41, 16]
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("width", [None, 64])
 def test_lengths(width, d, P, dtype):
-    more = {} if width is None else {"width": width * 16 // P * 3}
+    more = {} if width is None else {"width": width * 16 // P * 4}
     assert (kda.attn_chunk_fwd_workspace_bytes(sum(NEW), 12, 4, 2, d, P, more.get("width", -(-300 // P)), dtype) > 0) == (width is not None)
     check(f"P={P} d={d}", NEW, CTX, 4, 2, P, d, dtype, **more)
 
@@ -250,7 +264,7 @@ def test_a_workspace_of_any_contents():
     q = torch.randn(156, 4, 64).to(BF)
     want = run(c, t, q, new, ctx)
     for word in (1, 2, 0x7F7F7F7F, -1):
-        ws = torch.full((kda.attn_chunk_fwd_workspace_bytes(156, 3, 4, 2, 64, 16, len(t[0]), BF) // 4,), word, dtype=torch.int32, device=DEV)
+        ws = torch.full((kda.attn_chunk_fwd_workspace_bytes(156, 3, 4, 2, 64, 16, len(wider(t, 16)[0]), BF) // 4,), word, dtype=torch.int32, device=DEV)
         got = run(c, t, q, new, ctx, workspace=ws.view(torch.uint8))
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
@@ -343,7 +357,7 @@ def test_views_guards_tail_and_workspace(dtype):
         assert not want[0][n:].any() and not want[1][n:].any()
         compare("tail", want, c, t, whole[:n, 1:1 + Hq], new, ctx)
         (o, fine), (lse, fine_l) = guarded((rows, Hq, d), dtype), guarded((rows, Hq), F32)
-        ws = torch.full((max(16, kda.attn_chunk_fwd_workspace_bytes(rows, 3, Hq, 2, d, P, len(t[0]), dtype)),), 255, dtype=torch.uint8, device=DEV)
+        ws = torch.full((max(16, kda.attn_chunk_fwd_workspace_bytes(rows, 3, Hq, 2, d, P, len(wider(t, P)[0]), dtype)),), 255, dtype=torch.uint8, device=DEV)
         run(c, t, q, new, ctx, o=o, lse=lse, workspace=ws)
         torch.cuda.synchronize()
         assert fine() and fine_l() and torch.equal(o[:n], want[0][:n]) and torch.equal(lse[:n], want[1][:n])
@@ -355,7 +369,7 @@ def test_entries_out_of_order_touch_nothing_outside():
     c, t = filled([600, 90], 2, 16, 64)
     for cu in ([0, 50, 20], [30, 10, 5], [-7, 10, 10 ** 6], [0, 2 ** 31 - 1, 3], [60, 0, 0]):
         for ctx in ([600, 90], [-5, 2 ** 31 - 1], [2 ** 31 - 1, -2 ** 31]):
-            for tab in (t, [x[:20] for x in t]):
+            for tab in (wider(t, 16), [x[:20] for x in t]):
                 (o, fine), (lse, fine_l) = guarded((60, 4, 64), F32), guarded((60, 4), F32)
                 kda.attn_chunk_fwd(torch.randn(60, 4, 64, device=DEV), i32(cu), c["kc"], c["vc"], c["ks"], c["vs"], i32(tab), i32(ctx), o=o, lse=lse)
                 torch.cuda.synchronize()
@@ -366,7 +380,7 @@ def test_streams_replays_and_the_same_bits():
     new, ctx = [5, 1, 90, 33], [900, 40, 400, 64]
     c, t = filled([x + 3 for x in ctx], 2, 16, 128)
     q = torch.randn(sum(new), 8, 128, device=DEV).to(BF)
-    cu, held, table = i32(ends(new)), i32(ctx), i32(t)
+    cu, held, table = i32(ends(new)), i32(ctx), i32(wider(t, 16))
     call = lambda **kw: kda.attn_chunk_fwd(q, cu, c["kc"], c["vc"], c["ks"], c["vs"], table, held, want_lse=True, o_dtype=BF, **kw)  # noqa: E731
     want = call()
     side = torch.cuda.Stream()

@@ -107,12 +107,18 @@ def test_chunk_refusals(L):  # noqa: F811
 
 def test_chunk_workspace(L):  # noqa: F811
     size = L.kda_attn_chunk_fwd_workspace_bytes
-    assert size(10, 2, 4, 2, 64, 16, 32, BF16) == 0 and size(10, 2, 4, 2, 64, 16, 33, BF16) > 0  # 512 tokens
+    assert size(10, 2, 4, 2, 64, 16, 64, BF16) == 0 and size(10, 2, 4, 2, 64, 16, 65, BF16) > 0  # 1024 tokens
     assert size(0, 2, 4, 2, 64, 16, 400, BF16) == 0 and size(10, 0, 4, 2, 64, 16, 400, BF16) == 0
     for bad in (dict(d=32), dict(page=48), dict(Hq=3), dict(it=7), dict(n=-1)):
         a = dict(n=10, N=2, Hq=4, Hkv=2, d=64, page=16, mp=400, it=BF16) | bad
         assert size(*a.values()) == 0, bad
     assert size(1 << 20, 4096, 32, 8, 128, 64, 1 << 20, BF16) == size(1000, 256, 32, 8, 128, 64, 4096, BF16)  # goes by the GPU, not by the call
+    for page, mp in ((16, 100), (64, 30), (64, 60), (32, 2000)):  # what is enough for a call is enough for smaller ones
+        sizes = [size(n, N, 16, 4, 64, page, mp, BF16) for n, N in ((1, 1), (3, 2), (40, 7), (900, 64), (40000, 700))]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+        for n, N in ((1, 1), (40, 7), (40000, 700)):
+            ok = dict(n=n, N=N, Hq=16, Hkv=4, qs=1024, page=page, mp=mp, ws=P(20), wsb=size(n, N, 16, 4, 64, page, mp, BF16))
+            assert chunk(L, **ok, o=None) == ERR_NULL and chunk(L, **ok, q=P(20, 2)) == ERR_ALIGN
 
 
 def test_binding_refuses_cpu_tensors(L):  # noqa: F811
