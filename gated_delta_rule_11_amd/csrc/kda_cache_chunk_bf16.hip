@@ -17,10 +17,13 @@ int64_t cache_chunk_slots(int n, int N, int Hq, int Hkv) { return int64_t(n) * (
 //   room 1000:  4 single tokens 12.5, 20.3;  256 of them 71, 78;  one prompt 33, 49
 //   room 2000:  one prompt 63, 74;  16 prompts 306, 330;  two chunks of 40 tokens 55, 42
 //   room 4000:  one prompt 150, 176;  26 single tokens among 6 chunks 110, 84
+// fp32, a third of the steps' rate and half the workgroups at once: one prompt of 2000 121, 143 (508 tiles); four chunks of
+// 101 to 700 tokens in a room of 2000, 24 heads on 4 of 64, 60, 48 (237 tiles).
 int cache_chunk_groups(int n, int N, int Hq, int Hkv, int page, int max_pages, bool bf16) {
   const int64_t tiles = cache_chunk_slots(n, N, Hq, Hkv) * Hkv;
   const int64_t steps = (int64_t(max_pages) * page + 63) / 64;
-  if ((steps <= 32 && tiles >= 4 * steps) || (steps <= 64 && tiles >= 16 * steps)) return 0;
+  const int64_t few = (bf16 ? 4 : 12) * steps;
+  if ((steps <= 32 && tiles >= few) || (steps <= 64 && tiles >= 4 * few)) return 0;
   return cache_chunk_most_groups(n, N, Hq, Hkv, page, max_pages, bf16);
 }
 
