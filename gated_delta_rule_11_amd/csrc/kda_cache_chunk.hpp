@@ -15,6 +15,14 @@
 // consecutive tokens of one query row; P is then in place as the operand of O^T = V^T P^T, and V's pages,
 // [d][token], are that product's other operand as they lie.
 //
+// What bounds it (MI355X, 32 heads on 8 of 128, bf16): long chunks by the products and what stands between them, 1024 tokens
+// behind 64511 in 1112 us, 980 TFLOP/s, where the matrix pipe is busy in 43 % of the cycles and the rest goes to the
+// exponentials, the conversions of codes and the LDS (an 8192^3 library product reaches 1067); drafted tokens by the cache's
+// bytes, 64 x 5 tokens over up to 8192 in 103 us and 7 for the joins, 4.8 TB/s; whole prompts of 500 to 2048 tokens, 109 us
+// for 69 GFLOP, by the 5 us that each tile takes to start and to end (pages, queries, first codes, outputs).  A wavefront that
+// forms the scores of the next step beside the products of this one needs more registers than two to a SIMD have (135 us
+// grew to 170), 64 rows to a wavefront likewise; orders asked of the scheduler changed nothing.
+//
 // Sums and statistics are fp32.  bf16 queries: P is rounded to bf16, 2^-8 of a term, as a bf16 output is.  fp32
 // queries and their P go in as three bf16 parts that sum to them: against the codes' exact values
 // every product is exact.  The reference that exponents are taken to stays up to 2^8 above the
@@ -63,7 +71,10 @@ __device__ __forceinline__ bool finite_codes(u32x4& w, float scale) {
 // ---- the division of the work -------------------------------------------------------------
 //
 // Cost of a tile, in units of (64 keys, one head of a group): its steps, weighted, and a start.  Linear
-// in the tile's number, so that a sequence's sum is a closed form.
+// in the tile's number, so that a sequence's sum is a closed form.  A narrow step at half a wide one's cost (at a quarter
+// 26 single tokens among 6 chunks take 180 us, at three eighths 148, at a half 133); a start of 16 instead of 20 gives the
+// same batch 138 and four prompts 120 for 122, of 12 135 and 122; a workgroup takes no less than kLeastCost, so that short
+// work is not cut into starts alone (16 and 24 differ by 3 %).
 constexpr int64_t kNarrowCost = 2, kWideCost = 4, kStartCost = 20, kLeastCost = 16;
 
 struct ChunkSeq {
@@ -851,8 +862,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
 }
 
 // Joins the parts of the tile that begins in workgroup blockIdx.x and ends in a later one: a sixteenth of its
-// rows.  D / 4 threads to a row.  Most tiles have two to four parts, which are read all at once; of more, several
-// groups of threads share a row's.
+// rows.  D / 4 threads to a row.  Most tiles have two to four parts, which are read all at once (a walk of their number
+// first: one token over 131072 106 us instead of 64); of more, several groups of threads share a row's.  Bound by the
+// parts' bytes where tiles are wide: 58 MB in 18 us, launch and all; 12 MB of narrow ones in 6.7.
 constexpr int kJoinBlocks = 16, kJoinFew = 4;
 static_assert(kJoinBlocks * 8 >= kChunkRows, "every row has a group of threads");
 template <typename TO, int D>
