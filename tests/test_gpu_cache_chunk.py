@@ -404,6 +404,31 @@ def test_streams_replays_and_the_same_bits():
         held.add_(1 if i < 3 else 0)
 
 
+def test_two_graphs_on_one_workspace():
+    """Of different sizes, replayed in turn, with eager calls on it in between."""
+    c, t = filled([3000, 700, 90], 2, 16, 64)
+    q = torch.randn(160, 4, 64, device=DEV).to(BF)
+    table = i32(wider(t, 16))
+    most = kda.attn_chunk_fwd_workspace_bytes(160, 3, 4, 2, 64, 16, table.shape[1], BF)
+    ws = torch.full((most,), 255, dtype=torch.uint8, device=DEV)
+    cu = [i32(ends(new)) for new in ([5, 150, 1], [2, 0, 7])]
+    ctx = i32([3000, 700, 90])
+    call = lambda i, w: kda.attn_chunk_fwd(q[:(160, 9)[i]], cu[i], c["kc"], c["vc"], c["ks"], c["vs"], table, ctx, want_lse=True, workspace=w)  # noqa: E731
+    want = [call(i, None) for i in range(2)]
+    graphs, got = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            got.append(call(i, ws))
+    for i in (0, 1, 1, 0, 0, 1, 0):
+        for x in got[i]:
+            x.fill_(7)
+        graphs[i].replay()
+        eager = call(1 - i, ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i])) and all(torch.equal(a, b) for a, b in zip(eager, want[1 - i]))
+
+
 def test_nothing_to_do_and_no_pages():
     c, t = filled([40], 2, 16, 64)
     q = torch.randn(5, 4, 64, device=DEV)
