@@ -514,7 +514,7 @@ def _match(what: str, *specs, like=None):
         at = t.get_device()  # (-1: on the CPU)
         if dev is None:
             dev = at
-        if t.shape == shape and t.dtype in dtypes and at == dev and at >= 0 and t.is_contiguous():
+        if at == dev and t.shape == shape and t.dtype in dtypes and at >= 0 and t.is_contiguous():
             continue
         if t.shape != shape:
             raise KDAError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -787,8 +787,8 @@ def rope(x, positions, inv_freq, axes=None, interleaved: bool = False, inverse: 
         raise KDAError(f"{what}: positions must be a tensor [n] or [n, axes]")
     A, half, specs = _turn(what, n, positions, inv_freq, axes)
     _match(what, *specs, like=x)
-    _check(lib().kda_rope(_a(x), _dtype_code(x), xs, _a(positions), A, _a(inv_freq), _a(axes), 2 * half, int(bool(interleaved)),
-                          int(bool(inverse)), _a(out), _dtype_code(out), ys, n, H, d, _here(x)), what)
+    _check(lib().kda_rope(x.data_ptr(), _dtype_code(x), xs, positions.data_ptr(), A, inv_freq.data_ptr(), _a(axes), 2 * half,
+                          int(bool(interleaved)), int(bool(inverse)), out.data_ptr(), _dtype_code(out), ys, n, H, d, _here(x)), what)
     return out
 
 
@@ -851,11 +851,11 @@ def kv_cache_append_rope(k, v, cu_seqlens, context_len, block_table, k_cache, v_
     A, half, specs = _turn(what, n, positions, inv_freq, axes)
     N, page, pages, mp = _cache_shapes(what, Hkv, d, k_cache, v_cache, k_scale, v_scale, block_table, context_len, *specs,
                                        ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32), like=k)
-    _check(lib().kda_kv_cache_append_rope(_a(k), k_row, _a(v), v_row, _dtype_code(k), _a(q), q_row, _a(q_out), o_code, o_row,
-                                          _a(positions), A, _a(inv_freq), _a(axes), 2 * half, int(bool(interleaved)),
-                                          _a(cu_seqlens), _a(context_len), _a(block_table), _a(k_cache), _a(v_cache),
-                                          _a(k_scale), _a(v_scale), n, N, Hq, Hkv, d, page, pages, mp, int(not given),
-                                          _here(k)), what)
+    _check(lib().kda_kv_cache_append_rope(k.data_ptr(), k_row, v.data_ptr(), v_row, _dtype_code(k), _a(q), q_row, _a(q_out),
+                                          o_code, o_row, _a(positions), A, inv_freq.data_ptr(), _a(axes), 2 * half,
+                                          int(bool(interleaved)), cu_seqlens.data_ptr(), context_len.data_ptr(),
+                                          block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                          v_scale.data_ptr(), n, N, Hq, Hkv, d, page, pages, mp, int(not given), _here(k)), what)
     return q_out
 
 
@@ -927,7 +927,8 @@ def attn_chunk_fwd(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tabl
                                        ("cu_seqlens", cu_seqlens, (context_len.shape[0] + 1,), _I32), like=q)
     need = lib().kda_attn_chunk_fwd_workspace_bytes(n, N, Hq, Hkv, d, page, mp, _dtype_code(q)) if pages and Hkv else 0
     wp, wb, _keep = _need(workspace, need, q.device)
-    _check(lib().kda_attn_chunk_fwd(_a(q), q_row, _dtype_code(q), _a(cu_seqlens), _a(k_cache), _a(v_cache), _a(k_scale),
-                                    _a(v_scale), _a(block_table), _a(context_len), _a(o), _dtype_code(o), _a(lse), n, N, Hq, Hkv,
-                                    d, page, pages, mp, _softmax_scale(scale, d), int(not given), wp, wb, _here(q)), what)
+    _check(lib().kda_attn_chunk_fwd(q.data_ptr(), q_row, _dtype_code(q), cu_seqlens.data_ptr(), k_cache.data_ptr(),
+                                    v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                                    context_len.data_ptr(), o.data_ptr(), _dtype_code(o), _a(lse), n, N, Hq, Hkv, d, page,
+                                    pages, mp, _softmax_scale(scale, d), int(not given), wp, wb, _here(q)), what)
     return o, lse
