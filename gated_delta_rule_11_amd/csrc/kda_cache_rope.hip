@@ -468,10 +468,12 @@ template <typename T, typename TO, int D>
 hipError_t launch_form(const CacheRopeArgs& a, hipStream_t st) {
   // Few tokens to a sequence, and so to a page: 8 rows are one pass (d = 128) of one wavefront.  64 sequences of 8 tokens
   // take 9.4 us so and 11.9 by workgroups, of 16 tokens 20.2 and 14.5; 256 single tokens 12.7 and 30.6.
-  if (int64_t(a.c.n) <= 8 * int64_t(a.c.N)) return launch<T, TO, D, 0>(a, st);
+  // So do pages too many for one launch of the larger workgroups, which holds fewer than 2^32 threads.
+  const int64_t pairs = (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv, items = a.q.x ? rope_items(a.q) : 0;
+  if (int64_t(a.c.n) <= 8 * int64_t(a.c.N) || (pairs + items + 1) * kThreads<D, 1> >= int64_t(1) << 32)
+    return launch<T, TO, D, 0>(a, st);
   // Two heads that share the sines, where that leaves every compute unit three workgroups: 14300 tokens of 8 heads of 128
   // with 32 of queries take 78 us so and 80 by single heads, 2400 tokens of 64 sequences 25.3 and 24.5.
-  const int64_t pairs = (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv;
   if (a.c.Hkv % 2 == 0 && pairs >= 2 * 768) return launch<T, TO, D, 2>(a, st);
   return launch<T, TO, D, 1>(a, st);
 }

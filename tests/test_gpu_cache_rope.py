@@ -197,6 +197,28 @@ def test_a_cache_beyond_32_bits_of_offsets():
             assert torch.equal(big[x][far:], c[x].view(big[x].dtype)), x
 
 
+def test_more_pages_than_the_larger_workgroups_fit_a_launch():
+    """480000 sequences of eight tokens and more, seven heads: the last ones' pages are as if they came alone."""
+    N, Hkv, P, d, inv = 480000, 7, 16, 128, sv.frequencies(64).to(DEV)
+    new = torch.full((N,), 8, dtype=torch.int64)
+    new[-3:] = torch.tensor([21, 1, 16])
+    n = int(new.sum())
+    assert (n // P + 2 * N) * Hkv * 512 > 2 ** 32 and n > 8 * N
+    cu = torch.zeros(N + 1, dtype=torch.int32)
+    cu[1:] = new.cumsum(0)
+    x = torch.zeros(n, Hkv, d, dtype=BF, device=DEV)
+    last = n - 38
+    x[last:] = torch.randn(38, Hkv, d, device=DEV).to(BF)
+    table = torch.full((N, 2), -1, dtype=torch.int32)
+    table[-3:] = torch.tensor([[0, 3], [2, -1], [1, -1]])
+    got, want = cache(4, Hkv, P, d), cache(4, Hkv, P, d)
+    kda.kv_cache_append_rope(x, x, cu.to(DEV), torch.zeros(N, dtype=torch.int32, device=DEV), table.to(DEV), got["kc"], got["vc"], got["ks"], got["vs"], inv)
+    append(want, x[last:], x[last:], [0, 21, 22, 38], [0, 0, 0], [[0, 3], [2, -1], [1, -1]], inv)
+    torch.cuda.synchronize()
+    for y in got:
+        assert torch.equal(got[y].view(torch.uint8 if y[1] == "c" else F32), want[y].view(torch.uint8 if y[1] == "c" else F32)), y
+
+
 def test_special_values():
     """Infinities and NaN among the turned channels do not enter the scale; the largest values overflow to it."""
     inv, pos = sv.frequencies(32), torch.zeros(4, dtype=torch.int32)
