@@ -27,6 +27,11 @@
 // queries and their P go in as three bf16 parts that sum to them: against the codes' exact values
 // every product is exact.  The reference that exponents are taken to stays up to 2^8 above the
 // largest score seen, so that p <= 1 and most steps leave the accumulators alone.
+//
+// The sums of p v are divided at the end only: values of 2^119 and more can take them beyond fp32 although the mean is
+// not.  A tile that ends with a sum that is not finite and has such values in its pages is done once more with the values
+// 2^-26 times what they are, and l likewise: sums of up to 2^26 tokens then stay finite.  (The look at the sums and the
+// way back: 1 % of the times above.)
 #pragma once
 
 #include <type_traits>
@@ -42,6 +47,7 @@ __device__ __forceinline__ int scalar_load(const int* p) { return *(const_ints)(
 __device__ __forceinline__ float scalar_load(const float* p) { return *(const_floats)(uintptr_t)p; }
 
 constexpr int kNarrowRows = 32;
+constexpr int kShrinkBits = 26;  // (the least scale, 2^-100, stays a normal number)
 
 // A value that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t x) {
@@ -52,7 +58,8 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 
 // Sixteen codes without those whose value (code times a power of two) is no finite fp32 number: NaN, and
 // from a scale of 2^120 on the largest; whether there were any.  By bytes: a magnitude plus 128 less the least
-// such magnitude carries into the sign's place.
+// such magnitude carries into the sign's place.  (NAN_INSTEAD: those codes become NaN instead.)
+template <bool NAN_INSTEAD = false>
 __device__ __forceinline__ bool finite_codes(u32x4& w, float scale) {
   const int k = int(__float_as_uint(scale) >> 23) - 127;
   int least = (135 - k) * 8;  // the magnitude of 2^(128 - k)
@@ -63,7 +70,8 @@ __device__ __forceinline__ bool finite_codes(u32x4& w, float scale) {
   for (int i = 0; i < 4; ++i) {
     const uint32_t m = ((w[i] & 0x7f7f7f7fu) + add) & 0x80808080u;
     any |= m;
-    w[i] &= ~((m << 1) - (m >> 7));
+    if constexpr (NAN_INSTEAD) w[i] |= m - (m >> 7);
+    else w[i] &= ~((m << 1) - (m >> 7));
   }
   return any != 0;
 }
@@ -178,13 +186,17 @@ struct ChunkWork {
 
   const CacheChunkArgs& a;
   unsigned char* smem;
-  int* bad;  // set where values that are not finite have been left out
+  int* bad;   // set where values that are not finite have been left out
+  int* over;  // set where a sum is not finite
+  int lift;   // the values are taken as 2^-lift of what they are
   int tid, lane, wave, G, P, ps;
   float c;
   bool neg;
 
   __device__ __forceinline__ ChunkWork(const CacheChunkArgs& args, unsigned char* lds) : a(args), smem(lds) {
     bad = reinterpret_cast<int*>(lds + W::lds - 128);
+    over = bad + 1;
+    lift = 0;
     tid = threadIdx.x;
     lane = tid & 63;
     wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -210,6 +222,7 @@ struct ChunkWork {
     if (rows <= kNarrowRows) return rr * D + c0;
     return (((rr >> 5) * (D / 8) + (c0 >> 3)) * 64 + (c0 >> 2 & 1) * 32 + (rr & 31)) * 4;
   }
+  __device__ __forceinline__ float shrink() const { return __uint_as_float(uint32_t(127 - uniform(lift)) << 23); }
   __device__ __forceinline__ float* part(int slot) const { return a.part + int64_t(slot) * chunk_part_floats(D); }
 
   __device__ __forceinline__ void wide(const ChunkItem& x, const int* table) {
@@ -271,9 +284,10 @@ struct ChunkWork {
       }
     };
     const int first_edge = (tmin + 1) >> 6;  // the first step that some row does not see all of
+    const int first_look = lift == 0 ? first_edge : 0;  // (smaller values: all)
     // The values of a step that some row does not see all of, or with tokens in no page.
     auto clean_v = [&](Codes& v, int t, const Ids& z) {
-      if (t < first_edge && z.gone == 0) return;
+      if (t < first_look && z.gone == 0) return;
 #pragma unroll
       for (int i = 0; i < NPC; ++i) {
         const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
@@ -287,7 +301,11 @@ struct ChunkWork {
         }
         // A masked probability is zero, but zero times a NaN is not: where a step is masked for some rows such
         // values leave the product, and the rows that see them are set at the end (set_bad, from this step on).
-        if (t >= first_edge && finite_codes(v.w[i], v.scale[i])) *bad = 1;
+        if (t >= first_edge) {
+          if (finite_codes(v.w[i], v.scale[i])) *bad = 1;
+        } else if (t >= first_look) {
+          finite_codes<true>(v.w[i], v.scale[i]);  // (2^-lift of it would be finite)
+        }
       }
     };
     auto put_v = [&](bf16_t* V, const Codes& v) {
@@ -295,8 +313,8 @@ struct ChunkWork {
       for (int i = 0; i < NPC; ++i) {
         const int at = (wave * NPC + i) * 1024, o = (at & (P * D - 1)) + lane * 16;
         const int d = o >> ps, vt = ((at / (P * D)) << ps) + (o & (P - 1));
-        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt)) = codes(v.w[i][0], v.w[i][1], v.scale[i]);
-        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt + 8)) = codes(v.w[i][2], v.w[i][3], v.scale[i]);
+        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt)) = codes(v.w[i][0], v.w[i][1], v.scale[i] * shrink());
+        *reinterpret_cast<bf16x8*>(V + TV::off(d, vt + 8)) = codes(v.w[i][2], v.w[i][3], v.scale[i] * shrink());
       }
     };
     const uint32_t krow = TK::b_row8_32(lane), vrow = TV::b_row8_32(lane);
@@ -403,7 +421,14 @@ struct ChunkWork {
       two = three;
       lds_barrier();
     }
-    l = sum_halves(l);
+    l = sum_halves(l) * shrink();
+    ref += float(uniform(lift));
+    f32x4 none = {0, 0, 0, 0};  // of finite sums
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) none[e & 3] = __builtin_fmaf(acc[i][e], 0.f, none[e & 3]);
+    if ((none[0] + none[1]) + (none[2] + none[3]) != 0.f) *over = 1;
     const bool mine = w0 + l32 < x.rows;
     if (x.slot < 0) {
       // through the LDS, so that a row's channels leave side by side (every wavefront has left the last step)
@@ -605,6 +630,9 @@ struct ChunkWork {
 #pragma unroll
         for (int d = 0; d < ND; ++d) any |= finite_codes(vr[d], vsc);
         if (any) *bad = 1;
+      } else if (lift != 0) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) finite_codes<true>(vr[d], vsc);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -612,7 +640,7 @@ struct ChunkWork {
         for (int d0 = 0; d0 < ND; d0 += 4) {
           bf16x8 vf[4];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) vf[d] = codes(vr[d0 + d][2 * u], vr[d0 + d][2 * u + 1], vsc);
+          for (int d = 0; d < 4; ++d) vf[d] = codes(vr[d0 + d][2 * u], vr[d0 + d][2 * u + 1], vsc * shrink());
 #pragma unroll
           for (int n = 0; n < NC; ++n) {
             const Parts8 pf(__builtin_shufflevector(s[n][2 * u], s[n][2 * u + 1], 0, 1, 2, 3, 4, 5, 6, 7));
@@ -632,9 +660,9 @@ struct ChunkWork {
     if constexpr (QL) lds_barrier();                   // the queries have been read
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
-      const float ls = sum_groups(l[n]);
+      const float ls = sum_groups(l[n]) * shrink();
       if (g4 == 0) {
-        jm[wave * 16 * NC + 16 * n + r16] = ref[n];
+        jm[wave * 16 * NC + 16 * n + r16] = ref[n] + float(uniform(lift));
         jm[(4 + wave) * 16 * NC + 16 * n + r16] = ls;
       }
 #pragma unroll
@@ -655,6 +683,7 @@ struct ChunkWork {
         ls += f * jm[(4 + w) * 16 * NC + rr];
         y += *reinterpret_cast<const f32x4*>(jo + (w * 16 * NC + rr) * (D + 4) + c0) * f;
       }
+      if (((y[0] * 0.f + y[1] * 0.f) + (y[2] * 0.f + y[3] * 0.f)) != 0.f) *over = 1;
       if (x.slot < 0) {
         const uint32_t r = uint32_t(x.r0 + rr);
         const int64_t row = (int64_t(x.s.first) + r / uint32_t(G)) * a.Hq + x.kvh * G + int(r % uint32_t(G));
@@ -698,23 +727,46 @@ struct ChunkWork {
     }
   }
 
-  __device__ __forceinline__ void run(const ChunkItem& x, int seq) {
+  // Whether some page's values can add up to more than fp32 holds: 448 2^88 times 2^31 tokens cannot.
+  __device__ __forceinline__ bool large_values(const ChunkItem& x, const int* table) {
+    const int64_t k1 = x.end < int64_t(x.t1) * 64 ? x.end : int64_t(x.t1) * 64;
+    bool any = false;
+#pragma unroll 1
+    for (int64_t key = int64_t(x.t0) * 64 + 16 * tid; key < k1; key += 16 * 256) {
+      const int p = table[key >> ps];
+      if (p >= 0 && p < a.pages) any |= a.vs[int64_t(p) * a.Hkv + x.kvh] > 0x1p88f;
+    }
+    return any;
+  }
+
+  // The item's outputs or part; false if it has to be done again, with `lift` set.
+  __device__ __forceinline__ bool run(const ChunkItem& x, int seq) {
     const int* table = a.table + int64_t(seq) * a.max_pages;
     // what follows from the lane's number is formed again for each item: held over the loop, all three forms'
     // would be in registers at once
     asm volatile("" : "+v"(tid), "+v"(lane));
     lds_barrier();  // the item before is out of the LDS
-    if (tid == 0) *bad = 0;
+    if (tid == 0) *bad = *over = 0;
     lds_barrier();
     if (x.rows > kNarrowRows) wide(x, table);
     else if (x.rows > 16) narrow<2>(x, table);
     else narrow<1>(x, table);
     lds_barrier();
+    if (lift == 0 && uniform(*over)) {
+      if (large_values(x, table)) *over = 2;
+      lds_barrier();
+      if (uniform(*over) == 2) {
+        lift = kShrinkBits;
+        return false;
+      }
+    }
+    lift = 0;
     if (*bad) {
       __threadfence();  // behind the stores of the sums
       __syncthreads();
       set_bad(x, table);
     }
+    return true;
   }
 };
 
@@ -732,7 +784,7 @@ struct ChunkPart {
 };
 
 template <typename T, typename TO, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kernel(const CacheChunkArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? (D == 64 ? 3 : 2) : 1) void cache_chunk_kernel(const CacheChunkArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   if (a.zero_tail) {
@@ -817,8 +869,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
     z.s = chunk_seq(a, z.seq);
     z.w = w;
   }
-  // What comes next is kept in the LDS while an item is worked on: in scalar registers it would push others out.
+  // What comes next, and what the item began with, are kept in the LDS while it is worked on: in scalar registers
+  // they would push others out.
   ChunkState* const state = reinterpret_cast<ChunkState*>(smem + ChunkShape<T, D>::lds - 112);
+  static_assert(2 * sizeof(ChunkState) <= 112);
+  if (tid == 0) state[0] = z;
+  int now = 0;  // the item's own
   for (;;) {
     int64_t from = 0, to = 1, full = 1, rest = uniform(z.rest);
     ChunkSeq s = uniform(z.s);
@@ -853,10 +909,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
       if (tid == 0) parts[it.slot] = ChunkPart{to < full ? 1 : 2, s.first, kvh, it.r0, it.rows, {0, 0, 0}};
     }
     lds_barrier();  // the state has been read
-    if (tid == 0) *state = ChunkState{todo - (to - from), 0, seq, kvh, tile + 1, w, s};
-    work.run(it, seq);
+    if (tid == 0) state[now ^ 1] = ChunkState{todo - (to - from), 0, seq, kvh, tile + 1, w, s};
+    now ^= work.run(it, seq);
     lds_barrier();
-    z = *state;
+    z = state[now];
     if (uniform(z.todo) <= 0) return;
   }
 }
@@ -865,7 +921,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void cache_chunk_kerne
 // rows.  D / 4 threads to a row.  Most tiles have two to four parts, which are read all at once (a walk of their number
 // first: one token over 131072 106 us instead of 64); of more, several groups of threads share a row's.  Bound by the
 // parts' bytes where tiles are wide: 58 MB in 18 us, launch and all; 12 MB of narrow ones in 6.7.
+// Each part's factor is 2^-10 of its own (at most 512 parts): sums that are finite add up to a finite one.
 constexpr int kJoinBlocks = 16, kJoinFew = 4;
+constexpr float kJoinFactor = 1.f / 1024;
 static_assert(kJoinBlocks * 8 >= kChunkRows, "every row has a group of threads");
 template <typename TO, int D>
 __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkArgs a) {
@@ -892,7 +950,7 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
     const uint32_t rr = uint32_t(p.r0 + r);
     const int64_t row = (int64_t(p.first) + rr / uint32_t(G)) * a.Hq + p.kvh * G + int(rr % uint32_t(G));
     store4(static_cast<TO*>(a.o) + row * D + 4 * e, y * (l == 0.f ? 0.f : 1.0f / l));
-    if (a.lse && e == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+    if (a.lse && e == 0) a.lse[row] = (m + log2f(l * (1.f / kJoinFactor))) * 0.6931471805599453f;
   };
   int n = 0;  // parts, where they are few
 #pragma unroll
@@ -917,7 +975,7 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
 #pragma unroll
     for (int i = 0; i < kJoinFew; ++i)
       if (i < n) {
-        const float f = fast_exp2(ml[i][0] - from);
+        const float f = fast_exp2(ml[i][0] - from) * kJoinFactor;
         l += f * ml[i][1];
         sum += y[i] * f;
       }
@@ -945,7 +1003,7 @@ __global__ __launch_bounds__(256) void cache_chunk_join_kernel(const CacheChunkA
 #pragma unroll 4
     for (int i = g >> lg; i < n; i += share) {
       const float* pp = part(i);
-      const float f = fast_exp2(pp[kChunkRows * D + 2 * r] - from);
+      const float f = fast_exp2(pp[kChunkRows * D + 2 * r] - from) * kJoinFactor;
       l += f * pp[kChunkRows * D + 2 * r + 1];
       y += *reinterpret_cast<const f32x4*>(pp + at) * f;
     }

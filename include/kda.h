@@ -560,6 +560,7 @@ kda_status kda_attn_decode_step(const void* q, kda_dtype in_dtype, const void* k
  * At most 1024 query heads share a key head.  Roundings, missing pages and what lies behind the last token: as in
  * kda_attn_decode_step, whose results single tokens get (the sums in another order).  fp32 queries: every product is exact.
  * A NaN or infinity among the values reaches only the rows that see it.
+ * Finite values give finite outputs, however large they are, up to 2^26 tokens.
  * The work, the keys of all rows, is divided on the device, whatever the lengths: no list of them is needed on the host.
  * Where the table's room is long for the number of rows it is divided evenly over the GPU.  Every sum has a fixed order: the same bits every time.
  *   workspace  kda_attn_chunk_fwd_workspace_bytes bytes, 16-byte aligned (NULL when that is 0); contents do not matter.
