@@ -4,7 +4,8 @@
 // Pair j of a row's channels turns by the angle pos[axis(j)] inv_freq[j]:
 //   y_a = x_a cos t - x_b sin t,   y_b = x_b cos t + x_a sin t
 // with (a, b) = (j, j + half) or, interleaved, (2 j, 2 j + 1).  The angle is formed and reduced in 64
-// bits: a far position's angle has few fraction bits left in 32 (2^17 turns leave 2^-7 of a turn).
+// bits: a far position's angle has few fraction bits left in 32 (2^17 turns leave 2^-7 of a turn).  From a position of
+// 2^29 on the product has more than 53 bits, and what its rounding loses (up to 2^-23) is kept beside it.
 #pragma once
 
 #include "kda_mix_launch.hpp"
@@ -12,12 +13,17 @@
 
 namespace kda {
 
+// The product of a place and a frequency, up to 55 bits: rounded, and what the rounding lost.
+struct Angle {
+  double a, rest;
+};
+
 // Sine and cosine: a = k pi/2 + r with |r| <= pi/4 (pi/2 in two parts, so that r keeps 53 bits after the
 // point), then the Taylor sums, whose first terms left out are below 2^-49, and a quarter turn k mod 4.
 // The vector unit runs 64-bit multiply-adds at the rate of 32-bit ones.
-__device__ __forceinline__ void sine_cosine(double a, double& s, double& c) {
-  const double k = __builtin_rint(a * 0.63661977236758134308);
-  double r = __builtin_fma(-k, 1.57079632679489655800, a);
+__device__ __forceinline__ void sine_cosine(const Angle& t, double& s, double& c) {
+  const double k = __builtin_rint(t.a * 0.63661977236758134308);
+  double r = __builtin_fma(-k, 1.57079632679489655800, t.a) + t.rest;
   r = __builtin_fma(-k, 6.12323399573676603587e-17, r);
   const double z = r * r;
   double p = 1.0 / 1307674368000.0, q = 1.0 / 87178291200.0;
@@ -41,7 +47,7 @@ __device__ __forceinline__ void sine_cosine(double a, double& s, double& c) {
   c = (quarter + 1) & 2 ? -c : c;
 }
 
-__device__ __forceinline__ double angle_of(const Rotation& t, int64_t row, int64_t place, int j) {
+__device__ __forceinline__ Angle angle_of(const Rotation& t, int64_t row, int64_t place, int j) {
   double p = double(place);
   if (t.pos) {
     int x = 0;
@@ -51,7 +57,8 @@ __device__ __forceinline__ double angle_of(const Rotation& t, int64_t row, int64
     }
     p = double(t.pos[row * t.axes + x]);
   }
-  return p * double(t.inv[j]);
+  const double f = double(t.inv[j]), a = p * f;
+  return {a, __builtin_fma(p, f, -a)};
 }
 
 // A row is handled in units of two chunks of eight channels: u below half / 8 holds chunks u and

@@ -429,8 +429,8 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, k
  *   positions [n,n_axes] int32, n_axes 1 to 8 (time, height, width, ...); negative ones turn backwards.
  *   inv_freq  [rot/2] fp32          axes [rot/2] int32, the axis of each pair (clamped to
  *       0 .. n_axes - 1), or NULL: all of axis 0
- * Angles are formed and reduced in 64 bits (exact to 2^-50 while below 2^45); sines and cosines are rounded to fp32, the
- * rest is one fp32 multiply and one multiply-add a channel.
+ * Angles are formed and reduced in 64 bits, with what the product's rounding loses (exact to 2^-50 while below 2^45, at any
+ * position); sines and cosines are rounded to fp32, the rest is one fp32 multiply and one multiply-add a channel.
  */
 kda_status kda_rope(const void* x, kda_dtype in_dtype, int64_t x_stride, const int* positions, int n_axes,
                     const float* inv_freq, const int* axes, int rot, int interleaved, int inverse, void* y,
