@@ -34,17 +34,9 @@
 // way back: 1 % of the times above.)
 #pragma once
 
-#include <type_traits>
-
 #include "kda_cache.hpp"
 
 namespace kda {
-
-typedef const __attribute__((address_space(4))) int* const_ints;
-typedef const __attribute__((address_space(4))) float* const_floats;
-// A load by the scalar unit: the same address in every lane, memory that no kernel here writes.
-__device__ __forceinline__ int scalar_load(const int* p) { return *(const_ints)(uintptr_t)p; }
-__device__ __forceinline__ float scalar_load(const float* p) { return *(const_floats)(uintptr_t)p; }
 
 constexpr int kNarrowRows = 32;
 constexpr int kShrinkBits = 26;  // (the least scale, 2^-100, stays a normal number)
@@ -209,13 +201,6 @@ struct ChunkWork {
     neg = a.scale < 0.f;
   }
 
-  // The page of tokens `tok` .. + 15 of a sequence, -1 where there is none below `end`.
-  __device__ __forceinline__ int page_of(const int* table, int64_t tok, int64_t end) const {
-    int p = -1;
-    if (tok < end) p = scalar_load(table + (tok >> ps));
-    return p >= 0 && p < a.pages ? p : -1;
-  }
-
   // Four channels (c0 a multiple of 4) of row rr within a part of a tile of `rows`: as the wide form holds them, its 64
   // lanes one behind another; row by row in the narrow form.
   __device__ __forceinline__ static int part_at(int rows, int rr, int c0) {
@@ -270,6 +255,7 @@ struct ChunkWork {
         const int at = (wave * NPC + i) * 1024, g = (at / (P * D)) << (ps - 4);  // the page's first 16 tokens
         const int64_t ph = int64_t(__builtin_amdgcn_readlane(z.page, g)) * a.Hkv + x.kvh;
         to.w[i] = *reinterpret_cast<const u32x4*>(cache + ph * P * D + (at & (P * D - 1)) + lane * 16);
+        // (lane >> 6 is zero, which the compiler does not know: a vector load, as the pages' are, not a scalar one)
         to.scale[i] = scales[ph + (lane >> 6)];
       }
     };
