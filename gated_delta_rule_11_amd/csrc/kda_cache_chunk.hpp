@@ -16,10 +16,12 @@
 // [d][token], are that product's other operand as they lie.
 //
 // What bounds it (MI355X, 32 heads on 8 of 128, bf16): long chunks by the products and what stands between them, 1024 tokens
-// behind 64511 in 1112 us, 980 TFLOP/s, where the matrix pipe is busy in 43 % of the cycles and the rest goes to the
-// exponentials, the conversions of codes and the LDS (an 8192^3 library product reaches 1067); drafted tokens by the cache's
-// bytes, 64 x 5 tokens over up to 8192 in 103 us and 7 for the joins, 4.8 TB/s; whole prompts of 500 to 2048 tokens, 109 us
-// for 69 GFLOP, by the 5 us that each tile takes to start and to end (pages, queries, first codes, outputs).  A wavefront that
+// behind 64511 in 1110 to 1140 us, 957 to 980 TFLOP/s, where the matrix pipe is busy in 43 % of the cycles and the rest goes to
+// the exponentials, the conversions of codes and the LDS (an 8192^3 library product reaches 1070 to 1110 on such cards);
+// drafted tokens by the cache's bytes, 64 x 5 tokens over up to 8192 in 104 us and 7 for the joins, 4.7 TB/s; whole prompts of
+// 500 to 2048 tokens, 110 us for 69 GFLOP, by the order of the tiles (counted with the long chunk's 2.2 us a step, a long
+// sequence that starts late costs 20 us) and the 5 us that each takes to start and to end (pages, queries, first codes,
+// outputs; 13 us in all).  A wavefront that
 // forms the scores of the next step beside the products of this one needs more registers than two to a SIMD have (135 us
 // grew to 170), 64 rows to a wavefront likewise; orders asked of the scheduler changed nothing.
 //
@@ -769,6 +771,8 @@ struct ChunkPart {
   int first, kvh, r0, rows, pad[3];
 };
 
+// (Three workgroups to a compute unit for bf16 at d = 64: 83.1 us for a mixed batch, 84.3 where the registers were left to
+// themselves.)
 template <typename T, typename TO, int D>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? (D == 64 ? 3 : 2) : 1) void cache_chunk_kernel(const CacheChunkArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -792,7 +796,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? (D == 64 ? 3 : 2) : 1) void c
   ChunkPart* const parts = reinterpret_cast<ChunkPart*>(a.part + int64_t(a.groups) * 2 * chunk_part_floats(D));
   if (!shared) {
     // Sequence i's tiles sit at slots cu[i] G / 128 + i onwards, which leaves each at least as many as it has.
-    const int slots = int(gridDim.x / a.Hkv), slot = slots - 1 - int(blockIdx.x / a.Hkv);  // long rows first
+    const int slots = int(gridDim.x / a.Hkv), slot = slots - 1 - int(blockIdx.x / a.Hkv);
+    // (the last sequence first, of each sequence the longest tiles first: a long sequence that comes early ends late)
     z.kvh = int(blockIdx.x % a.Hkv);
     int lo = 0, up = a.N;
     auto start = [&](int64_t i) {

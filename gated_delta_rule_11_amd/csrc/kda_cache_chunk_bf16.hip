@@ -17,8 +17,13 @@ int64_t cache_chunk_slots(int n, int N, int Hq, int Hkv) { return int64_t(n) * (
 //   room 1000:  4 single tokens 12.5, 20.3;  256 of them 71, 78;  one prompt 33, 49
 //   room 2000:  one prompt 63, 74;  16 prompts 306, 330;  two chunks of 40 tokens 55, 42
 //   room 4000:  one prompt 150, 176;  26 single tokens among 6 chunks 110, 84
-// fp32, a third of the steps' rate and half the workgroups at once: one prompt of 2000 121, 143 (508 tiles); four chunks of
-// 101 to 700 tokens in a room of 2000, 24 heads on 4 of 64, 60, 48 (237 tiles).
+// fp32, a third of the steps' rate and half the workgroups at once, 24 heads on 4 of 64 in a room of 2048, at about 64, 236,
+// 404 and 804 tiles:
+//   whole prompts 19, 25;  48, 47;  65, 72;  96, 102;  single tokens 17, 24;  21, 26;  35, 34;  56, 51
+//   pieces of 64 to 512 tokens behind up to 2000: 26, 31;  69, 64;  103, 90;  159, 131
+// Neither is the faster at all lengths, which the host does not know; from 100 to 800 tiles the three together differ by a
+// tenth at most (with d = 128, 32 heads on 8 or a room of 1500 by less than a fifth, to either side).  The border, 12 tiles
+// to a step, is 384 here.
 int cache_chunk_groups(int n, int N, int Hq, int Hkv, int page, int max_pages, bool bf16) {
   const int64_t tiles = cache_chunk_slots(n, N, Hq, Hkv) * Hkv;
   const int64_t steps = (int64_t(max_pages) * page + 63) / 64;

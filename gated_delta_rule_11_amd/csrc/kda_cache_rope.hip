@@ -467,7 +467,7 @@ hipError_t launch(const CacheRopeArgs& a, hipStream_t st) {
 template <typename T, typename TO, int D>
 hipError_t launch_form(const CacheRopeArgs& a, hipStream_t st) {
   // Few tokens to a sequence, and so to a page: 8 rows are one pass (d = 128) of one wavefront.  64 sequences of 8 tokens
-  // take 9.4 us so and 11.9 by workgroups, of 16 tokens 20.2 and 14.5; 256 single tokens 12.7 and 30.6.
+  // take 9.4 us so and 11.9 by workgroups, of 16 tokens 20.2 and 14.5; 256 single tokens 13 and 31.
   // So do pages too many for one launch of the larger workgroups, which holds fewer than 2^32 threads.
   const int64_t pairs = (int64_t(a.c.n) / a.c.page + 2 * int64_t(a.c.N)) * a.c.Hkv, items = a.q.x ? rope_items(a.q) : 0;
   if (int64_t(a.c.n) <= 8 * int64_t(a.c.N) || (pairs + items + 1) * kThreads<D, 1> >= int64_t(1) << 32)

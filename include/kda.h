@@ -518,8 +518,8 @@ kda_status kda_kv_cache_append(const void* k, const void* v, kda_dtype in_dtype,
  *       context_len[i] plus its number among the new ones.
  *   inv_freq, axes, rot, interleaved: as in kda_rope.
  * Keys are turned in 64 bits and never rounded to in_dtype: the codes are those of the exactly turned
- * keys.  v is appended as it is.  Everything else as kda_kv_cache_append; queries are turned
- * also where a token is dropped.
+ * keys (one that the turn takes beyond fp32 counts as infinite).  v is appended as it is.
+ * Everything else as kda_kv_cache_append; queries are turned also where a token is dropped.
  */
 kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_stride, kda_dtype in_dtype,
                                     const void* q, int64_t q_stride, void* q_out, kda_dtype q_out_dtype,
@@ -539,6 +539,8 @@ kda_status kda_kv_cache_append_rope(const void* k, int64_t k_stride, const void*
  * pages, or in a page whose id is outside [0, n_pages), are left out.  What
  * lies in a page behind the last token is not used, whatever it holds.  With
  * n_pages == 0 the cache, the scales and block_table are not read and may be NULL.
+ * Sums of probabilities times values are fp32 before they are divided: values whose sum over the tokens leaves fp32
+ * (256 tokens of 2^120) give infinities.
  *   workspace  kda_attn_decode_step_workspace_bytes bytes, 16-byte aligned
  *          (NULL when that is 0)
  */
@@ -560,11 +562,14 @@ kda_status kda_attn_decode_step(const void* q, kda_dtype in_dtype, const void* k
  * At most 1024 query heads share a key head.  Roundings, missing pages and what lies behind the last token: as in
  * kda_attn_decode_step, whose results single tokens get (the sums in another order).  fp32 queries: every product is exact.
  * A NaN or infinity among the values reaches only the rows that see it.
- * Finite values give finite outputs, however large they are, up to 2^26 tokens.
+ * Finite values give finite outputs, however large they are, up to 2^26 tokens.  Of a scale only the exponent counts here:
+ * scales are powers of two, as the appends write them, and a cache with others is read wrongly.
  * The work, the keys of all rows, is divided on the device, whatever the lengths: no list of them is needed on the host.
- * Where the table's room is long for the number of rows it is divided evenly over the GPU.  Every sum has a fixed order: the same bits every time.
+ * Where the table's room is long for the number of rows it is divided evenly over the GPU, which prompts shorter than the
+ * room pay for: a table no wider than its longest sequence serves them best.
+ * Every sum has a fixed order: the same bits every time.
  *   workspace  kda_attn_chunk_fwd_workspace_bytes bytes, 16-byte aligned (NULL when that is 0); contents do not matter.
- *       The bytes for larger n or N are enough for smaller ones.
+ *       The bytes for larger n or N are enough for smaller ones.  A call whose work is not divided touches none of them.
  */
 size_t kda_attn_chunk_fwd_workspace_bytes(int n, int N, int Hq, int Hkv, int d, int page, int max_pages,
                                           kda_dtype in_dtype);
