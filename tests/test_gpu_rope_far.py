@@ -92,3 +92,24 @@ def test_codes_are_those_of_the_exactly_turned_keys(new):
     assert float(ks) == scale
     got = kc.view(torch.uint8).view(torch.float8_e4m3fn).float().cpu().double().numpy()[0, 0, :n, :32] * scale
     assert (got == want)[want != 0].all() and (want != 0).sum() > 16 * new
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [3, 16])
+def test_keys_that_turn_beyond_fp32_count_as_infinite(n, dtype):
+    """An eighth of a turn of two equal channels of 3e38: one becomes 4.2e38, the largest code and not in the scale.  The
+    other, 3e38 (cos t - sin t) with t = pi/4 + 2.2e-8 in fp32, is -9.3e30: 448 times the scale is at least that, 2^95."""
+    P, d, inv = 16, 64, torch.full((8,), math.pi / 4)
+    key = torch.zeros(n, 1, d)
+    key[1, 0, 0], key[1, 0, 8] = 3e38, 3e38
+    key[:, 0, 40] = 1.75
+    key = key.to(dtype).to(DEV)
+    kc, vc = (torch.zeros(1, 1, *s, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for s in ((P, d), (d, P)))
+    ks, vs = (torch.zeros(1, 1, device=DEV) for _ in range(2))
+    pos = i32([1] * n)
+    kda.kv_cache_append_rope(key, torch.zeros_like(key), i32([0, n]), i32([0]), i32([[0]]), kc, vc, ks, vs, inv.to(DEV), positions=pos)
+    torch.cuda.synchronize()
+    codes = kc.float()[0, 0]
+    assert float(ks) == 2.0 ** 95 and float(codes[1, 8]) == 448 and -448 <= float(codes[1, 0]) < -224
+    assert not codes[:n, 40].any()
